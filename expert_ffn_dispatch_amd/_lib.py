@@ -24,6 +24,10 @@ EXPORTS = (
     "moe_layer", "moe_set_stage_events", "moe_quantize_fp8", "moe_grouped_ffn_fp8", "moe_layer_fp8",
     "moe_layer_pipelined_workspace_bytes", "moe_layer_pipelined", "moe_layer_single_launch",
     "moe_layer_noalloc",
+    "moe_layer_norm", "moe_layer_norm_backward_workspace_bytes", "moe_layer_norm_backward",
+    "moe_linear_workspace_bytes", "moe_linear", "moe_linear_backward_workspace_bytes", "moe_linear_backward",
+    "moe_grouped_matmul", "moe_grouped_matmul_dgrad", "moe_grouped_matmul_wgrad_workspace_bytes",
+    "moe_grouped_matmul_wgrad",
 )
 # bytes of the library's own workspace array (moe_layer_noalloc)
 MOE_NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -38,6 +42,32 @@ class MoeDims(ctypes.Structure):
 class MoeFp8Ffn(ctypes.Structure):
     """struct moe_fp8_ffn: device pointers of E4M3 codes and per-channel scales."""
     _fields_ = [(n, ctypes.c_void_p) for n in ("gate", "up", "down", "gate_scale", "up_scale", "down_scale")]
+
+
+MOE_DTYPE_BF16 = 0
+MOE_DTYPE_F16 = 1
+MOE_DTYPE_F32 = 2
+# enum moe_act
+MOE_ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+MOE_NORM_RMS = 1
+
+
+class MoeNormDims(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("rows", "cols", "dtype", "param_dtype")]
+                + [("flags", ctypes.c_uint32), ("eps", ctypes.c_float)]
+                + [(n, ctypes.c_int64) for n in ("ld_x", "ld_y", "ld_dy", "ld_dx")])
+
+
+class MoeLinearDims(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("rows", "in_features", "out_features", "dtype", "act", "bias_dtype",
+                                               "dw_dtype")]
+                + [(n, ctypes.c_int64) for n in ("ld_x", "ld_w", "ld_residual", "ld_y", "ld_pre", "ld_dy", "ld_dx")])
+
+
+class MoeGroupedDims(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("rows", "n_experts", "in_features", "out_features", "dtype",
+                                               "dw_dtype")]
+                + [(n, ctypes.c_int64) for n in ("ld_x", "ld_y")])
 
 
 class MoeError(RuntimeError):
@@ -80,6 +110,19 @@ def load() -> ctypes.CDLL:
     lib.moe_layer_pipelined.argtypes = [DIMS, ctypes.c_uint32, ctypes.c_int32] + [P] * 13 + [ctypes.c_size_t, P]
     lib.moe_layer_single_launch.argtypes = [DIMS, ctypes.c_uint32, ctypes.c_int, ctypes.POINTER(ctypes.c_int)]
     lib.moe_layer_noalloc.argtypes = [DIMS, ctypes.c_uint32] + [P] * 12 + [P]
+    NORM, LIN, GRP = (ctypes.POINTER(c) for c in (MoeNormDims, MoeLinearDims, MoeGroupedDims))
+    SIZE, OUT = ctypes.c_size_t, ctypes.POINTER(ctypes.c_size_t)
+    lib.moe_layer_norm.argtypes = [NORM] + [P] * 7
+    lib.moe_layer_norm_backward_workspace_bytes.argtypes = [NORM, OUT]
+    lib.moe_layer_norm_backward.argtypes = [NORM] + [P] * 9 + [SIZE, P]
+    lib.moe_linear_workspace_bytes.argtypes = [LIN, OUT]
+    lib.moe_linear.argtypes = [LIN] + [P] * 7 + [SIZE, P]
+    lib.moe_linear_backward_workspace_bytes.argtypes = [LIN, OUT]
+    lib.moe_linear_backward.argtypes = [LIN] + [P] * 8 + [SIZE, P]
+    lib.moe_grouped_matmul.argtypes = [GRP] + [P] * 5
+    lib.moe_grouped_matmul_dgrad.argtypes = [GRP] + [P] * 5
+    lib.moe_grouped_matmul_wgrad_workspace_bytes.argtypes = [GRP, OUT]
+    lib.moe_grouped_matmul_wgrad.argtypes = [GRP] + [P] * 5 + [SIZE, P]
     for name in EXPORTS[2:]:
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib

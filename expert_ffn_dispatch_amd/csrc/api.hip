@@ -630,6 +630,200 @@ int scratch_address(const char* fn, void** ptr) {
   return MOE_OK;
 }
 
+// ------------- layer norm, linear layers and products by expert -------------
+
+constexpr int kMaxRows = 1 << 24;
+constexpr int kMaxWidth = 65536;
+constexpr int64_t kMaxLd = 1 << 20;
+constexpr int64_t kMaxTiles = 1 << 22;
+
+static_assert(moe::kTypeBf16 == MOE_DTYPE_BF16 && moe::kTypeF16 == MOE_DTYPE_F16 && moe::kTypeF32 == MOE_DTYPE_F32 &&
+                  moe::kActNone == MOE_ACT_NONE && moe::kActRelu == MOE_ACT_RELU && moe::kActGelu == MOE_ACT_GELU &&
+                  moe::kActGeluTanh == MOE_ACT_GELU_TANH && moe::kActSilu == MOE_ACT_SILU,
+              "the ABI's type and activation codes are the kernels'");
+
+size_t elem_bytes(int dtype) { return dtype == MOE_DTYPE_F32 ? 4 : 2; }
+bool al16(const void* p) { return aligned(p); }
+
+// A pointer that is there and has its element's alignment.
+#define REQ_ELEM(p, dtype)                                                                \
+  do {                                                                                    \
+    if ((p) == nullptr) return fail(MOE_ERR_INVALID, "%s: %s is NULL", fn, #p);          \
+    OPT_ELEM(p, dtype);                                                                   \
+  } while (0)
+#define OPT_ELEM(p, dtype)                                                                \
+  do {                                                                                    \
+    if ((reinterpret_cast<uintptr_t>(p) & (elem_bytes(dtype) - 1)) != 0)                  \
+      return fail(MOE_ERR_INVALID, "%s: %s is not aligned to its elements", fn, #p);     \
+  } while (0)
+// Resolves a row stride: 0 is packed; else width..kMaxLd.
+#define REQ_LD(ld, width)                                                                 \
+  do {                                                                                    \
+    if ((ld) == 0) (ld) = (width);                                                        \
+    if ((ld) < (width) || (ld) > kMaxLd)                                                  \
+      return fail(MOE_ERR_INVALID, "%s: %s=%lld outside [%lld, 2^20]", fn, #ld, (long long)(ld), (long long)(width)); \
+  } while (0)
+
+int check_rows(const char* fn, int rows) {
+  if (rows < 0 || rows > kMaxRows) return fail(MOE_ERR_INVALID, "%s: rows=%d outside [0, 2^24]", fn, rows);
+  return MOE_OK;
+}
+
+// `d` is a copy of the caller's dims, whose strides are resolved here.
+int check_norm(const char* fn, moe_norm_dims& d) {
+  if (int r = check_rows(fn, d.rows)) return r;
+  if (d.cols < 1 || d.cols > moe::kNormMaxCols)
+    return fail(MOE_ERR_INVALID, "%s: cols=%d outside [1, %d]", fn, d.cols, moe::kNormMaxCols);
+  if (d.dtype < MOE_DTYPE_BF16 || d.dtype > MOE_DTYPE_F32)
+    return fail(MOE_ERR_INVALID, "%s: unknown dtype %d", fn, d.dtype);
+  if (d.param_dtype != d.dtype && d.param_dtype != MOE_DTYPE_F32)
+    return fail(MOE_ERR_INVALID, "%s: param_dtype=%d must be dtype or MOE_DTYPE_F32", fn, d.param_dtype);
+  if (d.flags & ~uint32_t(MOE_NORM_RMS)) return fail(MOE_ERR_INVALID, "%s: unknown flags 0x%x", fn, d.flags);
+  if (!(d.eps >= 0.f)) return fail(MOE_ERR_INVALID, "%s: eps must be >= 0", fn);
+  REQ_LD(d.ld_x, d.cols);
+  REQ_LD(d.ld_y, d.cols);
+  REQ_LD(d.ld_dy, d.cols);
+  REQ_LD(d.ld_dx, d.cols);
+  return MOE_OK;
+}
+
+moe::NormArgs norm_args(const moe_norm_dims& d) {
+  moe::NormArgs a{};
+  a.rows = d.rows;
+  a.cols = d.cols;
+  a.type = d.dtype;
+  a.param_f32 = d.param_dtype == MOE_DTYPE_F32;
+  a.rms = (d.flags & MOE_NORM_RMS) != 0;
+  a.eps = d.eps;
+  a.ldx = d.ld_x;
+  return a;
+}
+
+int check_product(const char* fn, int rows, int n_in, int n_out, int dtype) {
+  if (int r = check_rows(fn, rows)) return r;
+  if (n_in < 1 || n_in > kMaxWidth)
+    return fail(MOE_ERR_INVALID, "%s: in_features=%d outside [1, %d]", fn, n_in, kMaxWidth);
+  if (n_out < 1 || n_out > kMaxWidth)
+    return fail(MOE_ERR_INVALID, "%s: out_features=%d outside [1, %d]", fn, n_out, kMaxWidth);
+  if (dtype != MOE_DTYPE_BF16 && dtype != MOE_DTYPE_F16)
+    return fail(MOE_ERR_INVALID, "%s: dtype=%d must be bf16 or fp16", fn, dtype);
+  return MOE_OK;
+}
+
+int check_tiles(const char* fn, int64_t groups, int64_t m, int64_t n) {
+  const int64_t t = groups * ((m + 127) / 128) * ((n + 127) / 128);
+  if (t > kMaxTiles)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: %lld output tiles of 128 x 128, above the supported 2^22", fn, (long long)t);
+  return MOE_OK;
+}
+
+int check_linear(const char* fn, moe_linear_dims& d) {
+  if (int r = check_product(fn, d.rows, d.in_features, d.out_features, d.dtype)) return r;
+  if (d.act < MOE_ACT_NONE || d.act > MOE_ACT_SILU) return fail(MOE_ERR_INVALID, "%s: unknown act %d", fn, d.act);
+  if (d.bias_dtype != d.dtype && d.bias_dtype != MOE_DTYPE_F32)
+    return fail(MOE_ERR_INVALID, "%s: bias_dtype=%d must be dtype or MOE_DTYPE_F32", fn, d.bias_dtype);
+  if (d.dw_dtype != d.dtype && d.dw_dtype != MOE_DTYPE_F32)
+    return fail(MOE_ERR_INVALID, "%s: dw_dtype=%d must be dtype or MOE_DTYPE_F32", fn, d.dw_dtype);
+  REQ_LD(d.ld_x, d.in_features);
+  REQ_LD(d.ld_w, d.in_features);
+  REQ_LD(d.ld_dx, d.in_features);
+  REQ_LD(d.ld_residual, d.out_features);
+  REQ_LD(d.ld_y, d.out_features);
+  REQ_LD(d.ld_pre, d.out_features);
+  REQ_LD(d.ld_dy, d.out_features);
+  if (int r = check_tiles(fn, 1, d.rows, d.out_features)) return r;
+  if (int r = check_tiles(fn, 1, d.rows, d.in_features)) return r;
+  return MOE_OK;
+}
+
+int check_grouped(const char* fn, moe_grouped_dims& d) {
+  if (int r = check_product(fn, d.rows, d.in_features, d.out_features, d.dtype)) return r;
+  if (d.n_experts < 1) return fail(MOE_ERR_INVALID, "%s: n_experts=%d must be >= 1", fn, d.n_experts);
+  if (d.n_experts > kMaxE)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: n_experts=%d above the supported %d", fn, d.n_experts, kMaxE);
+  if (d.dw_dtype != d.dtype && d.dw_dtype != MOE_DTYPE_F32)
+    return fail(MOE_ERR_INVALID, "%s: dw_dtype=%d must be dtype or MOE_DTYPE_F32", fn, d.dw_dtype);
+  REQ_LD(d.ld_x, d.in_features);
+  REQ_LD(d.ld_y, d.out_features);
+  // a group's last row tile may be short: one more tile per group
+  if (int r = check_tiles(fn, 1, d.rows + 128LL * d.n_experts, d.out_features)) return r;
+  if (int r = check_tiles(fn, 1, d.rows + 128LL * d.n_experts, d.in_features)) return r;
+  return check_tiles(fn, d.n_experts, d.out_features, d.in_features);
+}
+
+// Operands in 16-byte pieces: each as (pointer, row stride, row width).
+bool pieces16(const void* p, int64_t ld, int64_t width) { return al16(p) && ld % 8 == 0 && width % 8 == 0; }
+
+// dx = dy w over `rows` rows (grouped where offsets is set)
+moe::MatmulArgs row_grad_args(const void* dy, int64_t ld_dy, const void* w, int64_t ld_w, void* dx, int64_t ld_dx,
+                              int rows, int n_in, int n_out, int dtype) {
+  moe::MatmulArgs a{};
+  a.a = static_cast<const uint16_t*>(dy);
+  a.lda = ld_dy;
+  a.b = static_cast<const uint16_t*>(w);
+  a.ldb = ld_w;
+  a.out = dx;
+  a.ldo = ld_dx;
+  a.E = 1;
+  a.rows = a.m = rows;
+  a.n = n_in;
+  a.k = n_out;
+  a.f16 = dtype == MOE_DTYPE_F16;
+  a.aligned = pieces16(dy, ld_dy, n_out) && pieces16(w, ld_w, n_in);
+  a.vec = al16(dx) && ld_dx % 8 == 0;
+  return a;
+}
+
+moe::MatmulArgs weight_grad_args(const void* dy, int64_t ld_dy, const void* x, int64_t ld_x, void* dw, int dw_dtype,
+                                 int E, int rows, int n_in, int n_out, int dtype) {
+  moe::MatmulArgs a{};
+  a.a = static_cast<const uint16_t*>(dy);
+  a.lda = ld_dy;
+  a.b = static_cast<const uint16_t*>(x);
+  a.ldb = ld_x;
+  a.out = dw;
+  a.ldo = n_in;
+  a.out_group = (int64_t)n_out * n_in;
+  a.E = E;
+  a.rows = rows;
+  a.m = n_out;
+  a.n = n_in;
+  a.out_f32 = dw_dtype == MOE_DTYPE_F32;
+  a.f16 = dtype == MOE_DTYPE_F16;
+  a.aligned = pieces16(dy, ld_dy, n_out) && pieces16(x, ld_x, n_in);
+  a.vec = al16(dw) && n_in % 8 == 0;
+  return a;
+}
+
+struct LinearBackwardWs {
+  uint16_t* g;               // [rows][out], with an activation
+  float* sums;               // bias gradient's partial sums
+  void* parts;               // contraction slices of either product, one after the other
+};
+LinearBackwardWs carve_linear_backward(Carver& c, const moe_linear_dims& d) {
+  const int64_t R = d.rows, I = d.in_features, O = d.out_features;
+  LinearBackwardWs w;
+  w.g = d.act != MOE_ACT_NONE ? c.take<uint16_t>((size_t)(R * O)) : nullptr;
+  w.sums = c.take<float>(moe::act_grad_workspace_bytes(R, O) / sizeof(float));
+  const size_t a = moe::matmul_workspace_bytes(moe::kMmRowGrad, 1, false, R, R, I, O);
+  const size_t b = moe::matmul_workspace_bytes(moe::kMmWeightGrad, 1, false, R, O, I, R);
+  w.parts = c.take<char>(a > b ? a : b);
+  return w;
+}
+
+size_t linear_ws_bytes(const moe_linear_dims& d) {
+  return align_up(moe::matmul_workspace_bytes(moe::kMmForward, 1, false, d.rows, d.rows, d.out_features, d.in_features));
+}
+size_t grouped_wgrad_ws_bytes(const moe_grouped_dims& d) {
+  return align_up(moe::matmul_workspace_bytes(moe::kMmWeightGrad, d.n_experts, true, d.rows, d.out_features,
+                                              d.in_features, d.rows));
+}
+
+// A copy of the caller's dims to resolve strides in.
+#define COPY_DIMS(type, d)                                                                \
+  if (dims == nullptr) return fail(MOE_ERR_INVALID, "%s: dims is NULL", fn);             \
+  type d = *dims
+
 }  // namespace
 
 extern "C" {
@@ -918,6 +1112,285 @@ int moe_layer_pipelined(const moe_dims* dims, uint32_t flags, int32_t n_micro, c
   return run_layer_pipelined(fn, dims, flags, n_micro, x, w_router, router_bias, bf16_weights(w_gate, w_up, w_down),
                              bf16_weights(ws_gate, ws_up, ws_down), topk_ids, topk_weights, out, ws, ws_bytes,
                              stream);
+}
+
+int moe_layer_norm(const moe_norm_dims* dims, const void* x, const void* gamma, const void* beta, void* y,
+                   float* mean, float* rstd, moe_stream stream) {
+  const char* fn = "moe_layer_norm";
+  COPY_DIMS(moe_norm_dims, d);
+  if (int r = check_norm(fn, d)) return r;
+  if (d.rows == 0) return ok();
+  REQ_ELEM(x, d.dtype);
+  OPT_ELEM(gamma, d.param_dtype);
+  OPT_ELEM(beta, d.param_dtype);
+  REQ_ELEM(y, d.dtype);
+  OPT_ELEM(mean, MOE_DTYPE_F32);
+  OPT_ELEM(rstd, MOE_DTYPE_F32);
+  if (y == x && d.ld_y != d.ld_x) return fail(MOE_ERR_INVALID, "%s: y is x with another row stride", fn);
+  moe::NormArgs a = norm_args(d);
+  a.x = x;
+  a.gamma = gamma;
+  a.beta = beta;
+  a.out = y;
+  a.ldo = d.ld_y;
+  a.mean = mean;
+  a.rstd = rstd;
+  if (hipError_t e = moe::launch_norm_forward(a, static_cast<hipStream_t>(stream))) return device_error(fn, e);
+  return ok();
+}
+
+int moe_layer_norm_backward_workspace_bytes(const moe_norm_dims* dims, size_t* bytes) {
+  const char* fn = "moe_layer_norm_backward_workspace_bytes";
+  COPY_DIMS(moe_norm_dims, d);
+  if (int r = check_norm(fn, d)) return r;
+  if (bytes == nullptr) return fail(MOE_ERR_INVALID, "%s: bytes is NULL", fn);
+  *bytes = align_up(moe::norm_backward_workspace_bytes(d.rows, d.cols));
+  return ok();
+}
+
+int moe_layer_norm_backward(const moe_norm_dims* dims, const void* dy, const void* x, const void* gamma,
+                            const float* mean, const float* rstd, void* dx, void* dgamma, void* dbeta, void* ws,
+                            size_t ws_bytes, moe_stream stream) {
+  const char* fn = "moe_layer_norm_backward";
+  COPY_DIMS(moe_norm_dims, d);
+  if (int r = check_norm(fn, d)) return r;
+  const bool rms = (d.flags & MOE_NORM_RMS) != 0;
+  if (d.rows > 0) {
+    REQ_ELEM(dy, d.dtype);
+    REQ_ELEM(x, d.dtype);
+    if (!rms) REQ_ELEM(mean, MOE_DTYPE_F32);
+    REQ_ELEM(rstd, MOE_DTYPE_F32);
+  }
+  OPT_ELEM(gamma, d.param_dtype);
+  OPT_ELEM(dx, d.dtype);
+  OPT_ELEM(dgamma, d.param_dtype);
+  OPT_ELEM(dbeta, d.param_dtype);
+  if (dx != nullptr && ((dx == x && d.ld_dx != d.ld_x) || (dx == dy && d.ld_dx != d.ld_dy)))
+    return fail(MOE_ERR_INVALID, "%s: dx is x or dy with another row stride", fn);
+  if (dgamma != nullptr || dbeta != nullptr) {
+    if (int r = check_ws(fn, ws, ws_bytes, align_up(moe::norm_backward_workspace_bytes(d.rows, d.cols)))) return r;
+  } else if (dx == nullptr) {
+    return ok();
+  }
+  moe::NormArgs a = norm_args(d);
+  a.x = x;
+  a.dy = dy;
+  a.ldd = d.ld_dy;
+  a.gamma = gamma;
+  a.mean = const_cast<float*>(mean);
+  a.rstd = const_cast<float*>(rstd);
+  a.out = dx;
+  a.ldo = d.ld_dx;
+  a.dgamma = dgamma;
+  a.dbeta = dbeta;
+  if (hipError_t e = moe::launch_norm_backward(a, ws, static_cast<hipStream_t>(stream))) return device_error(fn, e);
+  return ok();
+}
+
+int moe_linear_workspace_bytes(const moe_linear_dims* dims, size_t* bytes) {
+  const char* fn = "moe_linear_workspace_bytes";
+  COPY_DIMS(moe_linear_dims, d);
+  if (int r = check_linear(fn, d)) return r;
+  if (bytes == nullptr) return fail(MOE_ERR_INVALID, "%s: bytes is NULL", fn);
+  *bytes = linear_ws_bytes(d);
+  return ok();
+}
+
+int moe_linear(const moe_linear_dims* dims, const void* x, const void* w, const void* bias, const void* residual,
+               void* y, void* pre, void* ws, size_t ws_bytes, moe_stream stream) {
+  const char* fn = "moe_linear";
+  COPY_DIMS(moe_linear_dims, d);
+  if (int r = check_linear(fn, d)) return r;
+  if (d.rows == 0) return ok();
+  REQ_ELEM(x, d.dtype);
+  REQ_ELEM(w, d.dtype);
+  OPT_ELEM(bias, d.bias_dtype);
+  OPT_ELEM(residual, d.dtype);
+  REQ_ELEM(y, d.dtype);
+  OPT_ELEM(pre, d.dtype);
+  if (y == x || y == w || (pre != nullptr && (pre == x || pre == w || pre == y || pre == residual)))
+    return fail(MOE_ERR_INVALID, "%s: an output is an input (only residual may be y)", fn);
+  if (residual == y && d.ld_residual != d.ld_y)
+    return fail(MOE_ERR_INVALID, "%s: residual is y with another row stride", fn);
+  if (int r = check_ws(fn, ws, ws_bytes, linear_ws_bytes(d))) return r;
+  moe::MatmulArgs a{};
+  a.a = static_cast<const uint16_t*>(x);
+  a.lda = d.ld_x;
+  a.b = static_cast<const uint16_t*>(w);
+  a.ldb = d.ld_w;
+  a.out = y;
+  a.ldo = d.ld_y;
+  a.E = 1;
+  a.rows = a.m = d.rows;
+  a.n = d.out_features;
+  a.k = d.in_features;
+  a.f16 = d.dtype == MOE_DTYPE_F16;
+  a.aligned = pieces16(x, d.ld_x, d.in_features) && pieces16(w, d.ld_w, d.in_features);
+  a.vec = al16(y) && d.ld_y % 8 == 0 && (residual == nullptr || (al16(residual) && d.ld_residual % 8 == 0)) &&
+          (pre == nullptr || (al16(pre) && d.ld_pre % 8 == 0));
+  a.bias = bias;
+  a.bias_f32 = d.bias_dtype == MOE_DTYPE_F32;
+  a.act = d.act;
+  a.residual = static_cast<const uint16_t*>(residual);
+  a.ldr = d.ld_residual;
+  a.pre = static_cast<uint16_t*>(pre);
+  a.ldp = d.ld_pre;
+  if (hipError_t e = moe::launch_matmul(moe::kMmForward, a, ws, static_cast<hipStream_t>(stream)))
+    return device_error(fn, e);
+  return ok();
+}
+
+int moe_linear_backward_workspace_bytes(const moe_linear_dims* dims, size_t* bytes) {
+  const char* fn = "moe_linear_backward_workspace_bytes";
+  COPY_DIMS(moe_linear_dims, d);
+  if (int r = check_linear(fn, d)) return r;
+  if (bytes == nullptr) return fail(MOE_ERR_INVALID, "%s: bytes is NULL", fn);
+  Carver c(nullptr);
+  carve_linear_backward(c, d);
+  *bytes = c.off;
+  return ok();
+}
+
+int moe_linear_backward(const moe_linear_dims* dims, const void* dy, const void* x, const void* w, const void* pre,
+                        void* dx, void* dw, void* dbias, void* ws, size_t ws_bytes, moe_stream stream) {
+  const char* fn = "moe_linear_backward";
+  COPY_DIMS(moe_linear_dims, d);
+  if (int r = check_linear(fn, d)) return r;
+  const bool act = d.act != MOE_ACT_NONE;
+  if (!act && pre != nullptr) return fail(MOE_ERR_INVALID, "%s: pre must be NULL with MOE_ACT_NONE", fn);
+  if (d.rows > 0) {
+    REQ_ELEM(dy, d.dtype);
+    if (act) REQ_ELEM(pre, d.dtype);
+    if (dw != nullptr) REQ_ELEM(x, d.dtype);
+    if (dx != nullptr) REQ_ELEM(w, d.dtype);
+  }
+  OPT_ELEM(dx, d.dtype);
+  OPT_ELEM(dw, d.dw_dtype);
+  OPT_ELEM(dbias, d.bias_dtype);
+  if ((dx != nullptr && (dx == dy || dx == w || dx == x || dx == pre)) ||
+      (dw != nullptr && (dw == w || dw == x || dw == dy || dw == pre)))
+    return fail(MOE_ERR_INVALID, "%s: an output is an input", fn);
+  if (dx == nullptr && dw == nullptr && dbias == nullptr) return ok();
+  Carver sz(nullptr);
+  carve_linear_backward(sz, d);
+  if (int r = check_ws(fn, ws, ws_bytes, sz.off)) return r;
+  Carver c(ws);
+  LinearBackwardWs b = carve_linear_backward(c, d);
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const bool products = dx != nullptr || dw != nullptr;
+  const void* g = dy;
+  int64_t ld_g = d.ld_dy;
+  if (dbias != nullptr || (act && products && d.rows > 0)) {
+    moe::ActGradArgs a{};
+    a.dy = static_cast<const uint16_t*>(dy);
+    a.ldd = d.ld_dy;
+    a.pre = static_cast<const uint16_t*>(pre);
+    a.ldp = d.ld_pre;
+    a.g = act && products ? b.g : nullptr;
+    a.dbias = dbias;
+    a.dbias_f32 = d.bias_dtype == MOE_DTYPE_F32;
+    a.rows = d.rows;
+    a.n = d.out_features;
+    a.act = d.act;
+    a.f16 = d.dtype == MOE_DTYPE_F16;
+    if (hipError_t e = moe::launch_act_grad(a, b.sums, st)) return device_error(fn, e);
+  }
+  if (act) {
+    g = b.g;
+    ld_g = d.out_features;
+  }
+  if (dx != nullptr) {
+    const moe::MatmulArgs a = row_grad_args(g, ld_g, w, d.ld_w, dx, d.ld_dx, d.rows, d.in_features, d.out_features, d.dtype);
+    if (hipError_t e = moe::launch_matmul(moe::kMmRowGrad, a, b.parts, st)) return device_error(fn, e);
+  }
+  if (dw != nullptr) {
+    const moe::MatmulArgs a =
+        weight_grad_args(g, ld_g, x, d.ld_x, dw, d.dw_dtype, 1, d.rows, d.in_features, d.out_features, d.dtype);
+    if (hipError_t e = moe::launch_matmul(moe::kMmWeightGrad, a, b.parts, st)) return device_error(fn, e);
+  }
+  return ok();
+}
+
+int moe_grouped_matmul(const moe_grouped_dims* dims, const void* x, const int32_t* expert_offsets, const void* w,
+                       void* y, moe_stream stream) {
+  const char* fn = "moe_grouped_matmul";
+  COPY_DIMS(moe_grouped_dims, d);
+  if (int r = check_grouped(fn, d)) return r;
+  if (d.rows == 0) return ok();
+  REQ_ELEM(x, d.dtype);
+  REQ_ELEM(expert_offsets, MOE_DTYPE_F32);
+  REQ_ELEM(w, d.dtype);
+  REQ_ELEM(y, d.dtype);
+  if (y == x || y == w) return fail(MOE_ERR_INVALID, "%s: y is an input", fn);
+  moe::MatmulArgs a{};
+  a.a = static_cast<const uint16_t*>(x);
+  a.lda = d.ld_x;
+  a.b = static_cast<const uint16_t*>(w);
+  a.ldb = d.in_features;
+  a.b_group = (int64_t)d.out_features * d.in_features;
+  a.out = y;
+  a.ldo = d.ld_y;
+  a.offsets = expert_offsets;
+  a.E = d.n_experts;
+  a.rows = a.m = d.rows;
+  a.n = d.out_features;
+  a.k = d.in_features;
+  a.f16 = d.dtype == MOE_DTYPE_F16;
+  a.aligned = pieces16(x, d.ld_x, d.in_features) && al16(w);
+  a.vec = al16(y) && d.ld_y % 8 == 0;
+  if (hipError_t e = moe::launch_matmul(moe::kMmForward, a, nullptr, static_cast<hipStream_t>(stream)))
+    return device_error(fn, e);
+  return ok();
+}
+
+int moe_grouped_matmul_dgrad(const moe_grouped_dims* dims, const void* dy, const int32_t* expert_offsets,
+                             const void* w, void* dx, moe_stream stream) {
+  const char* fn = "moe_grouped_matmul_dgrad";
+  COPY_DIMS(moe_grouped_dims, d);
+  if (int r = check_grouped(fn, d)) return r;
+  if (d.rows == 0) return ok();
+  REQ_ELEM(dy, d.dtype);
+  REQ_ELEM(expert_offsets, MOE_DTYPE_F32);
+  REQ_ELEM(w, d.dtype);
+  REQ_ELEM(dx, d.dtype);
+  if (dx == dy || dx == w) return fail(MOE_ERR_INVALID, "%s: dx is an input", fn);
+  moe::MatmulArgs a = row_grad_args(dy, d.ld_y, w, d.in_features, dx, d.ld_x, d.rows, d.in_features, d.out_features, d.dtype);
+  a.b_group = (int64_t)d.out_features * d.in_features;
+  a.offsets = expert_offsets;
+  a.E = d.n_experts;
+  if (hipError_t e = moe::launch_matmul(moe::kMmRowGrad, a, nullptr, static_cast<hipStream_t>(stream)))
+    return device_error(fn, e);
+  return ok();
+}
+
+int moe_grouped_matmul_wgrad_workspace_bytes(const moe_grouped_dims* dims, size_t* bytes) {
+  const char* fn = "moe_grouped_matmul_wgrad_workspace_bytes";
+  COPY_DIMS(moe_grouped_dims, d);
+  if (int r = check_grouped(fn, d)) return r;
+  if (bytes == nullptr) return fail(MOE_ERR_INVALID, "%s: bytes is NULL", fn);
+  *bytes = grouped_wgrad_ws_bytes(d);
+  return ok();
+}
+
+int moe_grouped_matmul_wgrad(const moe_grouped_dims* dims, const void* dy, const void* x,
+                             const int32_t* expert_offsets, void* dw, void* ws, size_t ws_bytes, moe_stream stream) {
+  const char* fn = "moe_grouped_matmul_wgrad";
+  COPY_DIMS(moe_grouped_dims, d);
+  if (int r = check_grouped(fn, d)) return r;
+  if (d.rows > 0) {
+    REQ_ELEM(dy, d.dtype);
+    REQ_ELEM(x, d.dtype);
+  }
+  REQ_ELEM(expert_offsets, MOE_DTYPE_F32);
+  REQ_ELEM(dw, d.dw_dtype);
+  if (dw == dy || dw == x) return fail(MOE_ERR_INVALID, "%s: dw is an input", fn);
+  if (int r = check_ws(fn, ws, ws_bytes, grouped_wgrad_ws_bytes(d))) return r;
+  moe::MatmulArgs a = weight_grad_args(dy, d.ld_y, x, d.ld_x, dw, d.dw_dtype, d.n_experts, d.rows, d.in_features,
+                                       d.out_features, d.dtype);
+  a.offsets = expert_offsets;
+  if (hipError_t e = moe::launch_matmul(moe::kMmWeightGrad, a, ws, static_cast<hipStream_t>(stream)))
+    return device_error(fn, e);
+  return ok();
 }
 
 }  // extern "C"

@@ -152,4 +152,81 @@ struct CombineArgs {
 };
 hipError_t launch_combine(const CombineArgs& a, hipStream_t st);
 
+// ---- matrix products of the linear layer and of the products by expert ----
+enum : int { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4 };
+// One product (matmul.h states the three forms).  Strides in elements.
+struct MatmulArgs {
+  const uint16_t* a;         // rows' operand: x | dy | dy
+  const uint16_t* b;         // columns' operand: W | W | x
+  void* out;
+  int64_t lda, ldb, ldo;
+  int64_t b_group;           // forward, row grad: elements from one group's W to the next
+  int64_t out_group;         // elements from one output (weight grad: group and slice; else slice) to the next
+  const int32_t* offsets;    // [E+1] device, or null: one group of all rows
+  int E;
+  int rows;                  // rows of the grouped operands
+  int m, n, k;               // output rows (of one group), output columns, contraction (weight grad: unused)
+  int splits;                // contraction slices (1: none); > 1: out holds fp32 partial sums
+  int out_f32;
+  int vec;                   // out, residual and pre take 16-byte accesses
+  // epilogue (null / kActNone: none): out = act(sum + bias) + residual, pre = sum + bias
+  const void* bias;
+  int bias_f32;
+  int act;
+  const uint16_t* residual;
+  int64_t ldr;
+  uint16_t* pre;
+  int64_t ldp;
+  int aligned;               // a and b take 16-byte loads
+  int f16;                   // operands are fp16 (else bf16)
+};
+enum MatmulForm { kMmForward = 0, kMmRowGrad = 1, kMmWeightGrad = 2 };
+// Contraction slices of a call (1: none) and the bytes of their partial sums.
+int matmul_splits(MatmulForm f, int E, bool ragged, int64_t rows, int64_t m, int64_t n, int64_t k);
+size_t matmul_workspace_bytes(MatmulForm f, int E, bool ragged, int64_t rows, int64_t m, int64_t n, int64_t k);
+// a.splits, out_group and the fp32 partials in ws are set up by the launcher.
+hipError_t launch_matmul(MatmulForm f, MatmulArgs a, void* ws, hipStream_t st);
+// The instances of one form (matmul_*.hip).
+hipError_t launch_matmul_forward(const MatmulArgs& a, hipStream_t st);
+hipError_t launch_matmul_row_grad(const MatmulArgs& a, hipStream_t st);
+hipError_t launch_matmul_weight_grad(const MatmulArgs& a, hipStream_t st);
+
+// g = dy * act'(pre) in the operands' type and, if dbias is set, its column
+// sums from the unrounded fp32 values.  g null: sums only.
+struct ActGradArgs {
+  const uint16_t* dy;
+  const uint16_t* pre;       // null with kActNone
+  uint16_t* g;               // [rows][n] packed, or null
+  void* dbias;               // [n] or null
+  int dbias_f32;
+  int64_t ldd, ldp;
+  int rows, n, act, f16;
+};
+size_t act_grad_workspace_bytes(int64_t rows, int64_t n);
+hipError_t launch_act_grad(const ActGradArgs& a, void* ws, hipStream_t st);
+
+// ---- layer norm ----
+enum : int { kTypeBf16 = 0, kTypeF16 = 1, kTypeF32 = 2 };
+constexpr int kNormMaxCols = 16384;
+struct NormArgs {
+  const void* x;
+  const void* dy;            // backward
+  const void* gamma;         // [cols] or null (ones)
+  const void* beta;          // [cols] or null (zeros)
+  void* out;                 // y | dx (backward: may be null)
+  float* mean;               // [rows]; forward: out or null; backward: in (null with rms)
+  float* rstd;               // [rows]; forward: out or null; backward: in
+  void* dgamma;              // [cols] or null
+  void* dbeta;               // [cols] or null
+  int64_t ldx, ldd, ldo;
+  int rows, cols;
+  int type;                  // of x, dy, y, dx
+  int param_f32;             // gamma, beta, dgamma, dbeta are fp32 (else of `type`)
+  int rms;
+  float eps;
+};
+hipError_t launch_norm_forward(const NormArgs& a, hipStream_t st);
+size_t norm_backward_workspace_bytes(int64_t rows, int64_t cols);
+hipError_t launch_norm_backward(const NormArgs& a, void* ws, hipStream_t st);
+
 }  // namespace moe

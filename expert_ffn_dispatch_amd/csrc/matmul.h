@@ -1,0 +1,639 @@
+// Matrix products on bf16 / fp16 MFMA (gfx950, fp32 accumulate) behind the
+// linear layer and the products grouped by expert, in the three forms a layer
+// and its gradients need.  W is [out][in], the contraction index is k:
+//   forward      y[r][c]     = sum_k x[r][k] W_e[c][k]     (e: r's group)
+//   row grad     dx[r][c]    = sum_k dy[r][k] W_e[k][c]
+//   weight grad  dW_e[r][c]  = sum_k dy[k][r] x[k][c],  k over e's rows
+// An operand is stored with k contiguous ("KC": x, dy and W of the first
+// form) or with k as its row index ("KS": W of the second, both of the third).
+#pragma once
+#include <type_traits>
+
+#include "common.h"
+#include "kernels.h"
+
+namespace moe {
+
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+
+constexpr int kMmK = 64;                          // contraction per stage
+constexpr uint32_t kMmBytes = 0x7fffff00u;        // buffer size of a tile's resource
+constexpr uint32_t kMmOut = 0x80000000u;          // an offset past it: the load returns zeros
+
+// ------------------------------------------------------------ small helpers
+
+template <bool F16>
+__device__ __forceinline__ f32x16_t mm_mfma(u32x4_t a, u32x4_t b, f32x16_t c) {
+  if constexpr (F16)
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c,
+                                                  0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b),
+                                                   c, 0, 0, 0);
+}
+
+template <bool F16>
+__device__ __forceinline__ float mm_load1(uint16_t v) {
+  if constexpr (F16) return static_cast<float>(__builtin_bit_cast(_Float16, v));
+  else return bf16_to_f32(v);
+}
+template <bool F16>
+__device__ __forceinline__ uint16_t mm_store1(float v) {
+  if constexpr (F16) return __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
+  else return f32_to_bf16(v);
+}
+template <bool F16>
+__device__ __forceinline__ uint32_t mm_pack2(float lo, float hi) {
+  if constexpr (F16) return (uint32_t)mm_store1<true>(lo) | ((uint32_t)mm_store1<true>(hi) << 16);
+  else return pack_bf16x2(lo, hi);
+}
+template <bool F16>
+__device__ __forceinline__ void mm_unpack8(u32x4_t v, float (&f)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = mm_load1<F16>((uint16_t)(v[i] & 0xffffu));
+    f[2 * i + 1] = mm_load1<F16>((uint16_t)(v[i] >> 16));
+  }
+}
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t mm_rsrc(const void* base) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)kMmBytes, 0x00020000);
+}
+__device__ __forceinline__ void mm_dma16(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff, uint16_t* lds) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, lds, 16, voff, soff, 0, 0);
+}
+// 4 x 16 transposing read of 16-bit values: within each 16 lanes, lane l
+// names the 8 bytes (row l >> 2, columns 4 (l & 3) ..+3) of a 4 x 16 block and
+// receives the block's column l, rows 0..3 (checked on the device).
+__device__ __forceinline__ s16x4_t mm_read_tr(const uint16_t* lds) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+      (__attribute__((address_space(3))) s16x4_t*)(const_cast<uint16_t*>(lds)));
+}
+__device__ __forceinline__ void mm_lds_barrier() {
+  __builtin_amdgcn_s_waitcnt(0xC07F);             // lgkmcnt(0)
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// Activation of the linear layer, in fp32.  One reciprocal instruction (1 ulp)
+// in place of a division: the result is rounded to 16 bits next.
+__device__ __forceinline__ float mm_act(float z, int act) {
+  switch (act) {
+    case kActRelu: return z > 0.f ? z : (z != z ? z : 0.f);
+    case kActGelu: return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+    case kActGeluTanh: {
+      // 0.5 z (1 + tanh u) = z / (1 + e^-2u)
+      const float u = 0.79788456080286536f * (z + 0.044715f * z * z * z);
+      return z * __builtin_amdgcn_rcpf(1.f + __expf(-2.f * u));
+    }
+    case kActSilu: return z * __builtin_amdgcn_rcpf(1.f + __expf(-z));
+    default: return z;
+  }
+}
+
+// ------------------------------------------------- operand staging in LDS
+
+// 16-byte chunk c of row r of a KC stage (64 k = 8 chunks a row) sits at
+// c ^ mm_swz(r): the 32 rows that a fragment read touches at one chunk fall
+// on distinct bank groups.
+__device__ __forceinline__ int mm_swz(int row) { return ((row >> 1) ^ ((row & 1) << 2)) & 7; }
+// KS stage: rows are k, R columns each; chunk c of row r sits at c ^ (4 (r & 3)),
+// so that the four rows x 64 bytes a transposing read of 32 lanes covers are
+// in distinct quarters of the 64 banks.
+__device__ __forceinline__ int mm_kswz(int krow) { return (krow & 3) << 2; }
+
+// How one operand's 64-wide stages reach LDS.  KC: stage [R rows][64 k]; KS:
+// stage [64 k][R columns].  Either way a stage is R * 128 bytes and each of
+// the NI loads of a wave fills 1 KB of it, lane l the bytes 16 l ..+15.
+// ALIGNED: 16-byte loads straight into LDS (rows of 16-byte pitch and
+// alignment, widths in multiples of 8).  Otherwise each element is loaded by
+// itself through registers: any strides and sizes.
+// Rows, columns and k past the ends take an offset past the buffer: zeros.
+template <bool KC, int R, int NW, bool ALIGNED>
+struct MmOperand {
+  static constexpr int NI = R / (8 * NW);
+  static constexpr int C = KC ? 8 : R / 8;        // chunks per LDS row
+  uint64_t base;                                  // byte address of the tile's first element
+  uint32_t pitch;                                 // row pitch in bytes
+  uint32_t off[NI];                               // per lane: byte offset within a stage
+  int kk[NI];                                     // per lane: first k of the piece within a stage
+  int wave;
+  int lim;                                        // !ALIGNED: KC unused; KS columns left from the lane's piece
+
+  // KC: p = element (first row of the tile, first k), ext = live rows.
+  // KS: p = element (first k, first column), ext = columns left in the matrix.
+  __device__ __forceinline__ void init(const uint16_t* p, int64_t ld, int ext, int wave_, int lane) {
+    base = reinterpret_cast<uint64_t>(p);
+    pitch = (uint32_t)ld * 2u;
+    wave = wave_;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int piece = wave * NI + i;
+      if constexpr (KC) {
+        const int r = 8 * piece + (lane >> 3);
+        const int ch = (lane & 7) ^ mm_swz(r);
+        off[i] = r < ext ? (uint32_t)r * pitch + (uint32_t)(ch * 16) : kMmOut;
+        kk[i] = ch * 8;
+      } else {
+        const int kr = piece * (64 / C) + lane / C;
+        const int ch = (lane % C) ^ mm_kswz(kr);
+        off[i] = ch * 8 < ext ? (uint32_t)kr * pitch + (uint32_t)(ch * 16) : kMmOut;
+        kk[i] = kr;
+        lim = ext;
+      }
+    }
+  }
+  // piece I of stage kt into `buf`; kend: the contraction's length
+  template <int I>
+  __device__ __forceinline__ void load(uint16_t* buf, int kt, int kend, int lane) const {
+    if constexpr (I < NI) {
+      // KC: k is contiguous, KS: k steps by the pitch.  The advance goes into
+      // the 64-bit scalar base, so lane offsets stay within one stage.
+      const uint64_t adv = KC ? (uint64_t)kt * (2 * kMmK) : (uint64_t)kt * kMmK * (uint64_t)pitch;
+      const __amdgpu_buffer_rsrc_t rs = mm_rsrc(reinterpret_cast<const void*>(base + adv));
+      const int left = kend - kt * kMmK;
+      uint16_t* dst = buf + (wave * NI + I) * 512;
+      if constexpr (ALIGNED) {
+        mm_dma16(rs, kk[I] < left ? off[I] : kMmOut, 0, dst);
+      } else {
+        uint32_t v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int piece = wave * NI + I;
+          bool in = off[I] != kMmOut;
+          if constexpr (KC) in = in && kk[I] + j < left;
+          else in = in && kk[I] < left && (((lane % C) ^ mm_kswz(piece * (64 / C) + lane / C)) * 8 + j) < lim;
+          v[j] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs, in ? off[I] + 2 * j : kMmOut, 0, 0);
+        }
+        u32x4_t w;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = v[2 * j] | (v[2 * j + 1] << 16);
+        *reinterpret_cast<u32x4_t*>(dst + lane * 8) = w;
+      }
+    }
+  }
+};
+
+// Fragments of a 32-wide block: lane l supplies row / column (l & 31) and the
+// k of 8 (l >> 5) ..+7 within each 16-wide step.
+template <bool KC, int R, int NB>
+struct MmFrag {
+  int o[KC ? 4 : NB];
+  // m0: first row / column of this wave's blocks within the tile (a multiple of 32)
+  __device__ __forceinline__ void init(int m0, int lane) {
+    if constexpr (KC) {
+      const int fr = lane & 31, fg = lane >> 5;
+#pragma unroll
+      for (int s = 0; s < 4; ++s) o[s] = (m0 + fr) * kMmK + (((2 * s + fg) ^ mm_swz(fr)) << 3);
+    } else {
+      const int q = (lane & 15) >> 2;
+      const int kr = 8 * (lane >> 5) + q;
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        const int ch = (m0 >> 3) + 4 * i + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+        o[i] = kr * R + ((ch ^ mm_kswz(q)) << 3) + 4 * (lane & 1);
+      }
+    }
+  }
+  template <int S, int I>
+  __device__ __forceinline__ u32x4_t get(const uint16_t* buf) const {
+    if constexpr (KC) {
+      return *reinterpret_cast<const u32x4_t*>(buf + o[S] + 32 * I * kMmK);
+    } else {
+      const s16x4_t lo = mm_read_tr(buf + o[I] + 16 * S * R);
+      const s16x4_t hi = mm_read_tr(buf + o[I] + (16 * S + 4) * R);
+      const uint2 l = __builtin_bit_cast(uint2, lo), h = __builtin_bit_cast(uint2, hi);
+      return u32x4_t{l.x, l.y, h.x, h.y};
+    }
+  }
+  static constexpr int kReads = KC ? 1 : 2;       // LDS reads per fragment
+};
+
+// -------------------------------------------------------------- tile list
+
+// Group bounds clamped into [0, rows] and non-decreasing, so that no offset
+// a caller can pass makes the kernel leave its buffers.
+__device__ __forceinline__ void mm_bounds(const MatmulArgs& p, int e, int& lo, int& hi) {
+  if (p.offsets == nullptr) {
+    lo = 0;
+    hi = p.rows;
+    return;
+  }
+  lo = min(max(p.offsets[e], 0), p.rows);
+  hi = min(max(p.offsets[e + 1], lo), p.rows);
+}
+
+struct MmTile {
+  int e;                                          // group
+  int split;                                      // contraction slice
+  int row0, nrows;                                // first output row (of the group), live rows
+  int col0;
+  int g0, gn;                                     // group's first row and rows
+};
+
+// Row tile rt of RT over cnt rows: whole 32-row blocks, dealt evenly.
+__device__ __forceinline__ void mm_row_tile(int cnt, int RT, int rt, int& off, int& n) {
+  const int b = ceil_div(cnt, 32);
+  const int lo = (int)((long long)b * rt / RT) * 32, hi = min((int)((long long)b * (rt + 1) / RT) * 32, cnt);
+  off = lo;
+  n = hi - lo;
+}
+
+// Tile `t` of an RT x NT grid, in bands of eight row tiles, row tiles fastest:
+// the tiles that run side by side on an XCD form a patch that shares both
+// operands in its L2.
+__device__ __forceinline__ void mm_grid_pos(int t, int RT, int NT, int& rt, int& ct) {
+  const int band = t / (8 * NT);
+  const int rem = t - band * 8 * NT;
+  const int nb = min(8, RT - 8 * band);
+  ct = rem / nb;
+  rt = 8 * band + rem - ct * nb;
+}
+
+// This block's tile, or false where the list is shorter than the grid.
+// Blocks go to the XCDs round-robin by index; XCD x takes the x-th eighth of
+// the list.  Ragged groups: every wave scans the group sizes (four per lane).
+template <bool WG, int BM, int BN>
+__device__ __forceinline__ bool mm_find_tile(const MatmulArgs& p, int lane, MmTile& t) {
+  const int NT = ceil_div(p.n, BN);
+  const bool ragged = !WG && p.offsets != nullptr;
+  long long total;
+  int sum = 0, cnt4[4] = {0, 0, 0, 0}, tl4[4] = {0, 0, 0, 0}, lo4[4] = {0, 0, 0, 0}, inc = 0;
+  const int RTd = ceil_div(p.m, BM);
+  if (ragged) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int e = 4 * lane + i;
+      if (e < p.E) {
+        int hi;
+        mm_bounds(p, e, lo4[i], hi);
+        cnt4[i] = hi - lo4[i];
+      }
+      tl4[i] = ceil_div(cnt4[i], BM) * NT;
+      sum += tl4[i];
+    }
+    inc = sum;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int o = __shfl_up(inc, d);
+      if (lane >= d) inc += o;
+    }
+    total = __builtin_amdgcn_readlane(inc, 63);
+  } else {
+    total = (long long)RTd * NT * p.splits * (WG ? p.E : 1);
+  }
+  const int x = blockIdx.x & 7;
+  const long long idx = (total * x >> 3) + (blockIdx.x >> 3);
+  if (idx >= (total * (x + 1) >> 3)) return false;
+  int local = (int)idx;
+  t.split = 0;
+  if (ragged) {
+    // the lane whose inclusive prefix first passes idx owns the group
+    const int L = __builtin_ctzll(__ballot(inc > local));
+    int before = __builtin_amdgcn_readlane(inc - sum, L);
+    int e = 4 * L, found = 0, lo = 0, cnt = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int n = __builtin_amdgcn_readlane(tl4[i], L);
+      if (!found) {
+        if (local < before + n) {
+          found = 1;
+          e = 4 * L + i;
+          lo = __builtin_amdgcn_readlane(lo4[i], L);
+          cnt = __builtin_amdgcn_readlane(cnt4[i], L);
+          local -= before;
+        } else {
+          before += n;
+        }
+      }
+    }
+    t.e = e;
+    t.g0 = lo;
+    t.gn = cnt;
+    const int RT = ceil_div(cnt, BM);
+    int rt, ct;
+    mm_grid_pos(local, RT, NT, rt, ct);
+    mm_row_tile(cnt, RT, rt, t.row0, t.nrows);
+    t.col0 = ct * BN;
+    return true;
+  }
+  const int per = RTd * NT;
+  const int v = local / per;                      // forward / row grad: slice; weight grad: group and slice
+  local -= v * per;
+  if constexpr (WG) {
+    t.e = v / p.splits;
+    t.split = v - t.e * p.splits;
+    mm_bounds(p, t.e, t.g0, t.gn);
+    t.gn -= t.g0;
+  } else {
+    t.e = 0;
+    t.split = v;
+    t.g0 = 0;
+    t.gn = p.rows;
+  }
+  int rt, ct;
+  mm_grid_pos(local, RTd, NT, rt, ct);
+  mm_row_tile(p.m, RTd, rt, t.row0, t.nrows);
+  t.col0 = ct * BN;
+  return true;
+}
+
+// ---------------------------------------------------------------- epilogue
+
+// Eight consecutive columns of one output row: bias, activation, residual,
+// stores.  `orow` is the row of out / residual / pre, `col` its first column.
+template <bool F16>
+__device__ __forceinline__ void mm_finish8(const MatmulArgs& p, float (&v)[8], const float (&bias)[8], int64_t orow,
+                                           int col, int64_t out_off) {
+  const int n = p.n - col;                        // columns left
+  if (p.bias != nullptr) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v[q] += bias[q];
+  }
+  const bool vec = p.vec && n >= 8;
+  if (p.pre != nullptr) {
+    uint16_t* o = p.pre + orow * p.ldp + col;
+    if (vec) {
+      *reinterpret_cast<u32x4_t*>(o) = u32x4_t{mm_pack2<F16>(v[0], v[1]), mm_pack2<F16>(v[2], v[3]),
+                                               mm_pack2<F16>(v[4], v[5]), mm_pack2<F16>(v[6], v[7])};
+    } else {
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (q < n) o[q] = mm_store1<F16>(v[q]);
+    }
+  }
+  if (p.act != kActNone) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v[q] = mm_act(v[q], p.act);
+  }
+  if (p.residual != nullptr) {
+    const uint16_t* r = p.residual + orow * p.ldr + col;
+    if (vec) {
+      float f[8];
+      mm_unpack8<F16>(*reinterpret_cast<const u32x4_t*>(r), f);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[q] += f[q];
+    } else {
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (q < n) v[q] += mm_load1<F16>(r[q]);
+    }
+  }
+  const int64_t at = out_off + orow * p.ldo + col;
+  if (p.out_f32) {
+    float* o = static_cast<float*>(p.out) + at;
+    if (vec) {
+      *reinterpret_cast<f32x4_t*>(o) = f32x4_t{v[0], v[1], v[2], v[3]};
+      *reinterpret_cast<f32x4_t*>(o + 4) = f32x4_t{v[4], v[5], v[6], v[7]};
+    } else {
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (q < n) o[q] = v[q];
+    }
+  } else {
+    uint16_t* o = static_cast<uint16_t*>(p.out) + at;
+    if (vec) {
+      *reinterpret_cast<u32x4_t*>(o) = u32x4_t{mm_pack2<F16>(v[0], v[1]), mm_pack2<F16>(v[2], v[3]),
+                                               mm_pack2<F16>(v[4], v[5]), mm_pack2<F16>(v[6], v[7])};
+    } else {
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (q < n) o[q] = mm_store1<F16>(v[q]);
+    }
+  }
+}
+
+template <bool F16>
+__device__ __forceinline__ void mm_bias8(const MatmulArgs& p, int col, float (&b)[8]) {
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    b[q] = 0.f;
+    if (p.bias != nullptr && col + q < p.n)
+      b[q] = p.bias_f32 ? static_cast<const float*>(p.bias)[col + q]
+                        : mm_load1<F16>(static_cast<const uint16_t*>(p.bias)[col + q]);
+  }
+}
+
+// -------------------------------------------------------------- the kernel
+
+#define MM_WAIT_VM(N) __builtin_amdgcn_s_waitcnt(((N) & 15) | (((N) >> 4) << 14) | 0x0F70)
+
+// One BM x BN output tile per block: WM x WN waves of (32 FM) x 64.  AKC /
+// BKC: how each operand is stored.  A is the operand of the output's rows, B
+// that of its columns; the MFMA takes B first, so a lane ends with one output
+// row and runs of four consecutive columns.
+template <bool F16, bool AKC, bool BKC, int BM, int BN, int WM, int WN, bool ALIGNED>
+__global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 ? 1 : 2) void matmul_tile_kernel(MatmulArgs p) {
+  constexpr int NW = WM * WN;
+  constexpr int FM = BM / (32 * WM);
+  static_assert(BN == 64 * WN, "a wave covers 64 columns");
+  constexpr bool WG = !AKC;                       // weight grad: the contraction runs over rows
+  constexpr int STA = BM * kMmK, STB = BN * kMmK;
+  // Every buffer an array of its own, so that the compiler knows that loads
+  // into one leave reads of another alone.
+  __shared__ __align__(16) uint16_t sa0[STA];
+  __shared__ __align__(16) uint16_t sa1[STA];
+  __shared__ __align__(16) uint16_t sb0[STB];
+  __shared__ __align__(16) uint16_t sb1[STB];
+  __shared__ __align__(16) uint16_t sb2[STB];
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+  MmTile t;
+  if (!mm_find_tile<WG, BM, BN>(p, lane, t)) return;
+
+  // contraction range of this tile, as whole stages of the slice
+  int kbeg = 0, kend = WG ? t.gn : p.k;
+  if (p.splits > 1) {
+    const int per = ceil_div(ceil_div(kend, kMmK), p.splits) * kMmK;
+    kbeg = min(t.split * per, kend);
+    kend = min(kbeg + per, kend) - kbeg;
+  }
+  const int KT = max(1, ceil_div(kend, kMmK));
+
+  MmOperand<AKC, BM, NW, ALIGNED> la;
+  MmOperand<BKC, BN, NW, ALIGNED> lb;
+  if constexpr (AKC)
+    la.init(p.a + (int64_t)(t.g0 + t.row0) * p.lda + kbeg, p.lda, t.nrows, wave, lane);
+  else
+    la.init(p.a + (int64_t)(t.g0 + kbeg) * p.lda + t.row0, p.lda, p.m - t.row0, wave, lane);
+  const uint16_t* bp = WG ? p.b + (int64_t)t.g0 * p.ldb : p.b + (int64_t)t.e * p.b_group;
+  if constexpr (BKC) lb.init(bp + (int64_t)t.col0 * p.ldb + kbeg, p.ldb, p.n - t.col0, wave, lane);
+  else lb.init(bp + (int64_t)kbeg * p.ldb + t.col0, p.ldb, p.n - t.col0, wave, lane);
+  constexpr int BI = MmOperand<BKC, BN, NW, ALIGNED>::NI;
+
+  MmFrag<AKC, BM, FM> ra;
+  MmFrag<BKC, BN, 2> rb;
+  ra.init(wm * 32 * FM, lane);
+  rb.init(wn * 64, lane);
+
+  // NBLK: this wave's 32-row blocks with live rows; the others are neither
+  // multiplied nor stored.  Every wave issues its loads and meets every barrier.
+  auto body = [&](auto nblk_c) __attribute__((always_inline)) {
+    constexpr int NBLK = decltype(nblk_c)::value;
+    constexpr int NA = NBLK > 0 ? NBLK : 1;
+    f32x16_t acc[NA][2];
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.f;
+    u32x4_t fa[NA], fb[2], ga[NA], gb[2];
+
+#define MM_FRAG1(FA, I_, ABUF, S_) if constexpr (NBLK > (I_)) FA[(I_) < NA ? (I_) : 0] = ra.template get<S_, I_>(ABUF);
+#define MM_FRAG(FA, FB, ABUF, BBUF, S_)                                        \
+  if constexpr (NBLK > 0) {                                                    \
+    MM_FRAG1(FA, 0, ABUF, S_) MM_FRAG1(FA, 1, ABUF, S_)                        \
+    MM_FRAG1(FA, 2, ABUF, S_) MM_FRAG1(FA, 3, ABUF, S_)                        \
+    FB[0] = rb.template get<S_, 0>(BBUF);                                      \
+    FB[1] = rb.template get<S_, 1>(BBUF);                                      \
+  }
+#define MM_MMA(FA, FB)                                                         \
+  _Pragma("unroll") for (int i = 0; i < NBLK; ++i)                             \
+      _Pragma("unroll") for (int j = 0; j < 2; ++j) acc[i][j] = mm_mfma<F16>(FB[j], FA[i], acc[i][j]);
+// One step: the next step's fragment reads, then this step's products, then a
+// load of the column operand; nothing moves past the end of the group.
+#define MM_ORDER(MMA_, VM_)                                                    \
+  if constexpr (NBLK > 0 && ALIGNED) {                                         \
+    __builtin_amdgcn_sched_group_barrier(0x100, NBLK * decltype(ra)::kReads + 2 * decltype(rb)::kReads, 0); \
+    if constexpr (MMA_) __builtin_amdgcn_sched_group_barrier(0x008, 2 * NBLK, 0); \
+  }                                                                            \
+  if constexpr ((VM_) && ALIGNED) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0); \
+  __builtin_amdgcn_sched_barrier(0);
+#define MM_LOAD_A(BUF, KT_)                                                    \
+  la.template load<0>(BUF, KT_, kend, lane); la.template load<1>(BUF, KT_, kend, lane); \
+  la.template load<2>(BUF, KT_, kend, lane); la.template load<3>(BUF, KT_, kend, lane);
+// Stage KT_: this wave's reads of the last stage and its loads of this one
+// are complete (the column operand of the next stage, issued last, may stay in
+// flight), the barrier publishes them; then the rows of the next stage start
+// into a buffer that every wave has finished reading, and the four 16-wide
+// steps run, pipelined by one across the barrier.
+#define MM_STAGE(ABUF, NABUF, BBUF, NBBUF, KT_, FIRST)                         \
+  {                                                                            \
+    __builtin_amdgcn_s_waitcnt(0xC07F);                                        \
+    if constexpr (ALIGNED) MM_WAIT_VM(BI);                                     \
+    __builtin_amdgcn_s_barrier();                                              \
+    MM_LOAD_A(NABUF, (KT_) + 1)                                                \
+    __builtin_amdgcn_sched_barrier(0);                                         \
+    MM_FRAG(ga, gb, ABUF, BBUF, 0)                                             \
+    if constexpr (!(FIRST)) { MM_MMA(fa, fb) }                                 \
+    lb.template load<0>(NBBUF, (KT_) + 2, kend, lane);                         \
+    MM_ORDER(!(FIRST), BI > 0)                                                 \
+    MM_FRAG(fa, fb, ABUF, BBUF, 1)                                             \
+    MM_MMA(ga, gb)                                                             \
+    lb.template load<1>(NBBUF, (KT_) + 2, kend, lane);                         \
+    MM_ORDER(true, BI > 1)                                                     \
+    MM_FRAG(ga, gb, ABUF, BBUF, 2)                                             \
+    MM_MMA(fa, fb)                                                             \
+    lb.template load<2>(NBBUF, (KT_) + 2, kend, lane);                         \
+    MM_ORDER(true, BI > 2)                                                     \
+    MM_FRAG(fa, fb, ABUF, BBUF, 3)                                             \
+    MM_MMA(ga, gb)                                                             \
+    lb.template load<3>(NBBUF, (KT_) + 2, kend, lane);                         \
+    MM_ORDER(true, BI > 3)                                                     \
+  }
+#define MM_A(I) ((I) % 2 == 0 ? sa0 : sa1)
+#define MM_B(I) ((I) % 3 == 0 ? sb0 : (I) % 3 == 1 ? sb1 : sb2)
+#define MM_U(U, KT_, FIRST) MM_STAGE(MM_A(U), MM_A((U) + 1), MM_B(U), MM_B((U) + 2), KT_, FIRST)
+
+    lb.template load<0>(sb0, 0, kend, lane);
+    lb.template load<1>(sb0, 0, kend, lane);
+    lb.template load<2>(sb0, 0, kend, lane);
+    lb.template load<3>(sb0, 0, kend, lane);
+    MM_LOAD_A(sa0, 0)
+    lb.template load<0>(sb1, 1, kend, lane);
+    lb.template load<1>(sb1, 1, kend, lane);
+    lb.template load<2>(sb1, 1, kend, lane);
+    lb.template load<3>(sb1, 1, kend, lane);
+    MM_U(0, 0, true)
+    int kt = 1;
+    for (; kt + 5 < KT; kt += 6) {
+      MM_U(1, kt, false)
+      MM_U(2, kt + 1, false)
+      MM_U(3, kt + 2, false)
+      MM_U(4, kt + 3, false)
+      MM_U(5, kt + 4, false)
+      MM_U(6, kt + 5, false)
+    }
+    if (kt < KT) MM_U(1, kt, false)
+    if (kt + 1 < KT) MM_U(2, kt + 1, false)
+    if (kt + 2 < KT) MM_U(3, kt + 2, false)
+    if (kt + 3 < KT) MM_U(4, kt + 3, false)
+    if (kt + 4 < KT) MM_U(5, kt + 4, false)
+    MM_MMA(fa, fb)
+    MM_WAIT_VM(0);
+    mm_lds_barrier();
+
+    // Epilogue: each wave stages one 32 x 64 fp32 block at a time (8 KB of the
+    // row buffers, free now) and reads it back as row segments of eight
+    // columns, so that loads and stores cover whole 128-byte segments.  Chunk
+    // c (four columns) of row r sits at c ^ (r & 15): no bank conflicts.
+    static_assert(STA * 2 * 2 >= NW * 8192, "staging slots in the row buffers");
+    float* blk = reinterpret_cast<float*>(wave < NW / 2 ? sa0 : sa1) + (wave % (NW / 2)) * 2048;
+    const int fr = lane & 31, fg = lane >> 5, ch = lane & 7;
+    const int col = t.col0 + wn * 64 + ch * 8;
+    float bias[8];
+    mm_bias8<F16>(p, col, bias);
+    const int64_t out_off =
+        WG ? ((int64_t)t.e * p.splits + t.split) * p.out_group : (int64_t)t.split * p.out_group;
+    const int64_t row_base = (int64_t)(WG ? 0 : t.g0) + t.row0;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      if (i >= NBLK) break;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const f32x16_t& a0 = acc[i < NA ? i : 0][j];
+          const int c = 8 * j + 2 * b + fg;
+          *reinterpret_cast<f32x4_t*>(blk + fr * 64 + ((c ^ (fr & 15)) << 2)) =
+              f32x4_t{a0[4 * b], a0[4 * b + 1], a0[4 * b + 2], a0[4 * b + 3]};
+        }
+      __builtin_amdgcn_wave_barrier();            // a wave's LDS operations complete in order
+      if (col < p.n) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          const int r = 8 * s + (lane >> 3);
+          const int row = wm * 32 * FM + 32 * i + r;
+          const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(blk + r * 64 + (((2 * ch) ^ (r & 15)) << 2));
+          const f32x4_t hi = *reinterpret_cast<const f32x4_t*>(blk + r * 64 + (((2 * ch + 1) ^ (r & 15)) << 2));
+          if (row < t.nrows) {
+            float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+            mm_finish8<F16>(p, v, bias, row_base + row, col, out_off);
+          }
+        }
+      }
+      __builtin_amdgcn_wave_barrier();
+    }
+  };
+  const int live = t.nrows - wm * 32 * FM;
+  const int nblk = live <= 0 ? 0 : min(FM, ceil_div(live, 32));
+  if (!ALIGNED || nblk == FM) {
+    body(std::integral_constant<int, FM>{});
+  } else if (nblk == 0) {
+    body(std::integral_constant<int, 0>{});
+  } else if (nblk == 1) {
+    body(std::integral_constant<int, 1>{});
+  } else if constexpr (FM >= 3) {
+    if (nblk == 2) body(std::integral_constant<int, 2>{});
+    else if constexpr (FM >= 4) body(std::integral_constant<int, 3>{});
+  }
+#undef MM_FRAG1
+#undef MM_FRAG
+#undef MM_MMA
+#undef MM_ORDER
+#undef MM_LOAD_A
+#undef MM_STAGE
+#undef MM_A
+#undef MM_B
+#undef MM_U
+}
+#undef MM_WAIT_VM
+
+}  // namespace moe

@@ -1,0 +1,41 @@
+// Launches the tile kernel's instances of one form (one form per source file,
+// so that they compile in parallel).
+#pragma once
+#include "matmul.h"
+
+namespace moe {
+
+template <bool F16, bool AKC, bool BKC, int BM, int BN, int WM, int WN, bool ALIGNED>
+hipError_t launch_matmul_tile(const MatmulArgs& a, hipStream_t st) {
+  constexpr bool WG = !AKC;
+  const long long NT = ceil_div(a.n, BN);
+  long long ub;                                   // at least the tiles of the list
+  if (!WG && a.offsets != nullptr)
+    ub = ((long long)a.rows / BM + (a.E < a.rows ? a.E : a.rows)) * NT;
+  else
+    ub = (long long)ceil_div(a.m, BM) * NT * a.splits * (WG ? a.E : 1);
+  const long long grid = (ub + 7) / 8 * 8;
+  if (grid <= 0) return hipSuccess;
+  if (grid > 0x7fffffffLL / (64 * WM * WN)) return hipErrorInvalidConfiguration;
+  hipLaunchKernelGGL((matmul_tile_kernel<F16, AKC, BKC, BM, BN, WM, WN, ALIGNED>), dim3((unsigned)grid),
+                     dim3(64 * WM * WN), 0, st, a);
+  return hipGetLastError();
+}
+
+// 256 x 256 tiles where they alone give the card about a block per CU, else
+// 128 x 128.
+inline bool matmul_big(const MatmulArgs& a, bool wg) {
+  const long long E = wg ? (long long)a.E * a.splits : a.offsets != nullptr ? a.E : a.splits;
+  const long long rows = (!wg && a.offsets != nullptr) ? (a.rows + a.E - 1) / a.E : a.m;
+  if (rows <= 128 || a.n <= 128) return false;
+  return E * ((rows + 255) / 256) * ((a.n + 255) / 256) >= 192;
+}
+
+template <bool F16, bool AKC, bool BKC>
+hipError_t launch_matmul_form(const MatmulArgs& a, hipStream_t st) {
+  if (!a.aligned) return launch_matmul_tile<F16, AKC, BKC, 128, 128, 2, 2, false>(a, st);
+  if (matmul_big(a, !AKC)) return launch_matmul_tile<F16, AKC, BKC, 256, 256, 2, 4, true>(a, st);
+  return launch_matmul_tile<F16, AKC, BKC, 128, 128, 2, 2, true>(a, st);
+}
+
+}  // namespace moe

@@ -355,6 +355,136 @@ int moe_layer_pipelined(const moe_dims* dims, uint32_t flags, int32_t n_micro, c
  */
 int moe_set_stage_events(void* const* events, int n);
 
+/* ===================== around the expert layer ============================
+ *
+ * Layer norm, linear layers with a fused epilogue and matrix products grouped
+ * by expert, each with its gradients: what a block needs beside moe_layer, and
+ * what training its experts needs.  The conventions above hold, except:
+ *  - types are given per call (moe_dtype); pointers need only their element's
+ *    alignment.  Rows may be strided: ld_* is the distance of two rows in
+ *    elements (0 = packed), at least the row's width and at most 2^20;
+ *    elements of a row are contiguous.  Rows of 16-byte pitch and alignment
+ *    whose widths are multiples of 8 take the fast loads, all others a path
+ *    that loads element by element.
+ *  - rows = 0 is allowed: outputs with a row per input row are left alone,
+ *    gradients summed over rows are set to zero.
+ *  - outputs must not overlap inputs unless stated.
+ *  - products: operands bf16 or fp16, sums in fp32, one rounding at the store.
+ *  - Limits: rows <= 2^24; widths of products 1..65536; norm widths 1..16384;
+ *    1 <= n_experts <= 256; at most 2^22 output tiles of 128 x 128 per product
+ *    (else MOE_ERR_UNSUPPORTED).
+ */
+enum moe_dtype { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F16 = 1, MOE_DTYPE_F32 = 2 };
+
+enum moe_act {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_RELU = 1,
+  MOE_ACT_GELU = 2,       /* z (1 + erf(z / sqrt 2)) / 2                               */
+  MOE_ACT_GELU_TANH = 3,  /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2           */
+  MOE_ACT_SILU = 4        /* z / (1 + e^-z)                                            */
+};
+
+enum {
+  /* moe_layer_norm*: root-mean-square form (the mean is not subtracted) */
+  MOE_NORM_RMS = 1u
+};
+
+typedef struct moe_norm_dims {
+  int32_t rows, cols;
+  int32_t dtype;          /* x, y, dy, dx: any moe_dtype                               */
+  int32_t param_dtype;    /* gamma, beta, dgamma, dbeta: dtype or MOE_DTYPE_F32        */
+  uint32_t flags;         /* MOE_NORM_RMS or 0                                         */
+  float eps;              /* >= 0                                                      */
+  int64_t ld_x, ld_y, ld_dy, ld_dx;
+} moe_norm_dims;
+
+/*
+ * moe_layer_norm - y = (x - mu) rstd gamma + beta by rows,
+ *   mu = mean(x) (0 with MOE_NORM_RMS), rstd = 1 / sqrt(mean((x - mu)^2) + eps),
+ * in fp32, the variance from the centred values.  gamma / beta [cols] or NULL
+ * (1 / 0); mean / rstd [rows] fp32: outputs for the backward pass, or NULL.
+ * y may be x (same pointer and stride).
+ */
+int moe_layer_norm(const moe_norm_dims* dims, const void* x, const void* gamma, const void* beta, void* y,
+                   float* mean, float* rstd, moe_stream stream);
+
+/*
+ * moe_layer_norm_backward - with n = (x - mu) rstd and g = dy gamma:
+ *   dx = rstd (g - mean(g) - n mean(g n))   (MOE_NORM_RMS: no mean(g)),
+ *   dgamma = sum over rows of dy n,  dbeta = sum over rows of dy.
+ * mean (ignored with MOE_NORM_RMS, may then be NULL) and rstd [rows] fp32 are
+ * those of the forward pass.  dx, dgamma, dbeta: outputs, each may be NULL.
+ * dx may be dy or x (same pointer and stride).
+ * ws: moe_layer_norm_backward_workspace_bytes.
+ */
+int moe_layer_norm_backward_workspace_bytes(const moe_norm_dims* dims, size_t* bytes);
+int moe_layer_norm_backward(const moe_norm_dims* dims, const void* dy, const void* x, const void* gamma,
+                            const float* mean, const float* rstd, void* dx, void* dgamma, void* dbeta, void* ws,
+                            size_t ws_bytes, moe_stream stream);
+
+typedef struct moe_linear_dims {
+  int32_t rows, in_features, out_features;
+  int32_t dtype;          /* x, w, residual, y, pre, dy, dx: bf16 or fp16              */
+  int32_t act;            /* moe_act                                                   */
+  int32_t bias_dtype;     /* bias, dbias: dtype or MOE_DTYPE_F32                       */
+  int32_t dw_dtype;       /* dw: dtype or MOE_DTYPE_F32                                */
+  int64_t ld_x, ld_w, ld_residual, ld_y, ld_pre, ld_dy, ld_dx;
+} moe_linear_dims;
+
+/*
+ * moe_linear - z = x w^T + bias, y = act(z) + residual, in one pass over the
+ * output.  x [rows][in]; w [out][in]; bias [out] or NULL; residual [rows][out]
+ * or NULL (may be y, same pointer and stride); y [rows][out]; pre [rows][out]
+ * or NULL: z rounded to dtype, for the backward pass (y uses z itself).
+ * ws: moe_linear_workspace_bytes (may be 0).
+ */
+int moe_linear_workspace_bytes(const moe_linear_dims* dims, size_t* bytes);
+int moe_linear(const moe_linear_dims* dims, const void* x, const void* w, const void* bias, const void* residual,
+               void* y, void* pre, void* ws, size_t ws_bytes, moe_stream stream);
+
+/*
+ * moe_linear_backward - with g = dy act'(pre) (rounded to dtype as an operand
+ * of the products; the bias gradient sums the unrounded values):
+ *   dx = g w,  dw = g^T x,  dbias = sum over rows of g.
+ * The residual's gradient is dy.  pre [rows][out] (NULL iff act is
+ * MOE_ACT_NONE; relu's slope at 0 is 0).  dx [rows][in], dw [out][in] packed,
+ * dbias [out]: outputs, each may be NULL (x may be NULL without dw, w without dx).
+ * ws: moe_linear_backward_workspace_bytes.
+ */
+int moe_linear_backward_workspace_bytes(const moe_linear_dims* dims, size_t* bytes);
+int moe_linear_backward(const moe_linear_dims* dims, const void* dy, const void* x, const void* w, const void* pre,
+                        void* dx, void* dw, void* dbias, void* ws, size_t ws_bytes, moe_stream stream);
+
+typedef struct moe_grouped_dims {
+  int32_t rows;           /* rows of x and y (at least expert_offsets[E])              */
+  int32_t n_experts, in_features, out_features;
+  int32_t dtype;          /* x, w, y, dy, dx: bf16 or fp16                             */
+  int32_t dw_dtype;       /* dw: dtype or MOE_DTYPE_F32                                */
+  int64_t ld_x;           /* x, dx                                                     */
+  int64_t ld_y;           /* y, dy                                                     */
+} moe_grouped_dims;
+
+/*
+ * Matrix products grouped by expert.  Rows [expert_offsets[e],
+ * expert_offsets[e+1]) belong to expert e (moe_permute's offsets, [E+1] int32
+ * on the device, never read by the host); w [E][out][in] packed.
+ *   moe_grouped_matmul:        y[r]  = x[r] w[e]^T
+ *   moe_grouped_matmul_dgrad:  dx[r] = dy[r] w[e]
+ *   moe_grouped_matmul_wgrad:  dw[e] = sum over e's rows of dy[r]^T x[r]
+ * Experts without rows cost nothing in the first two and get a zero dw.
+ * Rows behind expert_offsets[E] (and before expert_offsets[0]) are neither
+ * read nor written.  Offsets outside [0, rows] or decreasing are clamped on
+ * the device: no access leaves the buffers.
+ * ws: moe_grouped_matmul_wgrad_workspace_bytes (may be 0); the others need none.
+ */
+int moe_grouped_matmul(const moe_grouped_dims* dims, const void* x, const int32_t* expert_offsets, const void* w,
+                       void* y, moe_stream stream);
+int moe_grouped_matmul_dgrad(const moe_grouped_dims* dims, const void* dy, const int32_t* expert_offsets,
+                             const void* w, void* dx, moe_stream stream);
+int moe_grouped_matmul_wgrad_workspace_bytes(const moe_grouped_dims* dims, size_t* bytes);
+int moe_grouped_matmul_wgrad(const moe_grouped_dims* dims, const void* dy, const void* x,
+                             const int32_t* expert_offsets, void* dw, void* ws, size_t ws_bytes, moe_stream stream);
+
 #ifdef __cplusplus
 }
 #endif
