@@ -14,7 +14,6 @@
 
 namespace moe {
 
-typedef float f32x16_t __attribute__((ext_vector_type(16)));
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
@@ -26,13 +25,12 @@ constexpr uint32_t kMmOut = 0x80000000u;          // an offset past it: the load
 // ------------------------------------------------------------ small helpers
 
 template <bool F16>
-__device__ __forceinline__ f32x16_t mm_mfma(u32x4_t a, u32x4_t b, f32x16_t c) {
+__device__ __forceinline__ f32x4_t mm_mfma(u32x4_t a, u32x4_t b, f32x4_t c) {
   if constexpr (F16)
-    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c,
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c,
                                                   0, 0, 0);
   else
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b),
-                                                   c, 0, 0, 0);
+    return mfma16(a, b, c);
 }
 
 template <bool F16>
@@ -102,18 +100,22 @@ __device__ __forceinline__ float mm_act(float z, int act) {
 // c ^ mm_swz(r): the 32 rows that a fragment read touches at one chunk fall
 // on distinct bank groups.
 __device__ __forceinline__ int mm_swz(int row) { return ((row >> 1) ^ ((row & 1) << 2)) & 7; }
-// KS stage: rows are k, R columns each; chunk c of row r sits at c ^ (4 (r & 3)),
-// so that the four rows x 64 bytes a transposing read of 32 lanes covers are
-// in distinct quarters of the 64 banks.
-__device__ __forceinline__ int mm_kswz(int krow) { return (krow & 3) << 2; }
+// KS stage: rows are k, R columns each; chunk c of row r sits at c ^ mm_kswz(r).
+// A transposing read of 32 lanes covers 32 bytes of the four rows 8 g ..+3
+// (or +4 ..+7) for two neighbouring g: r & 3 picks a quarter of the 64 banks
+// and the parity of g a half of it, so the eight pieces do not meet.
+__device__ __forceinline__ int mm_kswz(int krow) { return ((krow & 3) << 2) | (((krow >> 3) & 1) << 1); }
 
 // How one operand's 64-wide stages reach LDS.  KC: stage [R rows][64 k]; KS:
 // stage [64 k][R columns].  Either way a stage is R * 128 bytes and each of
 // the NI loads of a wave fills 1 KB of it, lane l the bytes 16 l ..+15.
 // ALIGNED: 16-byte loads straight into LDS (rows of 16-byte pitch and
-// alignment, widths in multiples of 8).  Otherwise each element is loaded by
-// itself through registers: any strides and sizes.
-// Rows, columns and k past the ends take an offset past the buffer: zeros.
+// alignment, widths in multiples of 8).  Otherwise any strides and sizes: the
+// 16 bytes of a piece are loaded unaligned where they are whole, by elements
+// at the matrix's edge, into registers at the start of a stage and written to
+// LDS at its end.
+// Rows, columns and k past the ends become zeros (ALIGNED: by an offset past
+// the buffer, which reads no memory).
 template <bool KC, int R, int NW, bool ALIGNED>
 struct MmOperand {
   static constexpr int NI = R / (8 * NW);
@@ -123,7 +125,7 @@ struct MmOperand {
   uint32_t off[NI];                               // per lane: byte offset within a stage
   int kk[NI];                                     // per lane: first k of the piece within a stage
   int wave;
-  int lim;                                        // !ALIGNED: KC unused; KS columns left from the lane's piece
+  int lim;                                        // KS: columns left in the matrix
 
   // KC: p = element (first row of the tile, first k), ext = live rows.
   // KS: p = element (first k, first column), ext = columns left in the matrix.
@@ -148,66 +150,84 @@ struct MmOperand {
       }
     }
   }
-  // piece I of stage kt into `buf`; kend: the contraction's length
-  template <int I>
-  __device__ __forceinline__ void load(uint16_t* buf, int kt, int kend, int lane) const {
-    if constexpr (I < NI) {
-      // KC: k is contiguous, KS: k steps by the pitch.  The advance goes into
-      // the 64-bit scalar base, so lane offsets stay within one stage.
-      const uint64_t adv = KC ? (uint64_t)kt * (2 * kMmK) : (uint64_t)kt * kMmK * (uint64_t)pitch;
-      const __amdgpu_buffer_rsrc_t rs = mm_rsrc(reinterpret_cast<const void*>(base + adv));
+  // k is contiguous (KC) or steps by the pitch (KS).  The advance to stage kt
+  // goes into the 64-bit scalar base, so lane offsets stay within one stage.
+  __device__ __forceinline__ uint64_t at(int kt) const {
+    return base + (KC ? (uint64_t)kt * (2 * kMmK) : (uint64_t)kt * kMmK * (uint64_t)pitch);
+  }
+  // ALIGNED: pieces I0..I1-1 of stage kt into `buf`; kend: the contraction's length
+  template <int I0, int I1>
+  __device__ __forceinline__ void loads(uint16_t* buf, int kt, int kend) const {
+    if constexpr (ALIGNED && I0 < I1) {
+      mm_dma16(mm_rsrc(reinterpret_cast<const void*>(at(kt))), kk[I0] < kend - kt * kMmK ? off[I0] : kMmOut, 0,
+               buf + (wave * NI + I0) * 512);
+      loads<I0 + 1, I1>(buf, kt, kend);
+    }
+  }
+  // !ALIGNED: every piece of stage kt into registers, and from there to LDS
+  __device__ __forceinline__ void fetch(u32x4_t (&v)[NI], int kt, int kend, int lane) const {
+    if constexpr (!ALIGNED) {
+      const uint64_t b = at(kt);
       const int left = kend - kt * kMmK;
-      uint16_t* dst = buf + (wave * NI + I) * 512;
-      if constexpr (ALIGNED) {
-        mm_dma16(rs, kk[I] < left ? off[I] : kMmOut, 0, dst);
-      } else {
-        uint32_t v[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int piece = wave * NI + I;
-          bool in = off[I] != kMmOut;
-          if constexpr (KC) in = in && kk[I] + j < left;
-          else in = in && kk[I] < left && (((lane % C) ^ mm_kswz(piece * (64 / C) + lane / C)) * 8 + j) < lim;
-          v[j] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs, in ? off[I] + 2 * j : kMmOut, 0, 0);
+      for (int i = 0; i < NI; ++i) {
+        int n = 0;                                // elements of the piece inside the matrix
+        if (off[i] != kMmOut) {
+          const int piece = wave * NI + i;
+          if constexpr (KC) n = left - kk[i];
+          else n = kk[i] < left ? lim - ((lane % C) ^ mm_kswz(piece * (64 / C) + lane / C)) * 8 : 0;
         }
-        u32x4_t w;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = v[2 * j] | (v[2 * j + 1] << 16);
-        *reinterpret_cast<u32x4_t*>(dst + lane * 8) = w;
+        const uint16_t* src = reinterpret_cast<const uint16_t*>(b + off[i]);
+        if (n >= 8) {
+          __builtin_memcpy(&v[i], src, 16);       // one load: unaligned access is on
+        } else {
+          uint64_t lo = 0, hi = 0;
+#pragma nounroll
+          for (int j = 0; j < n; ++j) {
+            const uint64_t e = (uint64_t)src[j] << (16 * (j & 3));
+            if (j < 4) lo |= e;
+            else hi |= e;
+          }
+          v[i] = u32x4_t{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+        }
       }
+    }
+  }
+  __device__ __forceinline__ void put(const u32x4_t (&v)[NI], uint16_t* buf, int lane) const {
+    if constexpr (!ALIGNED) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) *reinterpret_cast<u32x4_t*>(buf + (wave * NI + i) * 512 + lane * 8) = v[i];
     }
   }
 };
 
-// Fragments of a 32-wide block: lane l supplies row / column (l & 31) and the
-// k of 8 (l >> 5) ..+7 within each 16-wide step.
-template <bool KC, int R, int NB>
+// Fragments of a 16-wide block: lane l supplies row / column (l & 15) and the
+// k of 8 (l >> 4) ..+7 within each 32-wide step.
+template <bool KC, int R>
 struct MmFrag {
-  int o[KC ? 4 : NB];
-  // m0: first row / column of this wave's blocks within the tile (a multiple of 32)
+  int o[KC ? 2 : 1];
+  // m0: first row / column of this wave's blocks within the tile (a multiple of 64)
   __device__ __forceinline__ void init(int m0, int lane) {
+    const int fr = lane & 15, fg = lane >> 4;
     if constexpr (KC) {
-      const int fr = lane & 31, fg = lane >> 5;
 #pragma unroll
-      for (int s = 0; s < 4; ++s) o[s] = (m0 + fr) * kMmK + (((2 * s + fg) ^ mm_swz(fr)) << 3);
+      for (int s = 0; s < 2; ++s) o[s] = (m0 + fr) * kMmK + (((4 * s + fg) ^ mm_swz(fr)) << 3);
     } else {
-      const int q = (lane & 15) >> 2;
-      const int kr = 8 * (lane >> 5) + q;
-#pragma unroll
-      for (int i = 0; i < NB; ++i) {
-        const int ch = (m0 >> 3) + 4 * i + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
-        o[i] = kr * R + ((ch ^ mm_kswz(q)) << 3) + 4 * (lane & 1);
-      }
+      const int kr = 8 * fg + (fr >> 2);
+      o[0] = kr * R + ((((m0 >> 3) + ((fr & 3) >> 1)) ^ mm_kswz(kr)) << 3) + 4 * (fr & 1);
     }
   }
+  // fragment of block I in step S
   template <int S, int I>
   __device__ __forceinline__ u32x4_t get(const uint16_t* buf) const {
     if constexpr (KC) {
-      return *reinterpret_cast<const u32x4_t*>(buf + o[S] + 32 * I * kMmK);
+      return *reinterpret_cast<const u32x4_t*>(buf + o[S] + 16 * I * kMmK);
     } else {
-      const s16x4_t lo = mm_read_tr(buf + o[I] + 16 * S * R);
-      const s16x4_t hi = mm_read_tr(buf + o[I] + (16 * S + 4) * R);
-      const uint2 l = __builtin_bit_cast(uint2, lo), h = __builtin_bit_cast(uint2, hi);
+      // block I is chunks 2 I, 2 I + 1 past the first: an exclusive or, like
+      // the swizzle, since m0 leaves those bits of the chunk index zero
+      const int at = (o[0] ^ (I << 4)) + 32 * S * R;
+      const uint2 l = __builtin_bit_cast(uint2, mm_read_tr(buf + at));
+      const uint2 h = __builtin_bit_cast(uint2, mm_read_tr(buf + at + 4 * R));
       return u32x4_t{l.x, l.y, h.x, h.y};
     }
   }
@@ -255,11 +275,24 @@ __device__ __forceinline__ void mm_grid_pos(int t, int RT, int NT, int& rt, int&
   rt = 8 * band + rem - ct * nb;
 }
 
-// This block's tile, or false where the list is shorter than the grid.
-// Blocks go to the XCDs round-robin by index; XCD x takes the x-th eighth of
-// the list.  Ragged groups: every wave scans the group sizes (four per lane).
+// The same value in every lane, kept in scalar registers.
+__device__ __forceinline__ void mm_scalar(MmTile& t) {
+  t.e = __builtin_amdgcn_readfirstlane(t.e);
+  t.split = __builtin_amdgcn_readfirstlane(t.split);
+  t.row0 = __builtin_amdgcn_readfirstlane(t.row0);
+  t.nrows = __builtin_amdgcn_readfirstlane(t.nrows);
+  t.col0 = __builtin_amdgcn_readfirstlane(t.col0);
+  t.g0 = __builtin_amdgcn_readfirstlane(t.g0);
+  t.gn = __builtin_amdgcn_readfirstlane(t.gn);
+}
+
+// Tile number `step` of this block, or false past the end of its list.  Blocks
+// go to the XCDs round-robin by index; XCD x takes the x-th eighth of the tile
+// list, and its blocks take that run in turn, so that tiles running side by
+// side share operands in the XCD's L2.  Ragged groups: every wave scans the
+// group sizes (four per lane).
 template <bool WG, int BM, int BN>
-__device__ __forceinline__ bool mm_find_tile(const MatmulArgs& p, int lane, MmTile& t) {
+__device__ __forceinline__ bool mm_find_tile(const MatmulArgs& p, int lane, int step, MmTile& t) {
   const int NT = ceil_div(p.n, BN);
   const bool ragged = !WG && p.offsets != nullptr;
   long long total;
@@ -288,7 +321,7 @@ __device__ __forceinline__ bool mm_find_tile(const MatmulArgs& p, int lane, MmTi
     total = (long long)RTd * NT * p.splits * (WG ? p.E : 1);
   }
   const int x = blockIdx.x & 7;
-  const long long idx = (total * x >> 3) + (blockIdx.x >> 3);
+  const long long idx = (total * x >> 3) + (blockIdx.x >> 3) + (long long)step * (gridDim.x >> 3);
   if (idx >= (total * (x + 1) >> 3)) return false;
   int local = (int)idx;
   t.split = 0;
@@ -421,17 +454,51 @@ __device__ __forceinline__ void mm_bias8(const MatmulArgs& p, int col, float (&b
 
 // -------------------------------------------------------------- the kernel
 
+// The kernel's arguments, read again from the kernarg segment at each use of
+// this function, and the lane index, computed again: what the tile loop could
+// otherwise hoist out of itself (arguments, lane offsets) took some 60
+// registers for the whole kernel and spilled.
+__device__ __forceinline__ MatmulArgs mm_args() {
+#ifdef __HIP_DEVICE_COMPILE__
+  typedef const __attribute__((address_space(4))) MatmulArgs* ArgsPtr;
+  uint64_t a = reinterpret_cast<uint64_t>(__builtin_amdgcn_kernarg_segment_ptr());
+  asm volatile("" : "+s"(a));
+  return *reinterpret_cast<ArgsPtr>(a);
+#else
+  return MatmulArgs{};
+#endif
+}
+__device__ __forceinline__ int mm_lane(int lane) {
+  asm volatile("" : "+v"(lane));
+  return lane;
+}
+
+// Order of one step's instructions: G rounds of R / G LDS reads, M / G matrix
+// instructions and V / G vector loads, so that neither pipe waits for the
+// other's whole batch.
+template <int R, int M, int V, int G, int I = 0>
+__device__ __forceinline__ void mm_order() {
+  if constexpr (I < G) {
+    constexpr int r = R * (I + 1) / G - R * I / G, m = M * (I + 1) / G - M * I / G, v = V * (I + 1) / G - V * I / G;
+    if constexpr (r > 0) __builtin_amdgcn_sched_group_barrier(0x100, r, 0);
+    if constexpr (m > 0) __builtin_amdgcn_sched_group_barrier(0x008, m, 0);
+    if constexpr (v > 0) __builtin_amdgcn_sched_group_barrier(0x020, v, 0);
+    mm_order<R, M, V, G, I + 1>();
+  }
+}
+
 #define MM_WAIT_VM(N) __builtin_amdgcn_s_waitcnt(((N) & 15) | (((N) >> 4) << 14) | 0x0F70)
 
-// One BM x BN output tile per block: WM x WN waves of (32 FM) x 64.  AKC /
+// BM x BN output tiles: WM x WN waves of (32 FM) x (16 FN).  AKC /
 // BKC: how each operand is stored.  A is the operand of the output's rows, B
 // that of its columns; the MFMA takes B first, so a lane ends with one output
 // row and runs of four consecutive columns.
 template <bool F16, bool AKC, bool BKC, int BM, int BN, int WM, int WN, bool ALIGNED>
-__global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 ? 1 : 2) void matmul_tile_kernel(MatmulArgs p) {
+__global__ __launch_bounds__(64 * WM * WN, BM * BN > 128 * 128 ? 1 : 2) void matmul_tile_kernel(MatmulArgs) {
   constexpr int NW = WM * WN;
-  constexpr int FM = BM / (32 * WM);
-  static_assert(BN == 64 * WN, "a wave covers 64 columns");
+  constexpr int FM = BM / (32 * WM);              // a wave's 32-row blocks
+  constexpr int FN = BN / (16 * WN);              // and 16-column blocks
+  static_assert(FM <= 4 && FN % 4 == 0, "a wave covers whole runs of 64 columns");
   constexpr bool WG = !AKC;                       // weight grad: the contraction runs over rows
   constexpr int STA = BM * kMmK, STB = BN * kMmK;
   // Every buffer an array of its own, so that the compiler knows that loads
@@ -445,112 +512,142 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 ? 1 : 2) void matmul_til
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
   MmTile t;
-  if (!mm_find_tile<WG, BM, BN>(p, lane, t)) return;
-
-  // contraction range of this tile, as whole stages of the slice
-  int kbeg = 0, kend = WG ? t.gn : p.k;
-  if (p.splits > 1) {
-    const int per = ceil_div(ceil_div(kend, kMmK), p.splits) * kMmK;
-    kbeg = min(t.split * per, kend);
-    kend = min(kbeg + per, kend) - kbeg;
-  }
-  const int KT = max(1, ceil_div(kend, kMmK));
+  if (!mm_find_tile<WG, BM, BN>(mm_args(), lane, 0, t)) return;
+  mm_scalar(t);
 
   MmOperand<AKC, BM, NW, ALIGNED> la;
   MmOperand<BKC, BN, NW, ALIGNED> lb;
-  if constexpr (AKC)
-    la.init(p.a + (int64_t)(t.g0 + t.row0) * p.lda + kbeg, p.lda, t.nrows, wave, lane);
-  else
-    la.init(p.a + (int64_t)(t.g0 + kbeg) * p.lda + t.row0, p.lda, p.m - t.row0, wave, lane);
-  const uint16_t* bp = WG ? p.b + (int64_t)t.g0 * p.ldb : p.b + (int64_t)t.e * p.b_group;
-  if constexpr (BKC) lb.init(bp + (int64_t)t.col0 * p.ldb + kbeg, p.ldb, p.n - t.col0, wave, lane);
-  else lb.init(bp + (int64_t)kbeg * p.ldb + t.col0, p.ldb, p.n - t.col0, wave, lane);
-  constexpr int BI = MmOperand<BKC, BN, NW, ALIGNED>::NI;
+  constexpr int AI = MmOperand<AKC, BM, NW, ALIGNED>::NI, BI = MmOperand<BKC, BN, NW, ALIGNED>::NI;
+  constexpr int B2 = (BI + 2) / 3, B3 = (2 * BI + 2) / 3;
+  int kend, KT;                                   // the tile's contraction, and its stages
+  // a tile's operands, and its first loads: columns of stages 0 and 1, rows of
+  // stage 0, in the buffers that the stage loop starts from
+  auto start = [&](const MmTile& q) __attribute__((always_inline)) {
+    const MatmulArgs p = mm_args();
+    const int lane = mm_lane(tid & 63);
+    int kbeg = 0;
+    kend = WG ? q.gn : p.k;
+    if (p.splits > 1) {                           // whole stages to a slice
+      const int per = ceil_div(ceil_div(kend, kMmK), p.splits) * kMmK;
+      kbeg = min(q.split * per, kend);
+      kend = min(kbeg + per, kend) - kbeg;
+    }
+    KT = max(1, ceil_div(kend, kMmK));
+    if constexpr (AKC)
+      la.init(p.a + (int64_t)(q.g0 + q.row0) * p.lda + kbeg, p.lda, q.nrows, wave, lane);
+    else
+      la.init(p.a + (int64_t)(q.g0 + kbeg) * p.lda + q.row0, p.lda, p.m - q.row0, wave, lane);
+    const uint16_t* bp = WG ? p.b + (int64_t)q.g0 * p.ldb : p.b + (int64_t)q.e * p.b_group;
+    if constexpr (BKC) lb.init(bp + (int64_t)q.col0 * p.ldb + kbeg, p.ldb, p.n - q.col0, wave, lane);
+    else lb.init(bp + (int64_t)kbeg * p.ldb + q.col0, p.ldb, p.n - q.col0, wave, lane);
+    lb.template loads<0, BI>(sb0, 0, kend);
+    la.template loads<0, AI>(sa0, 0, kend);
+    lb.template loads<0, BI>(sb1, 1, kend);
+    if constexpr (!ALIGNED) {
+      u32x4_t va[AI], vb[BI];
+      la.fetch(va, 0, kend, lane);
+      lb.fetch(vb, 0, kend, lane);
+      la.put(va, sa0, lane);
+      lb.put(vb, sb0, lane);
+      lb.fetch(vb, 1, kend, lane);
+      lb.put(vb, sb1, lane);
+    }
+  };
+  start(t);
 
-  MmFrag<AKC, BM, FM> ra;
-  MmFrag<BKC, BN, 2> rb;
+  MmFrag<AKC, BM> ra;
+  MmFrag<BKC, BN> rb;
   ra.init(wm * 32 * FM, lane);
-  rb.init(wn * 64, lane);
+  rb.init(wn * 16 * FN, lane);
+
+  for (int step = 1;; ++step) {
+  MmTile tn;
+  const bool more = __builtin_amdgcn_readfirstlane(mm_find_tile<WG, BM, BN>(mm_args(), mm_lane(lane), step, tn));
+  mm_scalar(tn);
 
   // NBLK: this wave's 32-row blocks with live rows; the others are neither
   // multiplied nor stored.  Every wave issues its loads and meets every barrier.
   auto body = [&](auto nblk_c) __attribute__((always_inline)) {
     constexpr int NBLK = decltype(nblk_c)::value;
-    constexpr int NA = NBLK > 0 ? NBLK : 1;
-    f32x16_t acc[NA][2];
+    constexpr int NF = 2 * NBLK;                  // live 16-row blocks
+    constexpr int FH = FM;                        // of 2 FM: the first and the second half of a step
+    constexpr int N1 = NF < FH ? NF : FH, N2 = NF - N1;
+    constexpr int NA = NF > 0 ? NF : 1;
+    f32x4_t acc[NA][FN];
 #pragma unroll
     for (int i = 0; i < NA; ++i)
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.f;
-    u32x4_t fa[NA], fb[2], ga[NA], gb[2];
+      for (int j = 0; j < FN; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    // row fragments of two half steps, column fragments of two steps
+    u32x4_t fa[FH], ga[FH], fb[2][FN];
+    u32x4_t va[AI], vb[BI];                       // !ALIGNED: the stages under way
 
-#define MM_FRAG1(FA, I_, ABUF, S_) if constexpr (NBLK > (I_)) FA[(I_) < NA ? (I_) : 0] = ra.template get<S_, I_>(ABUF);
-#define MM_FRAG(FA, FB, ABUF, BBUF, S_)                                        \
-  if constexpr (NBLK > 0) {                                                    \
-    MM_FRAG1(FA, 0, ABUF, S_) MM_FRAG1(FA, 1, ABUF, S_)                        \
-    MM_FRAG1(FA, 2, ABUF, S_) MM_FRAG1(FA, 3, ABUF, S_)                        \
-    FB[0] = rb.template get<S_, 0>(BBUF);                                      \
-    FB[1] = rb.template get<S_, 1>(BBUF);                                      \
+#define MM_FA1(F_, H_, S_, ABUF, I_)                                           \
+  if constexpr ((I_) < ((H_) ? N2 : N1)) F_[(I_) < FH ? (I_) : 0] = ra.template get<S_, (H_) * FH + ((I_) < FH ? (I_) : 0)>(ABUF);
+#define MM_FA(F_, H_, S_, ABUF)                                                \
+  MM_FA1(F_, H_, S_, ABUF, 0) MM_FA1(F_, H_, S_, ABUF, 1) MM_FA1(F_, H_, S_, ABUF, 2) MM_FA1(F_, H_, S_, ABUF, 3)
+#define MM_FB1(S_, I_, BBUF)                                                   \
+  if constexpr (NF > 0 && (I_) < FN) fb[S_][(I_) < FN ? (I_) : 0] = rb.template get<S_, (I_) < FN ? (I_) : 0>(BBUF);
+// half H_ of the column fragments of step S_
+#define MM_FB(S_, H_, BBUF)                                                    \
+  MM_FB1(S_, (H_) * (FN / 2), BBUF) MM_FB1(S_, (H_) * (FN / 2) + 1, BBUF)      \
+  if constexpr (FN > 4) {                                                      \
+    MM_FB1(S_, (H_) * (FN / 2) + 2, BBUF) MM_FB1(S_, (H_) * (FN / 2) + 3, BBUF) \
   }
-#define MM_MMA(FA, FB)                                                         \
-  _Pragma("unroll") for (int i = 0; i < NBLK; ++i)                             \
-      _Pragma("unroll") for (int j = 0; j < 2; ++j) acc[i][j] = mm_mfma<F16>(FB[j], FA[i], acc[i][j]);
-// One step: the next step's fragment reads, then this step's products, then a
-// load of the column operand; nothing moves past the end of the group.
-#define MM_ORDER(MMA_, VM_)                                                    \
-  if constexpr (NBLK > 0 && ALIGNED) {                                         \
-    __builtin_amdgcn_sched_group_barrier(0x100, NBLK * decltype(ra)::kReads + 2 * decltype(rb)::kReads, 0); \
-    if constexpr (MMA_) __builtin_amdgcn_sched_group_barrier(0x008, 2 * NBLK, 0); \
-  }                                                                            \
-  if constexpr ((VM_) && ALIGNED) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0); \
+// Products in snake order: from one to the next only one operand changes,
+// which costs the matrix pipe less power, and power is what bounds its clock.
+#define MM_MMA(F_, H_, S_)                                                     \
+  _Pragma("unroll") for (int i = 0; i < ((H_) ? N2 : N1); ++i)                 \
+      _Pragma("unroll") for (int jj = 0; jj < FN; ++jj) {                      \
+        const int j = (i & 1) ? FN - 1 - jj : jj;                              \
+        f32x4_t& c_ = acc[(H_) * FH + i < NA ? (H_) * FH + i : 0][j];          \
+        c_ = mm_mfma<F16>(fb[S_][j], F_[i], c_);                               \
+      }
+// End of one half step (RA_ / RB_ fragments read, M_ rows of products, V_
+// loads): nothing moves past it.
+#define MM_ORDER(RA_, RB_, M_, V_)                                             \
+  if constexpr (ALIGNED && NF > 0)                                             \
+    mm_order<(RA_) * decltype(ra)::kReads + (RB_) * decltype(rb)::kReads, (M_) * FN, (V_), 4>();   \
   __builtin_amdgcn_sched_barrier(0);
-#define MM_LOAD_A(BUF, KT_)                                                    \
-  la.template load<0>(BUF, KT_, kend, lane); la.template load<1>(BUF, KT_, kend, lane); \
-  la.template load<2>(BUF, KT_, kend, lane); la.template load<3>(BUF, KT_, kend, lane);
 // Stage KT_: this wave's reads of the last stage and its loads of this one
 // are complete (the column operand of the next stage, issued last, may stay in
-// flight), the barrier publishes them; then the rows of the next stage start
-// into a buffer that every wave has finished reading, and the four 16-wide
-// steps run, pipelined by one across the barrier.
+// flight), the barrier publishes them; then come two 32-wide steps of two
+// halves (of the wave's rows), pipelined by one half across the barrier, with
+// the loads between their products: the rows of the next stage, into a buffer
+// that every wave has finished reading, and the columns of the one after it.
 #define MM_STAGE(ABUF, NABUF, BBUF, NBBUF, KT_, FIRST)                         \
   {                                                                            \
     __builtin_amdgcn_s_waitcnt(0xC07F);                                        \
     if constexpr (ALIGNED) MM_WAIT_VM(BI);                                     \
     __builtin_amdgcn_s_barrier();                                              \
-    MM_LOAD_A(NABUF, (KT_) + 1)                                                \
     __builtin_amdgcn_sched_barrier(0);                                         \
-    MM_FRAG(ga, gb, ABUF, BBUF, 0)                                             \
-    if constexpr (!(FIRST)) { MM_MMA(fa, fb) }                                 \
-    lb.template load<0>(NBBUF, (KT_) + 2, kend, lane);                         \
-    MM_ORDER(!(FIRST), BI > 0)                                                 \
-    MM_FRAG(fa, fb, ABUF, BBUF, 1)                                             \
-    MM_MMA(ga, gb)                                                             \
-    lb.template load<1>(NBBUF, (KT_) + 2, kend, lane);                         \
-    MM_ORDER(true, BI > 1)                                                     \
-    MM_FRAG(ga, gb, ABUF, BBUF, 2)                                             \
-    MM_MMA(fa, fb)                                                             \
-    lb.template load<2>(NBBUF, (KT_) + 2, kend, lane);                         \
-    MM_ORDER(true, BI > 2)                                                     \
-    MM_FRAG(fa, fb, ABUF, BBUF, 3)                                             \
-    MM_MMA(ga, gb)                                                             \
-    lb.template load<3>(NBBUF, (KT_) + 2, kend, lane);                         \
-    MM_ORDER(true, BI > 3)                                                     \
+    la.template loads<0, AI>(NABUF, (KT_) + 1, kend);                          \
+    if constexpr (!ALIGNED) {                                                  \
+      la.fetch(va, (KT_) + 1, kend, lane);                                     \
+      lb.fetch(vb, (KT_) + 2, kend, lane);                                     \
+    }                                                                          \
+    MM_FB(0, 0, BBUF) MM_FA(ga, 0, 0, ABUF) MM_FB(0, 1, BBUF)                  \
+    if constexpr (!(FIRST)) { MM_MMA(fa, 1, 1) }                               \
+    MM_ORDER(N1, FN, (FIRST) ? 0 : N2, AI)                                     \
+    MM_FA(fa, 1, 0, ABUF) MM_FB(1, 0, BBUF)                                    \
+    MM_MMA(ga, 0, 0)                                                           \
+    lb.template loads<0, B2>(NBBUF, (KT_) + 2, kend);                    \
+    MM_ORDER(N2, FN / 2, N1, B2)                                                    \
+    MM_FA(ga, 0, 1, ABUF) MM_FB(1, 1, BBUF)                                    \
+    MM_MMA(fa, 1, 0)                                                           \
+    lb.template loads<B2, B3>(NBBUF, (KT_) + 2, kend);                   \
+    MM_ORDER(N1, FN / 2, N2, B3 - B2)                                               \
+    MM_FA(fa, 1, 1, ABUF)                                                      \
+    MM_MMA(ga, 0, 1)                                                           \
+    lb.template loads<B3, BI>(NBBUF, (KT_) + 2, kend);                   \
+    MM_ORDER(N2, 0, N1, BI - B3)                                               \
+    la.put(va, NABUF, lane);                                                   \
+    lb.put(vb, NBBUF, lane);                                                   \
   }
 #define MM_A(I) ((I) % 2 == 0 ? sa0 : sa1)
 #define MM_B(I) ((I) % 3 == 0 ? sb0 : (I) % 3 == 1 ? sb1 : sb2)
 #define MM_U(U, KT_, FIRST) MM_STAGE(MM_A(U), MM_A((U) + 1), MM_B(U), MM_B((U) + 2), KT_, FIRST)
 
-    lb.template load<0>(sb0, 0, kend, lane);
-    lb.template load<1>(sb0, 0, kend, lane);
-    lb.template load<2>(sb0, 0, kend, lane);
-    lb.template load<3>(sb0, 0, kend, lane);
-    MM_LOAD_A(sa0, 0)
-    lb.template load<0>(sb1, 1, kend, lane);
-    lb.template load<1>(sb1, 1, kend, lane);
-    lb.template load<2>(sb1, 1, kend, lane);
-    lb.template load<3>(sb1, 1, kend, lane);
     MM_U(0, 0, true)
     int kt = 1;
     for (; kt + 5 < KT; kt += 6) {
@@ -566,50 +663,56 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 ? 1 : 2) void matmul_til
     if (kt + 2 < KT) MM_U(3, kt + 2, false)
     if (kt + 3 < KT) MM_U(4, kt + 3, false)
     if (kt + 4 < KT) MM_U(5, kt + 4, false)
-    MM_MMA(fa, fb)
+    MM_MMA(fa, 1, 1)
+    // Loads past the last stage (zeros) still target the buffers of stages 0
+    // and 1 of the next tile and the staging slots: they land first.
     MM_WAIT_VM(0);
     mm_lds_barrier();
+    if (more) start(tn);                          // in flight during the epilogue
 
     // Epilogue: each wave stages one 32 x 64 fp32 block at a time (8 KB of the
-    // row buffers, free now) and reads it back as row segments of eight
+    // two buffers that the next tile's first loads leave free) and reads it back as row segments of eight
     // columns, so that loads and stores cover whole 128-byte segments.  Chunk
     // c (four columns) of row r sits at c ^ (r & 15): no bank conflicts.
-    static_assert(STA * 2 * 2 >= NW * 8192, "staging slots in the row buffers");
-    float* blk = reinterpret_cast<float*>(wave < NW / 2 ? sa0 : sa1) + (wave % (NW / 2)) * 2048;
-    const int fr = lane & 31, fg = lane >> 5, ch = lane & 7;
-    const int col = t.col0 + wn * 64 + ch * 8;
-    float bias[8];
-    mm_bias8<F16>(p, col, bias);
+    const MatmulArgs p = mm_args();
+    const int lane = mm_lane(tid & 63);
+    static_assert(STA * 2 >= NW * 4096 && STB * 2 >= NW * 4096, "half of the waves' staging slots in each");
+    float* blk = reinterpret_cast<float*>(wave < NW / 2 ? sa1 : sb2) + (wave % (NW / 2)) * 2048;
+    const int fr = lane & 15, fg = lane >> 4, ch = lane & 7;
     const int64_t out_off =
         WG ? ((int64_t)t.e * p.splits + t.split) * p.out_group : (int64_t)t.split * p.out_group;
     const int64_t row_base = (int64_t)(WG ? 0 : t.g0) + t.row0;
 #pragma unroll
-    for (int i = 0; i < FM; ++i) {
-      if (i >= NBLK) break;
+    for (int h = 0; h < FN / 4; ++h) {
+      const int col = t.col0 + wn * 16 * FN + 64 * h + ch * 8;
+      float bias[8];
+      mm_bias8<F16>(p, col, bias);
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int i = 0; i < FM; ++i) {
+        if (i >= NBLK) break;
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const f32x16_t& a0 = acc[i < NA ? i : 0][j];
-          const int c = 8 * j + 2 * b + fg;
-          *reinterpret_cast<f32x4_t*>(blk + fr * 64 + ((c ^ (fr & 15)) << 2)) =
-              f32x4_t{a0[4 * b], a0[4 * b + 1], a0[4 * b + 2], a0[4 * b + 3]};
-        }
-      __builtin_amdgcn_wave_barrier();            // a wave's LDS operations complete in order
-      if (col < p.n) {
+        for (int a = 0; a < 2; ++a)
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          const int r = 8 * s + (lane >> 3);
-          const int row = wm * 32 * FM + 32 * i + r;
-          const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(blk + r * 64 + (((2 * ch) ^ (r & 15)) << 2));
-          const f32x4_t hi = *reinterpret_cast<const f32x4_t*>(blk + r * 64 + (((2 * ch + 1) ^ (r & 15)) << 2));
-          if (row < t.nrows) {
-            float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-            mm_finish8<F16>(p, v, bias, row_base + row, col, out_off);
+          for (int j = 0; j < 4; ++j) {
+            const int r = 16 * a + fr, c = 4 * j + fg;
+            *reinterpret_cast<f32x4_t*>(blk + r * 64 + ((c ^ fr) << 2)) = acc[2 * i + a < NA ? 2 * i + a : 0][4 * h + j];
+          }
+        __builtin_amdgcn_wave_barrier();          // a wave's LDS operations complete in order
+        if (col < p.n) {
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            const int r = 8 * s + (lane >> 3);
+            const int row = wm * 32 * FM + 32 * i + r;
+            const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(blk + r * 64 + (((2 * ch) ^ (r & 15)) << 2));
+            const f32x4_t hi = *reinterpret_cast<const f32x4_t*>(blk + r * 64 + (((2 * ch + 1) ^ (r & 15)) << 2));
+            if (row < t.nrows) {
+              float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+              mm_finish8<F16>(p, v, bias, row_base + row, col, out_off);
+            }
           }
         }
+        __builtin_amdgcn_wave_barrier();
       }
-      __builtin_amdgcn_wave_barrier();
     }
   };
   const int live = t.nrows - wm * 32 * FM;
@@ -624,11 +727,15 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN == 8 ? 1 : 2) void matmul_til
     if (nblk == 2) body(std::integral_constant<int, 2>{});
     else if constexpr (FM >= 4) body(std::integral_constant<int, 3>{});
   }
-#undef MM_FRAG1
-#undef MM_FRAG
+  if (!more) break;
+  t = tn;
+  }
+#undef MM_FA1
+#undef MM_FA
+#undef MM_FB1
+#undef MM_FB
 #undef MM_MMA
 #undef MM_ORDER
-#undef MM_LOAD_A
 #undef MM_STAGE
 #undef MM_A
 #undef MM_B
