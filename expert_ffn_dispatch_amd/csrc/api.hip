@@ -811,7 +811,14 @@ LinearBackwardWs carve_linear_backward(Carver& c, const moe_linear_dims& d) {
   return w;
 }
 
+// Whether a call's shape and strides suit the kernel for a few rows, which
+// needs no workspace.  (Should only its pointers not suit, the tiles run
+// without contraction slices.)
+bool linear_streams(const moe_linear_dims& d) {
+  return d.rows <= 64 && d.in_features % 8 == 0 && d.ld_x % 8 == 0 && d.ld_w % 8 == 0;
+}
 size_t linear_ws_bytes(const moe_linear_dims& d) {
+  if (linear_streams(d)) return 0;
   return align_up(moe::matmul_workspace_bytes(moe::kMmForward, 1, false, d.rows, d.rows, d.out_features, d.in_features));
 }
 size_t grouped_wgrad_ws_bytes(const moe_grouped_dims& d) {
@@ -1228,6 +1235,7 @@ int moe_linear(const moe_linear_dims* dims, const void* x, const void* w, const 
   a.aligned = pieces16(x, d.ld_x, d.in_features) && pieces16(w, d.ld_w, d.in_features);
   a.vec = al16(y) && d.ld_y % 8 == 0 && (residual == nullptr || (al16(residual) && d.ld_residual % 8 == 0)) &&
           (pre == nullptr || (al16(pre) && d.ld_pre % 8 == 0));
+  a.whole = linear_streams(d);
   a.bias = bias;
   a.bias_f32 = d.bias_dtype == MOE_DTYPE_F32;
   a.act = d.act;

@@ -179,6 +179,7 @@ struct MatmulArgs {
   int64_t ldp;
   int aligned;               // a and b take 16-byte loads
   int f16;                   // operands are fp16 (else bf16)
+  int whole;                 // no contraction slices (no workspace for them)
 };
 enum MatmulForm { kMmForward = 0, kMmRowGrad = 1, kMmWeightGrad = 2 };
 // Contraction slices of a call (1: none) and the bytes of their partial sums.
@@ -186,6 +187,10 @@ int matmul_splits(MatmulForm f, int E, bool ragged, int64_t rows, int64_t m, int
 size_t matmul_workspace_bytes(MatmulForm f, int E, bool ragged, int64_t rows, int64_t m, int64_t n, int64_t k);
 // a.splits, out_group and the fp32 partials in ws are set up by the launcher.
 hipError_t launch_matmul(MatmulForm f, MatmulArgs a, void* ws, hipStream_t st);
+// Forward products of a few rows per group (matmul_stream.hip): whether a call
+// is one, and its launch.
+bool matmul_streams(const MatmulArgs& a);
+hipError_t launch_matmul_stream(const MatmulArgs& a, hipStream_t st);
 // The instances of one form (matmul_*.hip).
 hipError_t launch_matmul_forward(const MatmulArgs& a, hipStream_t st);
 hipError_t launch_matmul_row_grad(const MatmulArgs& a, hipStream_t st);

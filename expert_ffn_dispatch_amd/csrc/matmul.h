@@ -286,6 +286,17 @@ __device__ __forceinline__ void mm_scalar(MmTile& t) {
   t.gn = __builtin_amdgcn_readfirstlane(t.gn);
 }
 
+// Row tiles: dealt evenly from 64 rows on, else BM rows at a time.
+template <int BM>
+__device__ __forceinline__ void mm_row_part(int cnt, int RT, int rt, int& off, int& n) {
+  if constexpr (BM >= 64) {
+    mm_row_tile(cnt, RT, rt, off, n);
+  } else {
+    off = rt * BM;
+    n = min(cnt - off, BM);
+  }
+}
+
 // Tile number `step` of this block, or false past the end of its list.  Blocks
 // go to the XCDs round-robin by index; XCD x takes the x-th eighth of the tile
 // list, and its blocks take that run in turn, so that tiles running side by
@@ -351,7 +362,7 @@ __device__ __forceinline__ bool mm_find_tile(const MatmulArgs& p, int lane, int 
     const int RT = ceil_div(cnt, BM);
     int rt, ct;
     mm_grid_pos(local, RT, NT, rt, ct);
-    mm_row_tile(cnt, RT, rt, t.row0, t.nrows);
+    mm_row_part<BM>(cnt, RT, rt, t.row0, t.nrows);
     t.col0 = ct * BN;
     return true;
   }
@@ -371,7 +382,7 @@ __device__ __forceinline__ bool mm_find_tile(const MatmulArgs& p, int lane, int 
   }
   int rt, ct;
   mm_grid_pos(local, RTd, NT, rt, ct);
-  mm_row_tile(p.m, RTd, rt, t.row0, t.nrows);
+  mm_row_part<BM>(p.m, RTd, rt, t.row0, t.nrows);
   t.col0 = ct * BN;
   return true;
 }
@@ -670,14 +681,15 @@ __global__ __launch_bounds__(64 * WM * WN, BM * BN > 128 * 128 ? 1 : 2) void mat
     mm_lds_barrier();
     if (more) start(tn);                          // in flight during the epilogue
 
-    // Epilogue: each wave stages one 32 x 64 fp32 block at a time (8 KB of the
-    // two buffers that the next tile's first loads leave free) and reads it back as row segments of eight
-    // columns, so that loads and stores cover whole 128-byte segments.  Chunk
-    // c (four columns) of row r sits at c ^ (r & 15): no bank conflicts.
+    // Epilogue: each wave stages 16 rows x 64 columns of fp32 at a time (4 KB of
+    // the buffer that the next tile's first loads leave alone) and reads them
+    // back as row segments of eight columns, so that loads and stores cover
+    // whole 128-byte segments.  Chunk c (four columns) of row r sits at c ^ r:
+    // no bank conflicts.
     const MatmulArgs p = mm_args();
     const int lane = mm_lane(tid & 63);
-    static_assert(STA * 2 >= NW * 4096 && STB * 2 >= NW * 4096, "half of the waves' staging slots in each");
-    float* blk = reinterpret_cast<float*>(wave < NW / 2 ? sa1 : sb2) + (wave % (NW / 2)) * 2048;
+    static_assert(STB * 2 >= NW * 4096, "the waves' staging slots");
+    float* blk = reinterpret_cast<float*>(sb2) + wave * 1024;
     const int fr = lane & 15, fg = lane >> 4, ch = lane & 7;
     const int64_t out_off =
         WG ? ((int64_t)t.e * p.splits + t.split) * p.out_group : (int64_t)t.split * p.out_group;
@@ -688,23 +700,19 @@ __global__ __launch_bounds__(64 * WM * WN, BM * BN > 128 * 128 ? 1 : 2) void mat
       float bias[8];
       mm_bias8<F16>(p, col, bias);
 #pragma unroll
-      for (int i = 0; i < FM; ++i) {
-        if (i >= NBLK) break;
+      for (int i = 0; i < 2 * FM; ++i) {
+        if (i >= NF) break;
 #pragma unroll
-        for (int a = 0; a < 2; ++a)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int r = 16 * a + fr, c = 4 * j + fg;
-            *reinterpret_cast<f32x4_t*>(blk + r * 64 + ((c ^ fr) << 2)) = acc[2 * i + a < NA ? 2 * i + a : 0][4 * h + j];
-          }
+        for (int j = 0; j < 4; ++j)
+          *reinterpret_cast<f32x4_t*>(blk + fr * 64 + (((4 * j + fg) ^ fr) << 2)) = acc[i < NA ? i : 0][4 * h + j];
         __builtin_amdgcn_wave_barrier();          // a wave's LDS operations complete in order
         if (col < p.n) {
 #pragma unroll
-          for (int s = 0; s < 4; ++s) {
+          for (int s = 0; s < 2; ++s) {
             const int r = 8 * s + (lane >> 3);
-            const int row = wm * 32 * FM + 32 * i + r;
-            const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(blk + r * 64 + (((2 * ch) ^ (r & 15)) << 2));
-            const f32x4_t hi = *reinterpret_cast<const f32x4_t*>(blk + r * 64 + (((2 * ch + 1) ^ (r & 15)) << 2));
+            const int row = wm * 32 * FM + 16 * i + r;
+            const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(blk + r * 64 + (((2 * ch) ^ r) << 2));
+            const f32x4_t hi = *reinterpret_cast<const f32x4_t*>(blk + r * 64 + (((2 * ch + 1) ^ r) << 2));
             if (row < t.nrows) {
               float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
               mm_finish8<F16>(p, v, bias, row_base + row, col, out_off);

@@ -190,7 +190,11 @@ size_t matmul_workspace_bytes(MatmulForm f, int E, bool ragged, int64_t rows, in
 
 hipError_t launch_matmul(MatmulForm f, MatmulArgs a, void* ws, hipStream_t st) {
   if (a.m == 0 || (f != kMmWeightGrad && a.rows == 0)) return hipSuccess;
-  const int64_t s = matmul_splits(f, a.E, a.offsets != nullptr, a.rows, a.m, a.n, a.k);
+  if (f == kMmForward && matmul_streams(a)) {
+    a.splits = 1;
+    return launch_matmul_stream(a, st);
+  }
+  const int64_t s = a.whole ? 1 : matmul_splits(f, a.E, a.offsets != nullptr, a.rows, a.m, a.n, a.k);
   auto launch = [&](const MatmulArgs& q) {
     return f == kMmForward ? launch_matmul_forward(q, st)
            : f == kMmRowGrad ? launch_matmul_row_grad(q, st)

@@ -1,0 +1,188 @@
+// Forward products of a few rows (decode): y[r][c] = sum_k x[r][k] W[c][k] for
+// at most 16 RB rows of a group at a time, W read once from HBM.
+//
+// A block of NW waves owns 16 NC output columns; wave w takes every NW-th
+// 128-wide chunk of the contraction, so that the block reads 256 NW-byte runs
+// of its weight rows.  A chunk (16 NC rows x 256 bytes) goes straight into one
+// of two slots of the wave's own LDS, four rows to a load, and comes back as
+// MFMA fragments; no wave waits for another until the partial sums are added
+// in LDS, in wave order.  The rows of x come as fragments from L2, once per
+// block: the wider the block, the fewer of those.
+// Bound by the weights' bytes.
+#include "matmul.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kStK = 128;                         // contraction per chunk
+
+template <bool F16>
+__device__ __forceinline__ void finish1(const MatmulArgs& p, float v, int64_t row, int col) {
+  if (p.bias != nullptr)
+    v += p.bias_f32 ? static_cast<const float*>(p.bias)[col] : mm_load1<F16>(static_cast<const uint16_t*>(p.bias)[col]);
+  if (p.pre != nullptr) p.pre[row * p.ldp + col] = mm_store1<F16>(v);
+  v = mm_act(v, p.act);
+  if (p.residual != nullptr) v += mm_load1<F16>(p.residual[row * p.ldr + col]);
+  static_cast<uint16_t*>(p.out)[row * p.ldo + col] = mm_store1<F16>(v);
+}
+
+template <bool F16, int RB, int NC, int NW>
+__global__ __launch_bounds__(64 * NW, RB * NC == 1 ? 4 : NW / 4) void matmul_stream_kernel(MatmulArgs p) {
+  // an array per slot: loads into one do not hold up reads of the other
+  constexpr int kSlot = 16 * NC * kStK;
+  __shared__ __align__(16) uint16_t s0[NW * kSlot];
+  __shared__ __align__(16) uint16_t s1[NW * kSlot];
+  static_assert(RB * NC * 256 * 4 <= kSlot * 2, "a wave's sums fit its slot");
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int fr = lane & 15, fg = lane >> 4;
+  uint16_t* w0 = s0 + wave * kSlot;
+  uint16_t* w1 = s1 + wave * kSlot;
+  MmTile t;
+  for (int step = 0; mm_find_tile<false, 16 * RB, 16 * NC>(p, lane, step, t); ++step) {
+    mm_scalar(t);
+    const int chunks = ceil_div(p.k, kStK);
+    const int n = wave < chunks ? (chunks - wave + NW - 1) / NW : 0;   // this wave's
+    const __amdgpu_buffer_rsrc_t wr = mm_rsrc(p.b + (int64_t)t.e * p.b_group + (int64_t)t.col0 * p.ldb);
+    const __amdgpu_buffer_rsrc_t xr = mm_rsrc(p.a + (int64_t)(t.g0 + t.row0) * p.lda);
+    // weight rows 4 i + (lane >> 4) of load i, 16-byte piece (lane & 15) ^ (row & 15)
+    uint32_t wo[4 * NC];
+    int wk[4];
+#pragma unroll
+    for (int i = 0; i < 4 * NC; ++i) {
+      const int r = 4 * i + fg;
+      wk[i & 3] = (fr ^ (r & 15)) * 8;
+      wo[i] = t.col0 + r < p.n ? (uint32_t)r * (uint32_t)(2 * p.ldb) + (uint32_t)(wk[i & 3] * 2) : kMmOut;
+    }
+    uint32_t xo[RB];
+#pragma unroll
+    for (int b = 0; b < RB; ++b)
+      xo[b] = 16 * b + fr < t.nrows ? (uint32_t)(16 * b + fr) * (uint32_t)(2 * p.lda) + (uint32_t)(fg * 16) : kMmOut;
+    f32x4_t acc[NC][RB];
+#pragma unroll
+    for (int j = 0; j < NC; ++j)
+#pragma unroll
+      for (int b = 0; b < RB; ++b) acc[j][b] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    // chunk c of this wave starts at k = 128 (wave + 8 c); past the last all
+    // lanes take zeros
+    auto load_w = [&](uint16_t* dst, int c) __attribute__((always_inline)) {
+      const int k0 = (wave + NW * c) * kStK;
+#pragma unroll
+      for (int i = 0; i < 4 * NC; ++i)
+        mm_dma16(wr, k0 + wk[i & 3] < p.k ? wo[i] : kMmOut, (uint32_t)(2 * k0), dst + 512 * i);
+    };
+    auto load_x = [&](u32x4_t (&x)[RB][4], int c) __attribute__((always_inline)) {
+      const int k0 = (wave + NW * c) * kStK;
+#pragma unroll
+      for (int b = 0; b < RB; ++b)
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+          x[b][s] = __builtin_bit_cast(
+              u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                           xr, k0 + 32 * s + 8 * fg < p.k ? xo[b] + 64 * s : kMmOut, (uint32_t)(2 * k0), 0));
+    };
+    auto chunk = [&](const uint16_t* src, const u32x4_t (&x)[RB][4]) __attribute__((always_inline)) {
+#pragma unroll
+      for (int j = 0; j < NC; ++j) {
+        u32x4_t f[4];
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+          f[s] = *reinterpret_cast<const u32x4_t*>(src + (16 * j + fr) * kStK + (((4 * s + fg) ^ fr) << 3));
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+          for (int b = 0; b < RB; ++b) acc[j][b] = mm_mfma<F16>(f[s], x[b][s], acc[j][b]);
+      }
+    };
+    // Two chunks of weights and two of rows under way.  A slot is loaded again
+    // once its reads are complete; the wait leaves the younger chunk in flight.
+    u32x4_t xa[RB][4], xb[RB][4];
+    load_w(w0, 0);
+    load_x(xa, 0);
+    load_w(w1, 1);
+    constexpr int kYounger = 4 * NC + 4 * RB;
+    for (int c = 0; c < n; c += 2) {
+      load_x(xb, c + 1);
+      __builtin_amdgcn_s_waitcnt((kYounger & 15) | ((kYounger >> 4) << 14) | 0x0F70);
+      __builtin_amdgcn_sched_barrier(0);
+      chunk(w0, xa);
+      __builtin_amdgcn_s_waitcnt(0xC07F);
+      __builtin_amdgcn_sched_barrier(0);
+      load_w(w0, c + 2);
+      if (c + 1 >= n) break;
+      load_x(xa, c + 2);
+      __builtin_amdgcn_s_waitcnt((kYounger & 15) | ((kYounger >> 4) << 14) | 0x0F70);
+      __builtin_amdgcn_sched_barrier(0);
+      chunk(w1, xb);
+      __builtin_amdgcn_s_waitcnt(0xC07F);
+      __builtin_amdgcn_sched_barrier(0);
+      load_w(w1, c + 3);
+    }
+    __builtin_amdgcn_s_waitcnt(0x0F70);           // loads past the last chunk land
+    // partial sums [wave][16 RB rows][16 NC columns] over the slots; column c
+    // of row r at c ^ 4 (r & 3), for the banks
+    float* part = reinterpret_cast<float*>(w0);
+#pragma unroll
+    for (int b = 0; b < RB; ++b)
+#pragma unroll
+      for (int j = 0; j < NC; ++j)
+        *reinterpret_cast<f32x4_t*>(part + (16 * b + fr) * 16 * NC + 16 * j + 4 * (fg ^ (fr & 3))) = acc[j][b];
+    __syncthreads();
+    for (int i = tid; i < RB * NC * 256; i += 64 * NW) {
+      const int row = i / (16 * NC), c = i % (16 * NC), col = t.col0 + (c ^ (4 * (row & 3)));
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) v += reinterpret_cast<const float*>(s0 + w * kSlot)[i];
+      if (row < t.nrows && col < p.n) finish1<F16>(p, v, (int64_t)t.g0 + t.row0 + row, col);
+    }
+    __syncthreads();                              // the sums are read before the slots are loaded again
+  }
+}
+
+template <bool F16, int RB, int NC, int NW>
+hipError_t stream_go(const MatmulArgs& a, hipStream_t st) {
+  const long long groups = a.offsets != nullptr ? (a.E < a.rows ? a.E : a.rows) : 1;
+  long long grid = ((long long)a.rows / (16 * RB) + groups) * ceil_div(a.n, 16 * NC);
+  grid = (grid + 7) / 8 * 8;
+  if (grid > (1 << 20)) grid = 1 << 20;
+  hipLaunchKernelGGL((matmul_stream_kernel<F16, RB, NC, NW>), dim3((unsigned)grid), dim3(64 * NW), 0, st, a);
+  return hipGetLastError();
+}
+// Sixteen columns and eight waves, or 32 and four.  Wider blocks read the rows
+// of x half as often; they are taken where half as many blocks still cover the
+// card and x is more than one row block, or where groups share out many rows
+// (dense, us at 1 / 17 / 32 / 48 / 64 rows: 4096 x 4096 10.4 / 11.7 / 14.3 /
+// 18.4 / 22.5 narrow, 11.3 / 13.0 / 15.2 / 18.7 / 23.3 wide; 1024 -> 8192 10.4
+// / 10.3 / 11.5 / 17.1 / 20.0 narrow, 10.7 / 10.8 / 10.7 / 11.5 / 13.6 wide;
+// one row, 6144 -> 16384 36.8 narrow, 38.2 wide; 64 rows over 128 experts of
+// 2048 -> 768 31.9 narrow, 24.2 wide).
+template <bool F16, int RB>
+hipError_t stream_cols(const MatmulArgs& a, hipStream_t st) {
+  const bool wide = a.offsets != nullptr || (RB > 1 && a.n >= 256 * 32);
+  return wide ? stream_go<F16, RB, 2, 4>(a, st) : stream_go<F16, RB, 1, 8>(a, st);
+}
+template <bool F16>
+hipError_t stream_rows(const MatmulArgs& a, hipStream_t st) {
+  if (a.offsets != nullptr || a.rows <= 16) return stream_cols<F16, 1>(a, st);
+  if (a.rows <= 32) return stream_cols<F16, 2>(a, st);
+  if (a.rows <= 48) return stream_cols<F16, 3>(a, st);
+  return stream_cols<F16, 4>(a, st);
+}
+
+}  // namespace
+
+// Dense: up to 64 rows (above, slices of 128 x 128 tiles are as fast: 64 rows of
+// 4096 x 4096 22.5 us against 21.9).  Groups: where few experts have a row at
+// all, up to half as many rows as experts (8 rows over 128 experts of 2048 ->
+// 768 10.0 us against 18.1 by tiles, 64 rows 24.2 against 24.0, 256 rows 52
+// against 50, 1024 rows 86 against 85, 4096 rows 143 against 100).
+bool matmul_streams(const MatmulArgs& a) {
+  if (!a.aligned) return false;
+  return a.offsets != nullptr ? 2 * (long long)a.rows <= a.E : a.rows <= 64;
+}
+
+hipError_t launch_matmul_stream(const MatmulArgs& a, hipStream_t st) {
+  return a.f16 ? stream_rows<true>(a, st) : stream_rows<false>(a, st);
+}
+
+}  // namespace moe

@@ -98,7 +98,7 @@ def test_linear_pointers(lib):
     assert f(r(d), X, W, None, None, Y, Y, None, 0, None) == INV
     assert f(r(d), X, W, None, Z, Y, Z, None, 0, None) == INV
     assert f(r(lin(ld_y=80)), X, W, None, Y, Y, None, None, 0, None) == INV and "stride" in _err(lib)
-    assert f(r(lin(in_features=4096)), X, W, None, None, Y, None, None, 0, None) == WSP
+    assert f(r(lin(rows=100, in_features=4096)), X, W, None, None, Y, None, None, 0, None) == WSP
     assert f(r(lin(rows=0)), None, None, None, None, None, None, None, 0, None) == 0
     big = 1 << 40
     assert b(r(d), X, X, W, Z, Y, None, None, FAKE, big, None) == INV and "pre must be NULL" in _err(lib)
