@@ -418,7 +418,7 @@ def moe_layer_norm(x, gamma=None, beta=None, eps: float = 1e-5, rms: bool = Fals
     pt = _param_type(dt, gamma, beta)
     with _On(dev, stream) as st:
         if y is None:
-            y = torch.empty((rows, cols), dtype=dt, device=dev)
+            y = torch.empty_like(x)
         py, ldy = _mat(y, "y", dev, (dt,), rows, cols)
         mean = torch.empty(rows, dtype=torch.float32, device=dev) if want_stats else None
         rstd = torch.empty(rows, dtype=torch.float32, device=dev) if want_stats else None
@@ -450,7 +450,7 @@ def moe_layer_norm_backward(dy, x, gamma, mean, rstd, rms: bool = False, want_dx
     lib = _lib.load()
     with _On(dev, stream) as st:
         if dx is None and want_dx:
-            dx = torch.empty((rows, cols), dtype=dt, device=dev)
+            dx = torch.empty_like(x)
         po, ldo = _mat(dx, "dx", dev, (dt,), rows, cols) if dx is not None else (None, 0)
         dgamma = torch.empty(cols, dtype=pt, device=dev) if want_params else None
         dbeta = torch.empty(cols, dtype=pt, device=dev) if want_params else None

@@ -391,6 +391,14 @@ __device__ __forceinline__ bool mm_find_tile(const MatmulArgs& p, int lane, int 
 
 // Eight consecutive columns of one output row: bias, activation, residual,
 // stores.  `orow` is the row of out / residual / pre, `col` its first column.
+__device__ __forceinline__ void mm_store16(void* p, u32x4_t v) {
+#ifdef MMV
+  __builtin_nontemporal_store(v, static_cast<u32x4_t*>(p));
+#else
+  *static_cast<u32x4_t*>(p) = v;
+#endif
+}
+
 template <bool F16>
 __device__ __forceinline__ void mm_finish8(const MatmulArgs& p, float (&v)[8], const float (&bias)[8], int64_t orow,
                                            int col, int64_t out_off) {
@@ -403,8 +411,8 @@ __device__ __forceinline__ void mm_finish8(const MatmulArgs& p, float (&v)[8], c
   if (p.pre != nullptr) {
     uint16_t* o = p.pre + orow * p.ldp + col;
     if (vec) {
-      *reinterpret_cast<u32x4_t*>(o) = u32x4_t{mm_pack2<F16>(v[0], v[1]), mm_pack2<F16>(v[2], v[3]),
-                                               mm_pack2<F16>(v[4], v[5]), mm_pack2<F16>(v[6], v[7])};
+      mm_store16(o, u32x4_t{mm_pack2<F16>(v[0], v[1]), mm_pack2<F16>(v[2], v[3]), mm_pack2<F16>(v[4], v[5]),
+                            mm_pack2<F16>(v[6], v[7])});
     } else {
 #pragma unroll
       for (int q = 0; q < 8; ++q)
@@ -432,8 +440,8 @@ __device__ __forceinline__ void mm_finish8(const MatmulArgs& p, float (&v)[8], c
   if (p.out_f32) {
     float* o = static_cast<float*>(p.out) + at;
     if (vec) {
-      *reinterpret_cast<f32x4_t*>(o) = f32x4_t{v[0], v[1], v[2], v[3]};
-      *reinterpret_cast<f32x4_t*>(o + 4) = f32x4_t{v[4], v[5], v[6], v[7]};
+      mm_store16(o, __builtin_bit_cast(u32x4_t, f32x4_t{v[0], v[1], v[2], v[3]}));
+      mm_store16(o + 4, __builtin_bit_cast(u32x4_t, f32x4_t{v[4], v[5], v[6], v[7]}));
     } else {
 #pragma unroll
       for (int q = 0; q < 8; ++q)
@@ -442,8 +450,8 @@ __device__ __forceinline__ void mm_finish8(const MatmulArgs& p, float (&v)[8], c
   } else {
     uint16_t* o = static_cast<uint16_t*>(p.out) + at;
     if (vec) {
-      *reinterpret_cast<u32x4_t*>(o) = u32x4_t{mm_pack2<F16>(v[0], v[1]), mm_pack2<F16>(v[2], v[3]),
-                                               mm_pack2<F16>(v[4], v[5]), mm_pack2<F16>(v[6], v[7])};
+      mm_store16(o, u32x4_t{mm_pack2<F16>(v[0], v[1]), mm_pack2<F16>(v[2], v[3]), mm_pack2<F16>(v[4], v[5]),
+                            mm_pack2<F16>(v[6], v[7])});
     } else {
 #pragma unroll
       for (int q = 0; q < 8; ++q)
