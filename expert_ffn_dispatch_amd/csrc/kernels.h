@@ -161,12 +161,11 @@ struct MatmulArgs {
   void* out;
   int64_t lda, ldb, ldo;
   int64_t b_group;           // forward, row grad: elements from one group's W to the next
-  int64_t out_group;         // elements from one output (weight grad: group and slice; else slice) to the next
+  int64_t out_group;         // weight grad: elements from one group's output to the next
   const int32_t* offsets;    // [E+1] device, or null: one group of all rows
   int E;
   int rows;                  // rows of the grouped operands
   int m, n, k;               // output rows (of one group), output columns, contraction (weight grad: unused)
-  int splits;                // contraction slices (1: none); > 1: out holds fp32 partial sums
   int out_f32;
   int vec;                   // out, residual and pre take 16-byte accesses
   // epilogue (null / kActNone: none): out = act(sum + bias) + residual, pre = sum + bias
@@ -180,12 +179,15 @@ struct MatmulArgs {
   int aligned;               // a and b take 16-byte loads
   int f16;                   // operands are fp16 (else bf16)
   int whole;                 // no contraction slices (no workspace for them)
+  // set by launch_matmul: the plan
+  int big;                   // 256 x 256 tiles (else 128 x 128)
+  int tail;                  // tiles at the end of the list that are cut into
+  int splits;                // slices of the contraction, whose fp32 partial
+  float* parts;              // tiles are here, joined by another launch
 };
 enum MatmulForm { kMmForward = 0, kMmRowGrad = 1, kMmWeightGrad = 2 };
-// Contraction slices of a call (1: none) and the bytes of their partial sums.
-int matmul_splits(MatmulForm f, int E, bool ragged, int64_t rows, int64_t m, int64_t n, int64_t k);
+// Bytes of a call's partial tiles (0: none are cut).
 size_t matmul_workspace_bytes(MatmulForm f, int E, bool ragged, int64_t rows, int64_t m, int64_t n, int64_t k);
-// a.splits, out_group and the fp32 partials in ws are set up by the launcher.
 hipError_t launch_matmul(MatmulForm f, MatmulArgs a, void* ws, hipStream_t st);
 // Forward products of a few rows per group (matmul_stream.hip): whether a call
 // is one, and its launch.

@@ -6,37 +6,41 @@ namespace moe {
 
 namespace {
 
-// out = epilogue(sum over slices, in slice order).  parts [E][splits][m][n]
-// fp32; one thread per eight columns.  Bound by HBM / L2 reads of the parts.
-template <bool F16>
-__global__ __launch_bounds__(256) void matmul_join_kernel(MatmulArgs p, const float* parts, int splits) {
-  const int chunks = ceil_div(p.n, 8);
-  const long long total = (long long)p.E * p.m * chunks;
-  const int64_t one = (int64_t)p.m * p.n;
-  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < total; i += (long long)gridDim.x * 256) {
-    const int64_t row = i / chunks;               // over all groups
-    const int col = (int)(i - row * chunks) * 8;
-    const int64_t e = row / p.m;
-    const float* src = parts + e * splits * one + (row - e * p.m) * p.n + col;
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < splits; ++s, src += one) {
-      if ((p.n & 7) == 0) {
-        const f32x4_t a = *reinterpret_cast<const f32x4_t*>(src), b = *reinterpret_cast<const f32x4_t*>(src + 4);
+// out = epilogue(sum over the slices, in order) of the tiles that were cut;
+// parts [tail][splits][B][B] fp32.  A block takes 2048 values of a tile, a
+// thread eight columns of a row.  Bound by reading the parts, from L2 mostly.
+template <bool F16, bool WG, int B>
+__global__ __launch_bounds__(256) void matmul_join_kernel(MatmulArgs p) {
+  constexpr int kPer = B * B / 2048;
+  const int j = blockIdx.x / kPer;
+  MmTile t;
+  const int64_t tiles = (int64_t)ceil_div(p.m, B) * ceil_div(p.n, B) * (WG ? p.E : 1);
+  mm_plain_tile<WG, B, B>(p, (int)(tiles - p.tail) + j, t);
+  const int at = (blockIdx.x - j * kPer) * 2048 + threadIdx.x * 8;
+  const int row = at / B, col = t.col0 + at % B;
+  if (row >= t.nrows || col >= p.n) return;
+  const float* src = p.parts + (int64_t)j * p.splits * (B * B) + at;
+  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int s = 0; s < p.splits; ++s, src += B * B) {
+    const f32x4_t a = *reinterpret_cast<const f32x4_t*>(src), b = *reinterpret_cast<const f32x4_t*>(src + 4);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          v[q] += a[q];
-          v[4 + q] += b[q];
-        }
-      } else {
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-          if (col + q < p.n) v[q] += src[q];
-      }
+    for (int q = 0; q < 4; ++q) {
+      v[q] += a[q];
+      v[4 + q] += b[q];
     }
-    float bias[8];
-    mm_bias8<F16>(p, col, bias);
-    mm_finish8<F16>(p, v, bias, row, col, 0);
   }
+  float bias[8];
+  mm_bias8<F16>(p, col, bias);
+  mm_finish8<F16>(p, v, bias, (int64_t)t.row0 + row, col, WG ? (int64_t)t.e * p.out_group : 0);
+}
+
+template <bool WG, int B>
+hipError_t launch_join(const MatmulArgs& a, hipStream_t st) {
+  const dim3 grid((unsigned)(a.tail * (B * B / 2048)));
+  if (a.f16) hipLaunchKernelGGL((matmul_join_kernel<true, WG, B>), grid, dim3(256), 0, st, a);
+  else hipLaunchKernelGGL((matmul_join_kernel<false, WG, B>), grid, dim3(256), 0, st, a);
+  return hipGetLastError();
 }
 
 // act'(z) in fp32.
@@ -168,58 +172,83 @@ hipError_t launch_act_grad(const ActGradArgs& a, void* ws, hipStream_t st) {
   return hipSuccess;
 }
 
-int matmul_splits(MatmulForm f, int E, bool ragged, int64_t rows, int64_t m, int64_t n, int64_t k) {
-  if (ragged && f != kMmWeightGrad) return 1;
-  const int64_t groups = f == kMmWeightGrad ? E : 1;
-  const int64_t tiles = groups * ((m + 127) / 128) * ((n + 127) / 128);
+namespace {
+
+// How a call without ragged groups is cut into tiles: their size, and into how
+// many slices of the contraction the tiles of the last, partial round over the
+// card are cut (all tiles, where there is less than a round).
+struct Plan {
+  int big;
+  int tail;
+  int splits;
+  size_t bytes;
+};
+
+// The cheapest of both tile sizes and up to 32 slices by a model of the time
+// in us, from measurements: a 64-wide stage takes 1.2 us with a 256 x 256 tile
+// per CU and 1.07 us with two 128 x 128 tiles per CU (0.65 with one), a tile
+// costs 8 (6) us besides, partial sums pass twice through memory at 4 TB/s and
+// joining them costs a launch.
+Plan matmul_plan(MatmulForm f, int E, int64_t rows, int64_t m, int64_t n, int64_t k, bool aligned, bool whole) {
   const int64_t len = f == kMmWeightGrad ? (rows + E - 1) / E : k;
-  const int64_t stages = (len + kMmK - 1) / kMmK;
-  // two 128 x 128 blocks fit a CU: slice until about 512 blocks, four stages
-  // at least to a slice
-  int64_t s = 512 / (tiles > 0 ? tiles : 1);
-  if (s > stages / 4) s = stages / 4;
-  if (s > 32) s = 32;
-  return s < 2 ? 1 : (int)s;
+  const int64_t stages = len > kMmK ? (len + kMmK - 1) / kMmK : 1;
+  Plan best{0, 0, 1, 0};
+  double best_us = 0;
+  for (int big = 0; big < 2; ++big) {
+    if (big && (!aligned || m <= 128 || n <= 128)) continue;
+    const int64_t B = big ? 256 : 128, slots = big ? 256 : 512;
+    const int64_t tiles = (f == kMmWeightGrad ? E : 1) * ((m + B - 1) / B) * ((n + B - 1) / B);
+    const int64_t rest = tiles % slots, rounds = tiles / slots;
+    const double fixed = big ? 8 : 6;
+    for (int64_t s = 1; s <= 32 && (s == 1 || (s * 4 <= stages && !whole)); ++s) {
+      const int64_t items = rest * s, per = (stages + s - 1) / s;
+      const double stage = big ? 1.2 : rounds > 0 || items > 256 ? 1.07 : 0.65;
+      double us = rounds * (stages * (big ? 1.2 : 1.07) + fixed) + (items + slots - 1) / slots * (per * stage + fixed);
+      if (s > 1) us += 5 + (double)items * B * B * 8 / 4e6;
+      if ((big == 0 && s == 1) || us < best_us) {
+        best_us = us;
+        best = Plan{big, s > 1 ? (int)rest : 0, (int)s, s > 1 ? (size_t)(items * B * B) * sizeof(float) : 0};
+      }
+      if (rest == 0) break;
+    }
+  }
+  return best;
 }
 
+}  // namespace
+
 size_t matmul_workspace_bytes(MatmulForm f, int E, bool ragged, int64_t rows, int64_t m, int64_t n, int64_t k) {
-  const int s = matmul_splits(f, E, ragged, rows, m, n, k);
-  if (s == 1) return 0;
-  return (size_t)s * (f == kMmWeightGrad ? E : 1) * (size_t)m * (size_t)n * sizeof(float);
+  if (ragged && f != kMmWeightGrad) return 0;
+  // the pointers' alignment is not known yet
+  const size_t a = matmul_plan(f, E, rows, m, n, k, true, false).bytes;
+  const size_t b = matmul_plan(f, E, rows, m, n, k, false, false).bytes;
+  return a > b ? a : b;
 }
 
 hipError_t launch_matmul(MatmulForm f, MatmulArgs a, void* ws, hipStream_t st) {
   if (a.m == 0 || (f != kMmWeightGrad && a.rows == 0)) return hipSuccess;
-  if (f == kMmForward && matmul_streams(a)) {
+  if (f == kMmForward && matmul_streams(a)) return launch_matmul_stream(a, st);
+  if (f != kMmWeightGrad && a.offsets != nullptr) {
+    // ragged: 256 x 256 tiles where the mean group would fill the card with
+    // them, else 128 x 128
+    const int64_t mean = (a.rows + a.E - 1) / a.E;
+    a.big = mean > 128 && a.n > 128 && a.E * ((mean + 255) / 256) * ((a.n + 255) / 256) >= 192;
+    a.tail = 0;
     a.splits = 1;
-    return launch_matmul_stream(a, st);
+  } else {
+    const Plan plan = matmul_plan(f, a.E, a.rows, a.m, a.n, a.k, a.aligned != 0, a.whole != 0);
+    a.big = plan.big;
+    a.tail = plan.tail;
+    a.splits = plan.splits;
+    a.parts = static_cast<float*>(ws);
   }
-  const int64_t s = a.whole ? 1 : matmul_splits(f, a.E, a.offsets != nullptr, a.rows, a.m, a.n, a.k);
-  auto launch = [&](const MatmulArgs& q) {
-    return f == kMmForward ? launch_matmul_forward(q, st)
-           : f == kMmRowGrad ? launch_matmul_row_grad(q, st)
-                             : launch_matmul_weight_grad(q, st);
-  };
-  a.splits = (int)s;
-  if (s == 1) return launch(a);
-  MatmulArgs part = a;
-  part.out = ws;
-  part.out_f32 = 1;
-  part.ldo = a.n;
-  part.out_group = (int64_t)a.m * a.n;
-  part.vec = a.n % 4 == 0;
-  part.bias = nullptr;
-  part.act = kActNone;
-  part.residual = nullptr;
-  part.pre = nullptr;
-  if (hipError_t e = launch(part)) return e;
-  if (f != kMmWeightGrad) a.E = 1;
-  const long long work = (long long)a.E * a.m * ceil_div(a.n, 8);
-  const long long blocks = (work + 255) / 256;
-  const unsigned grid = (unsigned)(blocks < 8192 ? blocks : 8192);
-  if (a.f16) hipLaunchKernelGGL(matmul_join_kernel<true>, dim3(grid), dim3(256), 0, st, a, static_cast<const float*>(ws), (int)s);
-  else hipLaunchKernelGGL(matmul_join_kernel<false>, dim3(grid), dim3(256), 0, st, a, static_cast<const float*>(ws), (int)s);
-  return hipGetLastError();
+  if (hipError_t e = f == kMmForward ? launch_matmul_forward(a, st)
+                     : f == kMmRowGrad ? launch_matmul_row_grad(a, st)
+                                       : launch_matmul_weight_grad(a, st))
+    return e;
+  if (a.tail == 0) return hipSuccess;
+  if (f == kMmWeightGrad) return a.big ? launch_join<true, 256>(a, st) : launch_join<true, 128>(a, st);
+  return a.big ? launch_join<false, 256>(a, st) : launch_join<false, 128>(a, st);
 }
 
 }  // namespace moe

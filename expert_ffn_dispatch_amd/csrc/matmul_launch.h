@@ -12,7 +12,7 @@ hipError_t launch_matmul_tile(const MatmulArgs& a, hipStream_t st) {
   if (!WG && a.offsets != nullptr)
     ub = ((long long)a.rows / BM + (a.E < a.rows ? a.E : a.rows)) * NT;
   else
-    ub = (long long)ceil_div(a.m, BM) * NT * a.splits * (WG ? a.E : 1);
+    ub = (long long)ceil_div(a.m, BM) * NT * (WG ? a.E : 1) + (long long)a.tail * (a.splits - 1);
   long long grid = (ub + 7) / 8 * 8;
   // Resident blocks walk the list; each loads its next tile's first stages
   // before it stores the last one.  Against one block per tile: 8192 x 4096 x
@@ -25,19 +25,10 @@ hipError_t launch_matmul_tile(const MatmulArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
-// 256 x 256 tiles where they alone give the card about a block per CU, else
-// 128 x 128.
-inline bool matmul_big(const MatmulArgs& a, bool wg) {
-  const long long E = wg ? (long long)a.E * a.splits : a.offsets != nullptr ? a.E : a.splits;
-  const long long rows = (!wg && a.offsets != nullptr) ? (a.rows + a.E - 1) / a.E : a.m;
-  if (rows <= 128 || a.n <= 128) return false;
-  return E * ((rows + 255) / 256) * ((a.n + 255) / 256) >= 192;
-}
-
 template <bool F16, bool AKC, bool BKC>
 hipError_t launch_matmul_form(const MatmulArgs& a, hipStream_t st) {
   if (!a.aligned) return launch_matmul_tile<F16, AKC, BKC, 128, 128, 2, 2, false>(a, st);
-  if (matmul_big(a, !AKC)) return launch_matmul_tile<F16, AKC, BKC, 256, 256, 2, 4, true>(a, st);
+  if (a.big) return launch_matmul_tile<F16, AKC, BKC, 256, 256, 2, 4, true>(a, st);
   return launch_matmul_tile<F16, AKC, BKC, 128, 128, 2, 2, true>(a, st);
 }
 
