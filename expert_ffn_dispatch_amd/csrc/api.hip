@@ -752,11 +752,14 @@ int check_grouped(const char* fn, moe_grouped_dims& d) {
 }
 
 // Operands in 16-byte pieces: each as (pointer, row stride, row width).
-bool pieces16(const void* p, int64_t ld, int64_t width) { return al16(p) && ld % 8 == 0 && width % 8 == 0; }
+// padded: the row's last piece may be read whole, and holds zeros past the width.
+bool pieces16(const void* p, int64_t ld, int64_t width, bool padded = false) {
+  return al16(p) && ld % 8 == 0 && (padded || width % 8 == 0);
+}
 
-// dx = dy w over `rows` rows (grouped where offsets is set)
+// dx = dy w over `rows` rows (grouped where offsets is set); padded: of dy's rows
 moe::MatmulArgs row_grad_args(const void* dy, int64_t ld_dy, const void* w, int64_t ld_w, void* dx, int64_t ld_dx,
-                              int rows, int n_in, int n_out, int dtype) {
+                              int rows, int n_in, int n_out, int dtype, bool padded = false) {
   moe::MatmulArgs a{};
   a.a = static_cast<const uint16_t*>(dy);
   a.lda = ld_dy;
@@ -769,13 +772,13 @@ moe::MatmulArgs row_grad_args(const void* dy, int64_t ld_dy, const void* w, int6
   a.n = n_in;
   a.k = n_out;
   a.f16 = dtype == MOE_DTYPE_F16;
-  a.aligned = pieces16(dy, ld_dy, n_out) && pieces16(w, ld_w, n_in);
+  a.aligned = pieces16(dy, ld_dy, n_out, padded) && pieces16(w, ld_w, n_in);
   a.vec = al16(dx) && ld_dx % 8 == 0;
   return a;
 }
 
 moe::MatmulArgs weight_grad_args(const void* dy, int64_t ld_dy, const void* x, int64_t ld_x, void* dw, int dw_dtype,
-                                 int E, int rows, int n_in, int n_out, int dtype) {
+                                 int E, int rows, int n_in, int n_out, int dtype, bool padded = false) {
   moe::MatmulArgs a{};
   a.a = static_cast<const uint16_t*>(dy);
   a.lda = ld_dy;
@@ -790,20 +793,22 @@ moe::MatmulArgs weight_grad_args(const void* dy, int64_t ld_dy, const void* x, i
   a.n = n_in;
   a.out_f32 = dw_dtype == MOE_DTYPE_F32;
   a.f16 = dtype == MOE_DTYPE_F16;
-  a.aligned = pieces16(dy, ld_dy, n_out) && pieces16(x, ld_x, n_in);
+  a.aligned = pieces16(dy, ld_dy, n_out, padded) && pieces16(x, ld_x, n_in);
   a.vec = al16(dw) && n_in % 8 == 0;
   return a;
 }
 
+int64_t pitch8(int64_t width) { return (width + 7) / 8 * 8; }
+
 struct LinearBackwardWs {
-  uint16_t* g;               // [rows][out], with an activation
+  uint16_t* g;               // [rows][out to the next multiple of 8], with an activation
   float* sums;               // bias gradient's partial sums
   void* parts;               // contraction slices of either product, one after the other
 };
 LinearBackwardWs carve_linear_backward(Carver& c, const moe_linear_dims& d) {
   const int64_t R = d.rows, I = d.in_features, O = d.out_features;
   LinearBackwardWs w;
-  w.g = d.act != MOE_ACT_NONE ? c.take<uint16_t>((size_t)(R * O)) : nullptr;
+  w.g = d.act != MOE_ACT_NONE ? c.take<uint16_t>((size_t)(R * pitch8(O))) : nullptr;
   w.sums = c.take<float>(moe::act_grad_workspace_bytes(R, O) / sizeof(float));
   const size_t a = moe::matmul_workspace_bytes(moe::kMmRowGrad, 1, false, R, R, I, O);
   const size_t b = moe::matmul_workspace_bytes(moe::kMmWeightGrad, 1, false, R, O, I, R);
@@ -1295,6 +1300,7 @@ int moe_linear_backward(const moe_linear_dims* dims, const void* dy, const void*
     a.pre = static_cast<const uint16_t*>(pre);
     a.ldp = d.ld_pre;
     a.g = act && products ? b.g : nullptr;
+    a.ldg = pitch8(d.out_features);
     a.dbias = dbias;
     a.dbias_f32 = d.bias_dtype == MOE_DTYPE_F32;
     a.rows = d.rows;
@@ -1305,15 +1311,15 @@ int moe_linear_backward(const moe_linear_dims* dims, const void* dy, const void*
   }
   if (act) {
     g = b.g;
-    ld_g = d.out_features;
+    ld_g = pitch8(d.out_features);
   }
   if (dx != nullptr) {
-    const moe::MatmulArgs a = row_grad_args(g, ld_g, w, d.ld_w, dx, d.ld_dx, d.rows, d.in_features, d.out_features, d.dtype);
+    const moe::MatmulArgs a = row_grad_args(g, ld_g, w, d.ld_w, dx, d.ld_dx, d.rows, d.in_features, d.out_features, d.dtype, act);
     if (hipError_t e = moe::launch_matmul(moe::kMmRowGrad, a, b.parts, st)) return device_error(fn, e);
   }
   if (dw != nullptr) {
     const moe::MatmulArgs a =
-        weight_grad_args(g, ld_g, x, d.ld_x, dw, d.dw_dtype, 1, d.rows, d.in_features, d.out_features, d.dtype);
+        weight_grad_args(g, ld_g, x, d.ld_x, dw, d.dw_dtype, 1, d.rows, d.in_features, d.out_features, d.dtype, act);
     if (hipError_t e = moe::launch_matmul(moe::kMmWeightGrad, a, b.parts, st)) return device_error(fn, e);
   }
   return ok();

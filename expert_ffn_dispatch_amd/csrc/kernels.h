@@ -203,7 +203,8 @@ hipError_t launch_matmul_weight_grad(const MatmulArgs& a, hipStream_t st);
 struct ActGradArgs {
   const uint16_t* dy;
   const uint16_t* pre;       // null with kActNone
-  uint16_t* g;               // [rows][n] packed, or null
+  uint16_t* g;               // [rows][ldg], or null; 16-byte aligned, ldg % 8 == 0 and >= n, zeros past n
+  int64_t ldg;
   void* dbias;               // [n] or null
   int dbias_f32;
   int64_t ldd, ldp;

@@ -57,6 +57,24 @@ __device__ __forceinline__ void mm_unpack8(u32x4_t v, float (&f)[8]) {
   }
 }
 
+// 16 bytes / one element from an integer address in global memory (through a
+// pointer without that address space these would be flat loads, which every
+// wait for LDS waits for too).
+__device__ __forceinline__ u32x4_t mm_global16(uint64_t a) {
+#ifdef __HIP_DEVICE_COMPILE__
+  typedef uint32_t any_t __attribute__((ext_vector_type(4), aligned(2)));   // unaligned access is on
+  return *reinterpret_cast<const __attribute__((address_space(1))) any_t*>(a);
+#else
+  return u32x4_t{0, 0, 0, 0};
+#endif
+}
+__device__ __forceinline__ uint16_t mm_global2(uint64_t a) {
+#ifdef __HIP_DEVICE_COMPILE__
+  return *reinterpret_cast<const __attribute__((address_space(1))) uint16_t*>(a);
+#else
+  return 0;
+#endif
+}
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t mm_rsrc(const void* base) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)kMmBytes, 0x00020000);
 }
@@ -111,9 +129,8 @@ __device__ __forceinline__ int mm_kswz(int krow) { return ((krow & 3) << 2) | ((
 // the NI loads of a wave fills 1 KB of it, lane l the bytes 16 l ..+15.
 // ALIGNED: 16-byte loads straight into LDS (rows of 16-byte pitch and
 // alignment, widths in multiples of 8).  Otherwise any strides and sizes: the
-// 16 bytes of a piece are loaded unaligned where they are whole, by elements
-// at the matrix's edge, into registers at the start of a stage and written to
-// LDS at its end.
+// 16 bytes of a piece are loaded unaligned into registers at the start of a
+// stage and written to LDS at its end.
 // Rows, columns and k past the ends become zeros (ALIGNED: by an offset past
 // the buffer, which reads no memory).
 template <bool KC, int R, int NW, bool ALIGNED>
@@ -125,12 +142,16 @@ struct MmOperand {
   uint32_t off[NI];                               // per lane: byte offset within a stage
   int kk[NI];                                     // per lane: first k of the piece within a stage
   int wave;
-  int lim;                                        // KS: columns left in the matrix
+  int lim;                                        // rows (KC) or columns (KS) left in the matrix
+  int before;                                     // elements of the row in front of the tile
 
   // KC: p = element (first row of the tile, first k), ext = live rows.
   // KS: p = element (first k, first column), ext = columns left in the matrix.
-  __device__ __forceinline__ void init(const uint16_t* p, int64_t ld, int ext, int wave_, int lane) {
+  // front: elements of a row in front of p.
+  __device__ __forceinline__ void init(const uint16_t* p, int64_t ld, int ext, int front, int wave_, int lane) {
     base = reinterpret_cast<uint64_t>(p);
+    before = front;
+    lim = ext;
     pitch = (uint32_t)ld * 2u;
     wave = wave_;
 #pragma unroll
@@ -146,7 +167,6 @@ struct MmOperand {
         const int ch = (lane % C) ^ mm_kswz(kr);
         off[i] = ch * 8 < ext ? (uint32_t)kr * pitch + (uint32_t)(ch * 16) : kMmOut;
         kk[i] = kr;
-        lim = ext;
       }
     }
   }
@@ -164,39 +184,68 @@ struct MmOperand {
       loads<I0 + 1, I1>(buf, kt, kend);
     }
   }
-  // !ALIGNED: every piece of stage kt into registers, and from there to LDS
+  // !ALIGNED: elements of piece i of stage kt inside the matrix (at most 0:
+  // none, at least 8: all)
+  __device__ __forceinline__ int inside(int i, int kt, int kend, int lane) const {
+    if (off[i] == kMmOut) return 0;
+    const int left = kend - kt * kMmK;
+    if constexpr (KC) return left - kk[i];
+    else return kk[i] < left ? lim - chunk(i, lane) * 8 : 0;
+  }
+  // every piece of the stage is whole (the same for the whole block)
+  __device__ __forceinline__ bool interior(int kt, int kend) const { return lim >= R && kend - kt * kMmK >= kMmK; }
+  __device__ __forceinline__ int chunk(int i, int lane) const {
+    return (lane % C) ^ mm_kswz((wave * NI + i) * (64 / C) + lane / C);
+  }
+  // A piece of n elements (1..7) at the matrix's edge is read as the last
+  // eight elements of its row and shifted down; true where the row has them.
+  __device__ __forceinline__ bool back(int i, int kt, int n, int lane) const {
+    return before + (KC ? kt * kMmK + kk[i] : chunk(i, lane) * 8) >= 8 - n;
+  }
+  // The pieces of stage kt into registers (nothing waits for them here), and
+  // from there to LDS.  (With the edge's elements loaded one by one, the tiles
+  // that have an edge took microseconds a stage: a weight gradient of 261 x
+  // 320 over 20110 rows of 4 groups 53 us.)
   __device__ __forceinline__ void fetch(u32x4_t (&v)[NI], int kt, int kend, int lane) const {
     if constexpr (!ALIGNED) {
       const uint64_t b = at(kt);
-      const int left = kend - kt * kMmK;
+      if (interior(kt, kend)) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) v[i] = mm_global16(b + off[i]);
+        return;
+      }
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        int n = 0;                                // elements of the piece inside the matrix
-        if (off[i] != kMmOut) {
-          const int piece = wave * NI + i;
-          if constexpr (KC) n = left - kk[i];
-          else n = kk[i] < left ? lim - ((lane % C) ^ mm_kswz(piece * (64 / C) + lane / C)) * 8 : 0;
-        }
-        const uint16_t* src = reinterpret_cast<const uint16_t*>(b + off[i]);
-        if (n >= 8) {
-          __builtin_memcpy(&v[i], src, 16);       // one load: unaligned access is on
-        } else {
-          uint64_t lo = 0, hi = 0;
-#pragma nounroll
-          for (int j = 0; j < n; ++j) {
-            const uint64_t e = (uint64_t)src[j] << (16 * (j & 3));
-            if (j < 4) lo |= e;
-            else hi |= e;
-          }
-          v[i] = u32x4_t{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
-        }
+        const int n = inside(i, kt, kend, lane);
+        v[i] = u32x4_t{0, 0, 0, 0};
+        if (n >= 8 || (n > 0 && back(i, kt, n, lane))) v[i] = mm_global16(b + off[i] - (n < 8 ? 2 * (8 - n) : 0));
       }
     }
   }
-  __device__ __forceinline__ void put(const u32x4_t (&v)[NI], uint16_t* buf, int lane) const {
+  __device__ __forceinline__ void put(u32x4_t (&v)[NI], uint16_t* buf, int kt, int kend, int lane) const {
     if constexpr (!ALIGNED) {
 #pragma unroll
-      for (int i = 0; i < NI; ++i) *reinterpret_cast<u32x4_t*>(buf + (wave * NI + i) * 512 + lane * 8) = v[i];
+      for (int i = 0; i < NI; ++i) {
+        const int n = interior(kt, kend) ? 8 : inside(i, kt, kend, lane);
+        if (n > 0 && n < 8) {
+          uint64_t lo = v[i][0] | ((uint64_t)v[i][1] << 32), hi = v[i][2] | ((uint64_t)v[i][3] << 32);
+          if (back(i, kt, n, lane)) {
+            const int sh = 16 * (8 - n);
+            lo = sh < 64 ? (lo >> sh) | (hi << (64 - sh)) : hi >> (sh - 64);
+            hi = sh < 64 ? hi >> sh : 0;
+          } else {                                // a row of fewer than eight elements
+            const uint64_t src = at(kt) + off[i];
+#pragma nounroll
+            for (int j = 0; j < n; ++j) {
+              const uint64_t e = (uint64_t)mm_global2(src + 2 * j) << (16 * (j & 3));
+              if (j < 4) lo |= e;
+              else hi |= e;
+            }
+          }
+          v[i] = u32x4_t{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+        }
+        *reinterpret_cast<u32x4_t*>(buf + (wave * NI + i) * 512 + lane * 8) = v[i];
+      }
     }
   }
 };
@@ -566,12 +615,12 @@ __global__ __launch_bounds__(64 * WM * WN, BM * BN > 128 * 128 ? 1 : 2) void mat
     }
     KT = max(1, ceil_div(kend, kMmK));
     if constexpr (AKC)
-      la.init(p.a + (int64_t)(q.g0 + q.row0) * p.lda + kbeg, p.lda, q.nrows, wave, lane);
+      la.init(p.a + (int64_t)(q.g0 + q.row0) * p.lda + kbeg, p.lda, q.nrows, kbeg, wave, lane);
     else
-      la.init(p.a + (int64_t)(q.g0 + kbeg) * p.lda + q.row0, p.lda, p.m - q.row0, wave, lane);
+      la.init(p.a + (int64_t)(q.g0 + kbeg) * p.lda + q.row0, p.lda, p.m - q.row0, q.row0, wave, lane);
     const uint16_t* bp = WG ? p.b + (int64_t)q.g0 * p.ldb : p.b + (int64_t)q.e * p.b_group;
-    if constexpr (BKC) lb.init(bp + (int64_t)q.col0 * p.ldb + kbeg, p.ldb, p.n - q.col0, wave, lane);
-    else lb.init(bp + (int64_t)kbeg * p.ldb + q.col0, p.ldb, p.n - q.col0, wave, lane);
+    if constexpr (BKC) lb.init(bp + (int64_t)q.col0 * p.ldb + kbeg, p.ldb, p.n - q.col0, kbeg, wave, lane);
+    else lb.init(bp + (int64_t)kbeg * p.ldb + q.col0, p.ldb, p.n - q.col0, q.col0, wave, lane);
     lb.template loads<0, BI>(sb0, 0, kend);
     la.template loads<0, AI>(sa0, 0, kend);
     lb.template loads<0, BI>(sb1, 1, kend);
@@ -579,10 +628,8 @@ __global__ __launch_bounds__(64 * WM * WN, BM * BN > 128 * 128 ? 1 : 2) void mat
       u32x4_t va[AI], vb[BI];
       la.fetch(va, 0, kend, lane);
       lb.fetch(vb, 0, kend, lane);
-      la.put(va, sa0, lane);
-      lb.put(vb, sb0, lane);
-      lb.fetch(vb, 1, kend, lane);
-      lb.put(vb, sb1, lane);
+      la.put(va, sa0, 0, kend, lane);
+      lb.put(vb, sb0, 0, kend, lane);
     }
   };
   start(t);
@@ -612,7 +659,6 @@ __global__ __launch_bounds__(64 * WM * WN, BM * BN > 128 * 128 ? 1 : 2) void mat
       for (int j = 0; j < FN; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     // row fragments of two half steps, column fragments of two steps
     u32x4_t fa[FH], ga[FH], fb[2][FN];
-    u32x4_t va[AI], vb[BI];                       // !ALIGNED: the stages under way
 
 #define MM_FA1(F_, H_, S_, ABUF, I_)                                           \
   if constexpr ((I_) < ((H_) ? N2 : N1)) F_[(I_) < FH ? (I_) : 0] = ra.template get<S_, (H_) * FH + ((I_) < FH ? (I_) : 0)>(ABUF);
@@ -638,7 +684,7 @@ __global__ __launch_bounds__(64 * WM * WN, BM * BN > 128 * 128 ? 1 : 2) void mat
 // End of one half step (RA_ / RB_ fragments read, M_ rows of products, V_
 // loads): nothing moves past it.
 #define MM_ORDER(RA_, RB_, M_, V_)                                             \
-  if constexpr (ALIGNED && NF > 0)                                             \
+  if constexpr (NF > 0)                                                        \
     mm_order<(RA_) * decltype(ra)::kReads + (RB_) * decltype(rb)::kReads, (M_) * FN, (V_), 4>();   \
   __builtin_amdgcn_sched_barrier(0);
 // Stage KT_: this wave's reads of the last stage and its loads of this one
@@ -650,14 +696,10 @@ __global__ __launch_bounds__(64 * WM * WN, BM * BN > 128 * 128 ? 1 : 2) void mat
 #define MM_STAGE(ABUF, NABUF, BBUF, NBBUF, KT_, FIRST)                         \
   {                                                                            \
     __builtin_amdgcn_s_waitcnt(0xC07F);                                        \
-    if constexpr (ALIGNED) MM_WAIT_VM(BI);                                     \
+    MM_WAIT_VM(BI);                                                            \
     __builtin_amdgcn_s_barrier();                                              \
     __builtin_amdgcn_sched_barrier(0);                                         \
     la.template loads<0, AI>(NABUF, (KT_) + 1, kend);                          \
-    if constexpr (!ALIGNED) {                                                  \
-      la.fetch(va, (KT_) + 1, kend, lane);                                     \
-      lb.fetch(vb, (KT_) + 2, kend, lane);                                     \
-    }                                                                          \
     MM_FB(0, 0, BBUF) MM_FA(ga, 0, 0, ABUF) MM_FB(0, 1, BBUF)                  \
     if constexpr (!(FIRST)) { MM_MMA(fa, 1, 1) }                               \
     MM_ORDER(N1, FN, (FIRST) ? 0 : N2, AI)                                     \
@@ -673,29 +715,51 @@ __global__ __launch_bounds__(64 * WM * WN, BM * BN > 128 * 128 ? 1 : 2) void mat
     MM_MMA(ga, 0, 1)                                                           \
     lb.template loads<B3, BI>(NBBUF, (KT_) + 2, kend);                   \
     MM_ORDER(N2, 0, N1, BI - B3)                                               \
-    la.put(va, NABUF, lane);                                                   \
-    lb.put(vb, NBBUF, lane);                                                   \
   }
 #define MM_A(I) ((I) % 2 == 0 ? sa0 : sa1)
 #define MM_B(I) ((I) % 3 == 0 ? sb0 : (I) % 3 == 1 ? sb1 : sb2)
 #define MM_U(U, KT_, FIRST) MM_STAGE(MM_A(U), MM_A((U) + 1), MM_B(U), MM_B((U) + 2), KT_, FIRST)
 
-    MM_U(0, 0, true)
-    int kt = 1;
-    for (; kt + 5 < KT; kt += 6) {
-      MM_U(1, kt, false)
-      MM_U(2, kt + 1, false)
-      MM_U(3, kt + 2, false)
-      MM_U(4, kt + 3, false)
-      MM_U(5, kt + 4, false)
-      MM_U(6, kt + 5, false)
+    if constexpr (ALIGNED) {
+      MM_U(0, 0, true)
+      int kt = 1;
+      for (; kt + 5 < KT; kt += 6) {
+        MM_U(1, kt, false)
+        MM_U(2, kt + 1, false)
+        MM_U(3, kt + 2, false)
+        MM_U(4, kt + 3, false)
+        MM_U(5, kt + 4, false)
+        MM_U(6, kt + 5, false)
+      }
+      if (kt < KT) MM_U(1, kt, false)
+      if (kt + 1 < KT) MM_U(2, kt + 1, false)
+      if (kt + 2 < KT) MM_U(3, kt + 2, false)
+      if (kt + 3 < KT) MM_U(4, kt + 3, false)
+      if (kt + 4 < KT) MM_U(5, kt + 4, false)
+      MM_MMA(fa, 1, 1)
+    } else {
+      // One buffer: the next stage is on its way to registers during this
+      // one's products, and written when every wave has read this one.
+      mm_lds_barrier();
+#pragma nounroll
+      for (int kt = 0; kt < KT; ++kt) {
+        u32x4_t va[AI], vb[BI];
+        la.fetch(va, kt + 1, kend, lane);
+        lb.fetch(vb, kt + 1, kend, lane);
+        MM_FB(0, 0, sb0) MM_FA(ga, 0, 0, sa0) MM_FB(0, 1, sb0)
+        MM_FA(fa, 1, 0, sa0) MM_FB(1, 0, sb0)
+        MM_MMA(ga, 0, 0)
+        MM_FA(ga, 0, 1, sa0) MM_FB(1, 1, sb0)
+        MM_MMA(fa, 1, 0)
+        MM_FA(fa, 1, 1, sa0)
+        MM_MMA(ga, 0, 1)
+        MM_MMA(fa, 1, 1)
+        mm_lds_barrier();
+        la.put(va, sa0, kt + 1, kend, lane);
+        lb.put(vb, sb0, kt + 1, kend, lane);
+        mm_lds_barrier();
+      }
     }
-    if (kt < KT) MM_U(1, kt, false)
-    if (kt + 1 < KT) MM_U(2, kt + 1, false)
-    if (kt + 2 < KT) MM_U(3, kt + 2, false)
-    if (kt + 3 < KT) MM_U(4, kt + 3, false)
-    if (kt + 4 < KT) MM_U(5, kt + 4, false)
-    MM_MMA(fa, 1, 1)
     // Loads past the last stage (zeros) still target the buffers of stages 0
     // and 1 of the next tile and the staging slots: they land first.
     MM_WAIT_VM(0);

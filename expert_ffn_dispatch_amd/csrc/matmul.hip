@@ -63,48 +63,59 @@ __device__ __forceinline__ float act_grad(float z, int act) {
   }
 }
 
-// A block covers 512 columns (two per lane of each wave... 64 lanes x 8) and
-// a run of rows: wave w takes rows w, w + 4, ... of the run; lanes hold eight
-// columns each and their fp32 sums, which the four waves add up in LDS.
-// Partial sums [row runs][n]; dbias_join adds the runs in order.
+// Eight values of a row from column 0 of p on; n of them inside the matrix.
 template <bool F16>
-__global__ __launch_bounds__(256) void act_grad_kernel(ActGradArgs p, float* part, int run, int vec) {
+__device__ __forceinline__ u32x4_t act_load(const uint16_t* p, int n) {
+  u32x4_t v{0, 0, 0, 0};
+  if (n >= 8) {
+    __builtin_memcpy(&v, p, 16);                  // one load: unaligned access is on
+  } else if (n > 0) {
+#pragma unroll
+    for (int q = 0; q < 7; ++q)
+      if (q < n) v[q >> 1] |= (uint32_t)p[q] << (16 * (q & 1));
+  }
+  return v;
+}
+
+// A block covers 512 columns (eight per lane) and a run of rows; its four
+// waves take four neighbouring rows each at a time, loaded together.  Lanes
+// keep fp32 sums of their columns, which the waves add up in LDS; partial sums
+// [runs][n], and dbias_join_kernel adds the runs in order.
+// g has a row pitch of ldg; columns n..ldg-1 become zeros.
+template <bool F16>
+__global__ __launch_bounds__(256) void act_grad_kernel(ActGradArgs p, float* part, int run) {
   __shared__ float s_sum[4][512];
+  constexpr int U = 4;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int col = blockIdx.x * 512 + lane * 8;
   const int r0 = blockIdx.y * run, r1 = min(r0 + run, p.rows);
   const int left = p.n - col;
   float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  for (int r = r0 + wave; r < r1; r += 4) {
-    float d[8], z[8];
-    const uint16_t* dp = p.dy + (int64_t)r * p.ldd + col;
-    const uint16_t* zp = p.act != kActNone ? p.pre + (int64_t)r * p.ldp + col : nullptr;
-    if (vec && left >= 8) {
-      mm_unpack8<F16>(*reinterpret_cast<const u32x4_t*>(dp), d);
-      if (zp) mm_unpack8<F16>(*reinterpret_cast<const u32x4_t*>(zp), z);
-    } else {
+  for (int r = r0 + wave * U; r < r1; r += 4 * U) {
+    u32x4_t dv[U], zv[U];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        d[q] = q < left ? mm_load1<F16>(dp[q]) : 0.f;
-        z[q] = (zp && q < left) ? mm_load1<F16>(zp[q]) : 0.f;
-      }
-    }
-    if (zp) {
-#pragma unroll
-      for (int q = 0; q < 8; ++q) d[q] *= act_grad(z[q], p.act);
+    for (int k = 0; k < U; ++k) {
+      const int n = r + k < r1 ? left : 0;
+      dv[k] = act_load<F16>(p.dy + (int64_t)(r + k) * p.ldd + col, n);
+      zv[k] = u32x4_t{0, 0, 0, 0};
+      if (p.act != kActNone) zv[k] = act_load<F16>(p.pre + (int64_t)(r + k) * p.ldp + col, n);
     }
 #pragma unroll
-    for (int q = 0; q < 8; ++q) sum[q] += d[q];
-    if (p.g) {
-      uint16_t* gp = p.g + (int64_t)r * p.n + col;
-      if (vec && left >= 8) {
-        *reinterpret_cast<u32x4_t*>(gp) = u32x4_t{mm_pack2<F16>(d[0], d[1]), mm_pack2<F16>(d[2], d[3]),
-                                                  mm_pack2<F16>(d[4], d[5]), mm_pack2<F16>(d[6], d[7])};
-      } else {
+    for (int k = 0; k < U; ++k) {
+      float d[8], z[8];
+      mm_unpack8<F16>(dv[k], d);
+      if (p.act != kActNone) {
+        mm_unpack8<F16>(zv[k], z);
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
-          if (q < left) gp[q] = mm_store1<F16>(d[q]);
+        for (int q = 0; q < 8; ++q) d[q] *= act_grad(z[q], p.act);
       }
+#pragma unroll
+      for (int q = 0; q < 8; ++q) sum[q] += d[q]; // zeros past the ends
+      // (the pitch is a multiple of 8, and what lies past the width is zero)
+      if (p.g && r + k < r1 && col < p.ldg)
+        *reinterpret_cast<u32x4_t*>(p.g + (int64_t)(r + k) * p.ldg + col) =
+            u32x4_t{mm_pack2<F16>(d[0], d[1]), mm_pack2<F16>(d[2], d[3]), mm_pack2<F16>(d[4], d[5]),
+                    mm_pack2<F16>(d[6], d[7])};
     }
   }
   if (!p.dbias) return;
@@ -118,18 +129,22 @@ __global__ __launch_bounds__(256) void act_grad_kernel(ActGradArgs p, float* par
 }
 
 template <bool F16>
-__global__ __launch_bounds__(256) void dbias_join_kernel(ActGradArgs p, const float* part, int runs) {
-  // 64 columns per block; each wave sums every fourth run, LDS joins the four
-  __shared__ float s_sum[4][64];
+__global__ __launch_bounds__(1024) void dbias_join_kernel(ActGradArgs p, const float* part, int runs) {
+  // 64 columns per block; each wave sums every sixteenth run, LDS joins them
+  __shared__ float s_sum[16][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int c = blockIdx.x * 64 + lane;
   float s = 0.f;
-  if (c < p.n)
-    for (int r = wave; r < runs; r += 4) s += part[(int64_t)r * p.n + c];
+  if (c < p.n) {
+#pragma unroll 8
+    for (int r = wave; r < runs; r += 16) s += part[(int64_t)r * p.n + c];
+  }
   s_sum[wave][lane] = s;
   __syncthreads();
   if (wave == 0 && c < p.n) {
-    const float v = (s_sum[0][lane] + s_sum[1][lane]) + (s_sum[2][lane] + s_sum[3][lane]);
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) v += s_sum[w][lane];
     if (p.dbias_f32) static_cast<float*>(p.dbias)[c] = v;
     else static_cast<uint16_t*>(p.dbias)[c] = mm_store1<F16>(v);
   }
@@ -139,8 +154,8 @@ __global__ __launch_bounds__(256) void dbias_join_kernel(ActGradArgs p, const fl
 int act_grad_run(int64_t rows, int64_t n) {
   const int64_t col_blocks = (n + 511) / 512;
   const int64_t want = (1024 + col_blocks - 1) / col_blocks;
-  int64_t run = (rows + want - 1) / want;
-  return (int)(run < 16 ? 16 : run);
+  const int64_t run = (rows + want - 1) / want;
+  return (int)((run + 15) / 16 * 16 < 16 ? 16 : (run + 15) / 16 * 16);
 }
 
 }  // namespace
@@ -154,19 +169,16 @@ hipError_t launch_act_grad(const ActGradArgs& a, void* ws, hipStream_t st) {
   const int run = act_grad_run(a.rows, a.n);
   const int runs = ceil_div(a.rows, run);
   float* part = static_cast<float*>(ws);
-  auto al = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
-  const int vec = al(a.dy) && a.ldd % 8 == 0 && (a.act == kActNone || (al(a.pre) && a.ldp % 8 == 0)) &&
-                  (a.g == nullptr || (al(a.g) && a.n % 8 == 0));
   if (runs > 0) {
     const dim3 grid((unsigned)ceil_div(a.n, 512), (unsigned)runs);
-    if (a.f16) hipLaunchKernelGGL(act_grad_kernel<true>, grid, dim3(256), 0, st, a, part, run, vec);
-    else hipLaunchKernelGGL(act_grad_kernel<false>, grid, dim3(256), 0, st, a, part, run, vec);
+    if (a.f16) hipLaunchKernelGGL(act_grad_kernel<true>, grid, dim3(256), 0, st, a, part, run);
+    else hipLaunchKernelGGL(act_grad_kernel<false>, grid, dim3(256), 0, st, a, part, run);
     if (hipError_t e = hipGetLastError()) return e;
   }
   if (a.dbias) {
     const dim3 grid((unsigned)ceil_div(a.n, 64));
-    if (a.f16) hipLaunchKernelGGL(dbias_join_kernel<true>, grid, dim3(256), 0, st, a, part, runs);
-    else hipLaunchKernelGGL(dbias_join_kernel<false>, grid, dim3(256), 0, st, a, part, runs);
+    if (a.f16) hipLaunchKernelGGL(dbias_join_kernel<true>, grid, dim3(1024), 0, st, a, part, runs);
+    else hipLaunchKernelGGL(dbias_join_kernel<false>, grid, dim3(1024), 0, st, a, part, runs);
     return hipGetLastError();
   }
   return hipSuccess;
