@@ -643,7 +643,6 @@ static_assert(moe::kTypeBf16 == MOE_DTYPE_BF16 && moe::kTypeF16 == MOE_DTYPE_F16
               "the ABI's type and activation codes are the kernels'");
 
 size_t elem_bytes(int dtype) { return dtype == MOE_DTYPE_F32 ? 4 : 2; }
-bool al16(const void* p) { return aligned(p); }
 
 // A pointer that is there and has its element's alignment.
 #define REQ_ELEM(p, dtype)                                                                \
@@ -751,12 +750,6 @@ int check_grouped(const char* fn, moe_grouped_dims& d) {
   return check_tiles(fn, d.n_experts, d.out_features, d.in_features);
 }
 
-// Operands in 16-byte pieces: each as (pointer, row stride, row width).
-// padded: the row's last piece may be read whole, and holds zeros past the width.
-bool pieces16(const void* p, int64_t ld, int64_t width, bool padded = false) {
-  return al16(p) && ld % 8 == 0 && (padded || width % 8 == 0);
-}
-
 // dx = dy w over `rows` rows (grouped where offsets is set); padded: of dy's rows
 moe::MatmulArgs row_grad_args(const void* dy, int64_t ld_dy, const void* w, int64_t ld_w, void* dx, int64_t ld_dx,
                               int rows, int n_in, int n_out, int dtype, bool padded = false) {
@@ -772,8 +765,7 @@ moe::MatmulArgs row_grad_args(const void* dy, int64_t ld_dy, const void* w, int6
   a.n = n_in;
   a.k = n_out;
   a.f16 = dtype == MOE_DTYPE_F16;
-  a.aligned = pieces16(dy, ld_dy, n_out, padded) && pieces16(w, ld_w, n_in);
-  a.vec = al16(dx) && ld_dx % 8 == 0;
+  a.a_padded = padded;
   return a;
 }
 
@@ -793,42 +785,60 @@ moe::MatmulArgs weight_grad_args(const void* dy, int64_t ld_dy, const void* x, i
   a.n = n_in;
   a.out_f32 = dw_dtype == MOE_DTYPE_F32;
   a.f16 = dtype == MOE_DTYPE_F16;
-  a.aligned = pieces16(dy, ld_dy, n_out, padded) && pieces16(x, ld_x, n_in);
-  a.vec = al16(dw) && n_in % 8 == 0;
+  a.a_padded = padded;
   return a;
 }
 
 int64_t pitch8(int64_t width) { return (width + 7) / 8 * 8; }
 
+moe::MatmulArgs linear_args(const moe_linear_dims& d, const void* x, const void* w, void* y) {
+  moe::MatmulArgs a{};
+  a.a = static_cast<const uint16_t*>(x);
+  a.lda = d.ld_x;
+  a.b = static_cast<const uint16_t*>(w);
+  a.ldb = d.ld_w;
+  a.out = y;
+  a.ldo = d.ld_y;
+  a.E = 1;
+  a.rows = a.m = d.rows;
+  a.n = d.out_features;
+  a.k = d.in_features;
+  a.f16 = d.dtype == MOE_DTYPE_F16;
+  // A shape for the kernel for a few rows: no workspace.  (Should only the
+  // pointers not suit it, the tiles run without slices and copies.)
+  a.whole = d.rows <= 64 && d.in_features % 8 == 0 && d.ld_x % 8 == 0 && d.ld_w % 8 == 0;
+  return a;
+}
+
 struct LinearBackwardWs {
   uint16_t* g;               // [rows][out to the next multiple of 8], with an activation
   float* sums;               // bias gradient's partial sums
-  void* parts;               // contraction slices of either product, one after the other
+  void* products;            // workspace of either product, one after the other
 };
 LinearBackwardWs carve_linear_backward(Carver& c, const moe_linear_dims& d) {
-  const int64_t R = d.rows, I = d.in_features, O = d.out_features;
+  const int64_t R = d.rows, O = d.out_features;
+  const bool act = d.act != MOE_ACT_NONE;
+  const int64_t ld_g = act ? pitch8(O) : d.ld_dy;
   LinearBackwardWs w;
-  w.g = d.act != MOE_ACT_NONE ? c.take<uint16_t>((size_t)(R * pitch8(O))) : nullptr;
+  w.g = act ? c.take<uint16_t>((size_t)(R * pitch8(O))) : nullptr;
   w.sums = c.take<float>(moe::act_grad_workspace_bytes(R, O) / sizeof(float));
-  const size_t a = moe::matmul_workspace_bytes(moe::kMmRowGrad, 1, false, R, R, I, O);
-  const size_t b = moe::matmul_workspace_bytes(moe::kMmWeightGrad, 1, false, R, O, I, R);
-  w.parts = c.take<char>(a > b ? a : b);
+  const size_t a = moe::matmul_workspace_bytes(
+      moe::kMmRowGrad, row_grad_args(nullptr, ld_g, nullptr, d.ld_w, nullptr, d.ld_dx, d.rows, d.in_features,
+                                     d.out_features, d.dtype, act));
+  const size_t b = moe::matmul_workspace_bytes(
+      moe::kMmWeightGrad, weight_grad_args(nullptr, ld_g, nullptr, d.ld_x, nullptr, d.dw_dtype, 1, d.rows,
+                                           d.in_features, d.out_features, d.dtype, act));
+  w.products = c.take<char>(a > b ? a : b);
   return w;
 }
 
-// Whether a call's shape and strides suit the kernel for a few rows, which
-// needs no workspace.  (Should only its pointers not suit, the tiles run
-// without contraction slices.)
-bool linear_streams(const moe_linear_dims& d) {
-  return d.rows <= 64 && d.in_features % 8 == 0 && d.ld_x % 8 == 0 && d.ld_w % 8 == 0;
-}
 size_t linear_ws_bytes(const moe_linear_dims& d) {
-  if (linear_streams(d)) return 0;
-  return align_up(moe::matmul_workspace_bytes(moe::kMmForward, 1, false, d.rows, d.rows, d.out_features, d.in_features));
+  return align_up(moe::matmul_workspace_bytes(moe::kMmForward, linear_args(d, nullptr, nullptr, nullptr)));
 }
 size_t grouped_wgrad_ws_bytes(const moe_grouped_dims& d) {
-  return align_up(moe::matmul_workspace_bytes(moe::kMmWeightGrad, d.n_experts, true, d.rows, d.out_features,
-                                              d.in_features, d.rows));
+  return align_up(moe::matmul_workspace_bytes(
+      moe::kMmWeightGrad, weight_grad_args(nullptr, d.ld_y, nullptr, d.ld_x, nullptr, d.dw_dtype, d.n_experts, d.rows,
+                                           d.in_features, d.out_features, d.dtype)));
 }
 
 // A copy of the caller's dims to resolve strides in.
@@ -1225,22 +1235,7 @@ int moe_linear(const moe_linear_dims* dims, const void* x, const void* w, const 
   if (residual == y && d.ld_residual != d.ld_y)
     return fail(MOE_ERR_INVALID, "%s: residual is y with another row stride", fn);
   if (int r = check_ws(fn, ws, ws_bytes, linear_ws_bytes(d))) return r;
-  moe::MatmulArgs a{};
-  a.a = static_cast<const uint16_t*>(x);
-  a.lda = d.ld_x;
-  a.b = static_cast<const uint16_t*>(w);
-  a.ldb = d.ld_w;
-  a.out = y;
-  a.ldo = d.ld_y;
-  a.E = 1;
-  a.rows = a.m = d.rows;
-  a.n = d.out_features;
-  a.k = d.in_features;
-  a.f16 = d.dtype == MOE_DTYPE_F16;
-  a.aligned = pieces16(x, d.ld_x, d.in_features) && pieces16(w, d.ld_w, d.in_features);
-  a.vec = al16(y) && d.ld_y % 8 == 0 && (residual == nullptr || (al16(residual) && d.ld_residual % 8 == 0)) &&
-          (pre == nullptr || (al16(pre) && d.ld_pre % 8 == 0));
-  a.whole = linear_streams(d);
+  moe::MatmulArgs a = linear_args(d, x, w, y);
   a.bias = bias;
   a.bias_f32 = d.bias_dtype == MOE_DTYPE_F32;
   a.act = d.act;
@@ -1315,12 +1310,12 @@ int moe_linear_backward(const moe_linear_dims* dims, const void* dy, const void*
   }
   if (dx != nullptr) {
     const moe::MatmulArgs a = row_grad_args(g, ld_g, w, d.ld_w, dx, d.ld_dx, d.rows, d.in_features, d.out_features, d.dtype, act);
-    if (hipError_t e = moe::launch_matmul(moe::kMmRowGrad, a, b.parts, st)) return device_error(fn, e);
+    if (hipError_t e = moe::launch_matmul(moe::kMmRowGrad, a, b.products, st)) return device_error(fn, e);
   }
   if (dw != nullptr) {
     const moe::MatmulArgs a =
         weight_grad_args(g, ld_g, x, d.ld_x, dw, d.dw_dtype, 1, d.rows, d.in_features, d.out_features, d.dtype, act);
-    if (hipError_t e = moe::launch_matmul(moe::kMmWeightGrad, a, b.parts, st)) return device_error(fn, e);
+    if (hipError_t e = moe::launch_matmul(moe::kMmWeightGrad, a, b.products, st)) return device_error(fn, e);
   }
   return ok();
 }
@@ -1350,8 +1345,6 @@ int moe_grouped_matmul(const moe_grouped_dims* dims, const void* x, const int32_
   a.n = d.out_features;
   a.k = d.in_features;
   a.f16 = d.dtype == MOE_DTYPE_F16;
-  a.aligned = pieces16(x, d.ld_x, d.in_features) && al16(w);
-  a.vec = al16(y) && d.ld_y % 8 == 0;
   if (hipError_t e = moe::launch_matmul(moe::kMmForward, a, nullptr, static_cast<hipStream_t>(stream)))
     return device_error(fn, e);
   return ok();

@@ -167,7 +167,6 @@ struct MatmulArgs {
   int rows;                  // rows of the grouped operands
   int m, n, k;               // output rows (of one group), output columns, contraction (weight grad: unused)
   int out_f32;
-  int vec;                   // out, residual and pre take 16-byte accesses
   // epilogue (null / kActNone: none): out = act(sum + bias) + residual, pre = sum + bias
   const void* bias;
   int bias_f32;
@@ -176,18 +175,20 @@ struct MatmulArgs {
   int64_t ldr;
   uint16_t* pre;
   int64_t ldp;
-  int aligned;               // a and b take 16-byte loads
+  int a_padded;              // a's last piece of a row may be read whole and is zero past the width
   int f16;                   // operands are fp16 (else bf16)
   int whole;                 // no contraction slices (no workspace for them)
   // set by launch_matmul: the plan
+  int aligned;               // a and b take 16-byte loads
   int big;                   // 256 x 256 tiles (else 128 x 128)
   int tail;                  // tiles at the end of the list that are cut into
   int splits;                // slices of the contraction, whose fp32 partial
   float* parts;              // tiles are here, joined by another launch
 };
 enum MatmulForm { kMmForward = 0, kMmRowGrad = 1, kMmWeightGrad = 2 };
-// Bytes of a call's partial tiles (0: none are cut).
-size_t matmul_workspace_bytes(MatmulForm f, int E, bool ragged, int64_t rows, int64_t m, int64_t n, int64_t k);
+// Workspace of a call (0: none): partial tiles and copies of operands that
+// would not take 16-byte loads.  Of `a` it reads sizes, strides and flags only.
+size_t matmul_workspace_bytes(MatmulForm f, const MatmulArgs& a);
 hipError_t launch_matmul(MatmulForm f, MatmulArgs a, void* ws, hipStream_t st);
 // Forward products of a few rows per group (matmul_stream.hip): whether a call
 // is one, and its launch.

@@ -457,8 +457,10 @@ __device__ __forceinline__ bool mm_find_tile(const MatmulArgs& p, int lane, int 
 // Results carry the non-temporal hint: no tile reads them again, and L2 stays
 // with the operands (8192 x 4096 x 16384 with the pre-activation saved 942 ->
 // 929 us, 24576 rows over 160 experts 635 -> 615).
+// (At whatever alignment the rows have: unaligned access is on.)
+typedef uint32_t u32x4_any_t __attribute__((ext_vector_type(4), aligned(2)));
 __device__ __forceinline__ void mm_store16(void* p, u32x4_t v) {
-  __builtin_nontemporal_store(v, static_cast<u32x4_t*>(p));
+  __builtin_nontemporal_store(v, static_cast<u32x4_any_t*>(p));
 }
 
 template <bool F16>
@@ -469,7 +471,7 @@ __device__ __forceinline__ void mm_finish8(const MatmulArgs& p, float (&v)[8], c
 #pragma unroll
     for (int q = 0; q < 8; ++q) v[q] += bias[q];
   }
-  const bool vec = p.vec && n >= 8;
+  const bool vec = n >= 8;
   if (p.pre != nullptr) {
     uint16_t* o = p.pre + orow * p.ldp + col;
     if (vec) {
@@ -489,7 +491,7 @@ __device__ __forceinline__ void mm_finish8(const MatmulArgs& p, float (&v)[8], c
     const uint16_t* r = p.residual + orow * p.ldr + col;
     if (vec) {
       float f[8];
-      mm_unpack8<F16>(*reinterpret_cast<const u32x4_t*>(r), f);
+      mm_unpack8<F16>(*reinterpret_cast<const u32x4_any_t*>(r), f);
 #pragma unroll
       for (int q = 0; q < 8; ++q) v[q] += f[q];
     } else {

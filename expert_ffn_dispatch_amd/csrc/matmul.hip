@@ -63,9 +63,8 @@ __device__ __forceinline__ float act_grad(float z, int act) {
   }
 }
 
-// Eight values of a row from column 0 of p on; n of them inside the matrix.
-template <bool F16>
-__device__ __forceinline__ u32x4_t act_load(const uint16_t* p, int n) {
+// Eight 16-bit values from p on, zeros from the n-th on.
+__device__ __forceinline__ u32x4_t load8(const uint16_t* p, int n) {
   u32x4_t v{0, 0, 0, 0};
   if (n >= 8) {
     __builtin_memcpy(&v, p, 16);                  // one load: unaligned access is on
@@ -96,9 +95,9 @@ __global__ __launch_bounds__(256) void act_grad_kernel(ActGradArgs p, float* par
 #pragma unroll
     for (int k = 0; k < U; ++k) {
       const int n = r + k < r1 ? left : 0;
-      dv[k] = act_load<F16>(p.dy + (int64_t)(r + k) * p.ldd + col, n);
+      dv[k] = load8(p.dy + (int64_t)(r + k) * p.ldd + col, n);
       zv[k] = u32x4_t{0, 0, 0, 0};
-      if (p.act != kActNone) zv[k] = act_load<F16>(p.pre + (int64_t)(r + k) * p.ldp + col, n);
+      if (p.act != kActNone) zv[k] = load8(p.pre + (int64_t)(r + k) * p.ldp + col, n);
     }
 #pragma unroll
     for (int k = 0; k < U; ++k) {
@@ -229,16 +228,95 @@ Plan matmul_plan(MatmulForm f, int E, int64_t rows, int64_t m, int64_t n, int64_
 
 }  // namespace
 
-size_t matmul_workspace_bytes(MatmulForm f, int E, bool ragged, int64_t rows, int64_t m, int64_t n, int64_t k) {
-  if (ragged && f != kMmWeightGrad) return 0;
-  // the pointers' alignment is not known yet
-  const size_t a = matmul_plan(f, E, rows, m, n, k, true, false).bytes;
-  const size_t b = matmul_plan(f, E, rows, m, n, k, false, false).bytes;
-  return a > b ? a : b;
+namespace {
+
+// out[r] = in[r], widened to `pitch` with zeros; a thread moves eight columns.
+__global__ __launch_bounds__(256) void pack_kernel(const uint16_t* in, int64_t ld, int64_t rows, int width,
+                                                   uint16_t* out, int pitch) {
+  const int chunks = pitch / 8;
+  const int64_t total = rows * chunks;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / chunks;
+    const int c = (int)(i - r * chunks) * 8;
+    *reinterpret_cast<u32x4_t*>(out + r * pitch + c) = load8(in + r * ld + c, width - c);
+  }
+}
+
+// Operands that do not take 16-byte loads are copied with padded rows where
+// that costs less than the products gain: a product runs at 1000 TFLOP/s with
+// such loads and at 440 without, and takes about 1 us less a stage where it is
+// bound by latency; a copy passes twice through memory at 4 TB/s and takes a
+// launch (2000 x 7041 x 7041 448 us without, and 8 + 30 us for the copies).
+struct Packing {
+  bool a, b;
+  int wa, wb, pa, pb;        // widths, pitches
+  int64_t ra, rb;            // rows
+  size_t bytes_a, bytes_b;
+};
+size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
+Packing packing(MatmulForm f, const MatmulArgs& q) {
+  Packing k{};
+  k.wa = f == kMmWeightGrad ? q.m : q.k;
+  k.wb = f == kMmForward ? q.k : q.n;
+  k.ra = q.rows;
+  k.rb = f == kMmForward ? q.n : f == kMmRowGrad ? q.k : q.rows;
+  if (q.whole || (f != kMmWeightGrad && q.offsets != nullptr)) return k;
+  const bool a = !(q.lda % 8 == 0 && (q.a_padded || k.wa % 8 == 0)), b = !(q.ldb % 8 == 0 && k.wb % 8 == 0);
+  if (!a && !b) return k;
+  auto pitch = [](int w) { return w >= 512 ? (w + 63) / 64 * 64 : (w + 7) / 8 * 8; };
+  k.pa = pitch(k.wa);
+  k.pb = pitch(k.wb);
+  const size_t na = (size_t)k.ra * k.pa * 2, nb = (size_t)k.rb * k.pb * 2;
+  const int64_t len = f == kMmWeightGrad ? q.rows / q.E : q.k, stages = len / kMmK;
+  const double flops = 2.0 * q.rows * (f == kMmForward ? (double)q.n * q.k : f == kMmRowGrad ? (double)q.k * q.n : (double)q.m * q.n);
+  const double gain = flops * 1.2e-9 + (stages < 16 ? stages : 16);
+  const double cost = (a ? na * 2 / 4e6 + 4 : 0) + (b ? nb * 2 / 4e6 + 4 : 0);
+  if (gain <= cost) return k;
+  k.a = a;
+  k.b = b;
+  k.bytes_a = a ? up256(na) : 0;
+  k.bytes_b = b ? up256(nb) : 0;
+  return k;
+}
+hipError_t launch_pack(const uint16_t* in, int64_t ld, int64_t rows, int width, void* out, int pitch, hipStream_t st) {
+  const int64_t blocks = (rows * (pitch / 8) + 255) / 256;
+  hipLaunchKernelGGL(pack_kernel, dim3((unsigned)(blocks < 16384 ? blocks : 16384)), dim3(256), 0, st, in, ld, rows,
+                     width, static_cast<uint16_t*>(out), pitch);
+  return hipGetLastError();
+}
+bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+}  // namespace
+
+size_t matmul_workspace_bytes(MatmulForm f, const MatmulArgs& a) {
+  if (a.whole || (f != kMmWeightGrad && a.offsets != nullptr)) return 0;
+  const Packing k = packing(f, a);
+  // the pointers' alignment is not known here: either plan may run
+  const size_t x = matmul_plan(f, a.E, a.rows, a.m, a.n, a.k, true, false).bytes;
+  const size_t y = matmul_plan(f, a.E, a.rows, a.m, a.n, a.k, false, false).bytes;
+  return k.bytes_a + k.bytes_b + up256(x > y ? x : y);
 }
 
 hipError_t launch_matmul(MatmulForm f, MatmulArgs a, void* ws, hipStream_t st) {
   if (a.m == 0 || (f != kMmWeightGrad && a.rows == 0)) return hipSuccess;
+  const Packing k = packing(f, a);
+  const bool a16 = al16(a.a) && a.lda % 8 == 0 && (a.a_padded || k.wa % 8 == 0);
+  const bool b16 = al16(a.b) && a.ldb % 8 == 0 && k.wb % 8 == 0;
+  a.aligned = (a16 || k.a) && (b16 || k.b);
+  char* w = static_cast<char*>(ws);
+  if (a.aligned && a.rows > 0) {
+    if (k.a) {
+      if (hipError_t e = launch_pack(a.a, a.lda, k.ra, k.wa, w, k.pa, st)) return e;
+      a.a = reinterpret_cast<const uint16_t*>(w);
+      a.lda = k.pa;
+    }
+    if (k.b) {
+      if (hipError_t e = launch_pack(a.b, a.ldb, k.rb, k.wb, w + k.bytes_a, k.pb, st)) return e;
+      a.b = reinterpret_cast<const uint16_t*>(w + k.bytes_a);
+      a.ldb = k.pb;
+    }
+  }
+  a.parts = reinterpret_cast<float*>(w + k.bytes_a + k.bytes_b);
   if (f == kMmForward && matmul_streams(a)) return launch_matmul_stream(a, st);
   if (f != kMmWeightGrad && a.offsets != nullptr) {
     // ragged: 256 x 256 tiles where the mean group would fill the card with
@@ -252,7 +330,6 @@ hipError_t launch_matmul(MatmulForm f, MatmulArgs a, void* ws, hipStream_t st) {
     a.big = plan.big;
     a.tail = plan.tail;
     a.splits = plan.splits;
-    a.parts = static_cast<float*>(ws);
   }
   if (hipError_t e = f == kMmForward ? launch_matmul_forward(a, st)
                      : f == kMmRowGrad ? launch_matmul_row_grad(a, st)
