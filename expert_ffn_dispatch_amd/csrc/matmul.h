@@ -81,6 +81,10 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t mm_rsrc(const void* base) {
 __device__ __forceinline__ void mm_dma16(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff, uint16_t* lds) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, lds, 16, voff, soff, 0, 0);
 }
+// The same with the non-temporal hint, for weights read once.
+__device__ __forceinline__ void mm_dma16_nt(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff, uint16_t* lds) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, lds, 16, voff, soff, 0, 2);
+}
 // 4 x 16 transposing read of 16-bit values: within each 16 lanes, lane l
 // names the 8 bytes (row l >> 2, columns 4 (l & 3) ..+3) of a 4 x 16 block and
 // receives the block's column l, rows 0..3 (checked on the device).
@@ -385,6 +389,18 @@ __device__ __forceinline__ bool mm_find_tile(const MatmulArgs& p, int lane, int 
     const int64_t tiles = (int64_t)ceil_div(p.m, BM) * ceil_div(p.n, BN) * (WG ? p.E : 1);
     const int64_t whole = tiles - p.tail, items = p.tail * p.splits;
     const int64_t w0 = whole * x >> 3, w1 = whole * (x + 1) >> 3;
+    // Weight gradients of several groups: every XCD takes its eighth of each
+    // group's tiles, since a tile's time goes with its group's rows (16 groups
+    // of 32768 rows, the largest with four times the smallest's, 1536 x 4096:
+    // 439 -> 374 us).
+    const int per = ceil_div(p.m, BM) * ceil_div(p.n, BN);
+    if (WG && p.E > 1 && p.tail == 0 && per >= 64) {
+      const int lo = (int)((int64_t)per * x >> 3), n = (int)((int64_t)per * (x + 1) >> 3) - lo;
+      if (mine >= (int64_t)n * p.E) return false;
+      const int g = (int)mine / n;
+      mm_plain_tile<WG, BM, BN>(p, g * per + lo + (int)mine - g * n, t);
+      return true;
+    }
     if (mine < w1 - w0) {
       mm_plain_tile<WG, BM, BN>(p, (int)(w0 + mine), t);
       return true;
@@ -792,7 +808,30 @@ __global__ __launch_bounds__(64 * WM * WN, BM * BN > 128 * 128 ? 1 : 2) void mat
         for (int j = 0; j < 4; ++j)
           *reinterpret_cast<f32x4_t*>(blk + fr * 64 + (((4 * j + fg) ^ fr) << 2)) = acc[i < NA ? i : 0][4 * h + j];
         __builtin_amdgcn_wave_barrier();          // a wave's LDS operations complete in order
-        if (col < p.n) {
+        if (t.split >= 0 || p.out_f32) {
+          // fp32, nothing to apply: sixteen lanes to a row, so that each store
+          // covers whole lines (16 weight gradients of 1536 x 4096, 2048 rows
+          // each: 430 -> 374 us)
+          const int c4 = lane & 15, at = wn * 16 * FN + 64 * h + 4 * c4;
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            const int r = 4 * s + fg, row = wm * 32 * FM + 16 * i + r;
+            const f32x4_t v = *reinterpret_cast<const f32x4_t*>(blk + r * 64 + ((c4 ^ r) << 2));
+            if (row >= t.nrows || t.col0 + at >= p.n) continue;
+            if (t.split >= 0) {                   // partial tile [BM][BN], read again by the join
+              *reinterpret_cast<f32x4_t*>(p.parts + ((int64_t)t.part * BM + row) * BN + at) = v;
+            } else {
+              float* o = static_cast<float*>(p.out) + out_off + (row_base + row) * p.ldo + t.col0 + at;
+              if (t.col0 + at + 4 <= p.n) {
+                mm_store16(o, __builtin_bit_cast(u32x4_t, v));
+              } else {
+#pragma unroll
+                for (int q = 0; q < 3; ++q)
+                  if (t.col0 + at + q < p.n) o[q] = v[q];
+              }
+            }
+          }
+        } else if (col < p.n) {
 #pragma unroll
           for (int s = 0; s < 2; ++s) {
             const int r = 8 * s + (lane >> 3);
@@ -801,13 +840,7 @@ __global__ __launch_bounds__(64 * WM * WN, BM * BN > 128 * 128 ? 1 : 2) void mat
             const f32x4_t hi = *reinterpret_cast<const f32x4_t*>(blk + r * 64 + (((2 * ch + 1) ^ r) << 2));
             if (row < t.nrows) {
               float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-              if (t.split < 0) {
-                mm_finish8<F16>(p, v, bias, row_base + row, col, out_off);
-              } else {                            // partial tile [BM][BN]
-                float* o = p.parts + ((int64_t)t.part * BM + row) * BN + (col - t.col0);
-                *reinterpret_cast<f32x4_t*>(o) = lo;
-                *reinterpret_cast<f32x4_t*>(o + 4) = hi;
-              }
+              mm_finish8<F16>(p, v, bias, row_base + row, col, out_off);
             }
           }
         }

@@ -27,7 +27,10 @@ __device__ __forceinline__ void finish1(const MatmulArgs& p, float v, int64_t ro
   static_cast<uint16_t*>(p.out)[row * p.ldo + col] = mm_store1<F16>(v);
 }
 
-template <bool F16, int RB, int NC, int NW>
+// NT: the weights are loaded with the non-temporal hint: one group, which reads
+// them once (6144 -> 16384, one row: 36.5 -> 33.4 us; among groups some are read
+// in several passes, 64 rows over 128 experts of 2048 -> 768 23.8 -> 25.1).
+template <bool F16, int RB, int NC, int NW, bool NT>
 __global__ __launch_bounds__(64 * NW, RB * NC == 1 ? 4 : NW / 4) void matmul_stream_kernel(MatmulArgs p) {
   // an array per slot: loads into one do not hold up reads of the other
   constexpr int kSlot = 16 * NC * kStK;
@@ -68,8 +71,11 @@ __global__ __launch_bounds__(64 * NW, RB * NC == 1 ? 4 : NW / 4) void matmul_str
     auto load_w = [&](uint16_t* dst, int c) __attribute__((always_inline)) {
       const int k0 = (wave + NW * c) * kStK;
 #pragma unroll
-      for (int i = 0; i < 4 * NC; ++i)
-        mm_dma16(wr, k0 + wk[i & 3] < p.k ? wo[i] : kMmOut, (uint32_t)(2 * k0), dst + 512 * i);
+      for (int i = 0; i < 4 * NC; ++i) {
+        const uint32_t o = k0 + wk[i & 3] < p.k ? wo[i] : kMmOut;
+        if constexpr (NT) mm_dma16_nt(wr, o, (uint32_t)(2 * k0), dst + 512 * i);
+        else mm_dma16(wr, o, (uint32_t)(2 * k0), dst + 512 * i);
+      }
     };
     auto load_x = [&](u32x4_t (&x)[RB][4], int c) __attribute__((always_inline)) {
       const int k0 = (wave + NW * c) * kStK;
@@ -139,34 +145,35 @@ __global__ __launch_bounds__(64 * NW, RB * NC == 1 ? 4 : NW / 4) void matmul_str
   }
 }
 
-template <bool F16, int RB, int NC, int NW>
+template <bool F16, int RB, int NC, int NW, bool NT>
 hipError_t stream_go(const MatmulArgs& a, hipStream_t st) {
   const long long groups = a.offsets != nullptr ? (a.E < a.rows ? a.E : a.rows) : 1;
   long long grid = ((long long)a.rows / (16 * RB) + groups) * ceil_div(a.n, 16 * NC);
   grid = (grid + 7) / 8 * 8;
   if (grid > (1 << 20)) grid = 1 << 20;
-  hipLaunchKernelGGL((matmul_stream_kernel<F16, RB, NC, NW>), dim3((unsigned)grid), dim3(64 * NW), 0, st, a);
+  hipLaunchKernelGGL((matmul_stream_kernel<F16, RB, NC, NW, NT>), dim3((unsigned)grid), dim3(64 * NW), 0, st, a);
   return hipGetLastError();
 }
-// Sixteen columns and eight waves, or 32 and four.  Wider blocks read the rows
-// of x half as often; they are taken where half as many blocks still cover the
-// card and x is more than one row block, or where groups share out many rows
-// (dense, us at 1 / 17 / 32 / 48 / 64 rows: 4096 x 4096 10.4 / 11.7 / 14.3 /
-// 18.4 / 22.5 narrow, 11.3 / 13.0 / 15.2 / 18.7 / 23.3 wide; 1024 -> 8192 10.4
-// / 10.3 / 11.5 / 17.1 / 20.0 narrow, 10.7 / 10.8 / 10.7 / 11.5 / 13.6 wide;
-// one row, 6144 -> 16384 36.8 narrow, 38.2 wide; 64 rows over 128 experts of
-// 2048 -> 768 31.9 narrow, 24.2 wide).
+// Columns per block: sixteen (eight waves) for up to sixteen rows; above, as
+// many as leave about 192 blocks, since every block reads all rows of x (32
+// rows, us with 16 / 32 / 64 columns: 4096 x 4096 14.6 / 16.8 / 23.7, 16384 ->
+// 6144 77.3 / 52.0 / 70.2, 5120 -> 12288 38.2 / 38.2 / 32.9, 6144 -> 16384 47.8
+// / 47.7 / 43.3).
 template <bool F16, int RB>
-hipError_t stream_cols(const MatmulArgs& a, hipStream_t st) {
-  const bool wide = a.offsets != nullptr || (RB > 1 && a.n >= 256 * 32);
-  return wide ? stream_go<F16, RB, 2, 4>(a, st) : stream_go<F16, RB, 1, 8>(a, st);
+hipError_t stream_dense(const MatmulArgs& a, hipStream_t st) {
+  if (RB == 1 || a.n < 192 * 32) return stream_go<F16, RB, 1, 8, true>(a, st);
+  if (a.n < 192 * 64) return stream_go<F16, RB, 2, 4, true>(a, st);
+  return stream_go<F16, RB, 4, 4, true>(a, st);
 }
 template <bool F16>
 hipError_t stream_rows(const MatmulArgs& a, hipStream_t st) {
-  if (a.offsets != nullptr || a.rows <= 16) return stream_cols<F16, 1>(a, st);
-  if (a.rows <= 32) return stream_cols<F16, 2>(a, st);
-  if (a.rows <= 48) return stream_cols<F16, 3>(a, st);
-  return stream_cols<F16, 4>(a, st);
+  // groups of a row or two: 32 columns (64 rows over 128 experts of 2048 ->
+  // 768 24.2 us, 31.9 with sixteen)
+  if (a.offsets != nullptr) return stream_go<F16, 1, 2, 4, false>(a, st);
+  if (a.rows <= 16) return stream_dense<F16, 1>(a, st);
+  if (a.rows <= 32) return stream_dense<F16, 2>(a, st);
+  if (a.rows <= 48) return stream_dense<F16, 3>(a, st);
+  return stream_dense<F16, 4>(a, st);
 }
 
 }  // namespace
