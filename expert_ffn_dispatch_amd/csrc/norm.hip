@@ -421,13 +421,26 @@ hipError_t backward_type(const NormArgs& a, float* part, hipStream_t st) {
 
 }  // namespace
 
-hipError_t launch_norm_forward(const NormArgs& a, hipStream_t st) {
-  if (a.rows == 0) return hipSuccess;
-  switch (a.type) {
-    case kTypeBf16: return forward_type<NormElem<kTypeBf16>>(a, st);
-    case kTypeF16: return forward_type<NormElem<kTypeF16>>(a, st);
-    default: return forward_type<NormElem<kTypeF32>>(a, st);
+hipError_t launch_norm_forward(const NormArgs& all, hipStream_t st) {
+  // a launch takes at most 2^21 rows (of up to 1024 threads: 2^31)
+  constexpr int kMost = 1 << 21;
+  const int64_t size = all.type == kTypeF32 ? 4 : 2;
+  for (int r0 = 0; r0 < all.rows; r0 += kMost) {
+    NormArgs a = all;
+    a.rows = all.rows - r0 < kMost ? all.rows - r0 : kMost;
+    a.x = static_cast<const char*>(all.x) + r0 * all.ldx * size;
+    a.out = static_cast<char*>(all.out) + r0 * all.ldo * size;
+    if (all.mean) a.mean = all.mean + r0;
+    if (all.rstd) a.rstd = all.rstd + r0;
+    hipError_t e;
+    switch (a.type) {
+      case kTypeBf16: e = forward_type<NormElem<kTypeBf16>>(a, st); break;
+      case kTypeF16: e = forward_type<NormElem<kTypeF16>>(a, st); break;
+      default: e = forward_type<NormElem<kTypeF32>>(a, st); break;
+    }
+    if (e != hipSuccess) return e;
   }
+  return hipSuccess;
 }
 
 size_t norm_backward_workspace_bytes(int64_t rows, int64_t cols) {

@@ -163,6 +163,17 @@ def test_norm_strides(cols, pad, shift):
         check(q, p.double(), 2 * u(BF) * p.double().abs() + 1e-5, "gradient")
 
 
+def test_norm_many_rows():
+    """More rows than one launch takes."""
+    g = gen(12)
+    x = randn(g, 2 ** 21 + 5, 8)
+    y, mean, rstd = moe.moe_layer_norm(x, want_stats=True)
+    ref, mu, rs, n = norm_ref(x, None, None, 1e-5, False)
+    scale = x.double().abs().max(1).values
+    check(mean, mu, FUN * scale + 1e-30, "mean")
+    check(y, ref, u(BF) * ref.abs() + FUN * (1 + (scale * rs)[:, None]) * (n.abs() + 1), "y")
+
+
 def test_norm_in_place_and_empty():
     g = gen(1)
     x = randn(g, 300, 640)
@@ -204,7 +215,8 @@ def act_grad_ref(z, act):
 ACTS = ["none", "relu", "gelu", "gelu_tanh", "silu"]
 # rows, in, out: one token, ragged tiles, odd widths, several tiles, contraction slices
 LIN_SHAPES = [(1, 64, 64), (1, 2048, 512), (3, 1, 1), (2, 7, 5), (17, 72, 40), (37, 512, 256), (64, 1000, 136),
-              (130, 264, 392), (129, 65, 131), (300, 4096, 64), (257, 768, 512), (1, 4097, 33)]
+              (130, 264, 392), (129, 65, 131), (300, 4096, 64), (257, 768, 512), (1, 4097, 33), (700, 1001, 1003), (333, 1003, 96),
+              (40, 1536, 6200), (33, 256, 12400)]
 
 
 @pytest.mark.parametrize("act", ACTS)
@@ -294,6 +306,36 @@ def test_linear_strides(n_in, n_out, pad, shift):
         check(q, p.double(), 2 * u(BF) * p.double().abs() + 1e-4, "gradient")
 
 
+@pytest.mark.parametrize("rows", [1, 20, 64])
+def test_linear_few_rows_misaligned(rows):
+    """Shapes for the kernel of a few rows whose pointers do not suit it."""
+    g = gen(rows)
+    x, w = randn(g, rows, 256), randn(g, 96, 256, scale=0.06)
+    ref = x.double() @ w.double().T
+    tol = u(BF) * ref.abs() + 1.01 * 256 * ACC * x.double().abs() @ w.double().abs().T + tiny(BF)
+    check(moe.moe_linear(x, w), ref, tol, "aligned")
+    check(moe.moe_linear(strided(x, 8, 1), w), ref, tol, "x")
+    check(moe.moe_linear(x, strided(w, 8, 3)), ref, tol, "w")
+    check(moe.moe_linear(strided(x, 3, 1), strided(w, 5, 2)), ref, tol, "both")
+
+
+@pytest.mark.parametrize("rows,n_in,n_out", [(4400, 1024, 4400), (2200, 512, 4000), (4001, 520, 4361)])
+def test_linear_rounds_with_a_cut_tail(rows, n_in, n_out):
+    """More tiles than the card has CUs, the last round of them cut along the contraction."""
+    g = gen(rows)
+    x, w, b = randn(g, rows, n_in), randn(g, n_out, n_in, scale=n_in ** -0.5), randn(g, n_out)
+    X, W = x.double(), w.double()
+    ref = X @ W.T + b.double()
+    check(moe.moe_linear(x, w, b), ref, u(BF) * ref.abs() + 1.01 * (n_in + 2) * ACC * (X.abs() @ W.abs().T + b.double().abs())
+          + tiny(BF), "y")
+    dy = randn(g, rows, n_out)
+    dx, dw, db = moe.moe_linear_backward(dy, x, w, want_dbias=True, dw_dtype=F32)
+    D = dy.double()
+    check(dx, D @ W, u(BF) * (D @ W).abs() + 1.01 * n_out * ACC * D.abs() @ W.abs() + tiny(BF), "dx")
+    check(dw, D.T @ X, u(F32) * (D.T @ X).abs() + rows * ACC * D.abs().T @ X.abs(), "dw")
+    check(db, D.sum(0), u(BF) * D.sum(0).abs() + (rows + 8) * ACC * D.abs().sum(0) + tiny(BF), "dbias")
+
+
 def test_linear_residual_in_place_and_empty():
     g = gen(5)
     x, w, r = randn(g, 50, 64), randn(g, 80, 64), randn(g, 50, 80)
@@ -321,7 +363,7 @@ def offsets_of(counts, first=0):
 GROUPS = [
     ([5], 64, 64), ([1], 1, 1), ([0], 40, 24), ([0, 0, 3, 0], 72, 136), ([1] * 7, 128, 256), ([130, 0, 1, 33, 257], 192, 264),
     ([31, 32, 33, 0, 64, 65, 127, 128, 129], 256, 128), ([3, 9, 0, 2], 65, 131), ([700, 0, 2, 600], 512, 320),
-    ([2] * 256, 64, 72), ([0] * 100 + [50] + [0] * 59, 128, 128), ([20] * 16, 1024, 768),
+    ([2] * 256, 64, 72), ([300, 0, 77], 2048, 2048), ([120, 200], 2056, 1999), ([0] * 100 + [50] + [0] * 59, 128, 128), ([20] * 16, 1024, 768),
 ]
 
 
