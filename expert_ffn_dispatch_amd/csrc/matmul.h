@@ -6,6 +6,23 @@
 //   weight grad  dW_e[r][c]  = sum_k dy[k][r] x[k][c],  k over e's rows
 // An operand is stored with k contiguous ("KC": x, dy and W of the first
 // form) or with k as its row index ("KS": W of the second, both of the third).
+//
+// One kernel: a block multiplies BM x BN tiles over 64-wide stages of k that go
+// straight into LDS (columns two stages ahead in three buffers, rows one ahead
+// in two), 16x16x32 MFMA, sums in fp32 registers, one rounding at the store.
+// KS operands are turned by LDS's transposing reads, so no form needs a
+// transposed copy.  Resident blocks start their next tile's loads before they
+// store the last one.
+//
+// Bound by the matrix pipes, whose clock falls with the power that the
+// operands' switching costs: 8192 x 8192 x 8192 takes 773 us (1.42 PFLOP/s) of
+// random bf16 values and 627 us (1.75) of zeros.  With 32x32x16 MFMA and with
+// products not in snake order (below) a loop of products on registers alone
+// reached 1.68 PFLOP/s on random values, with 16x16x32 in snake order 1.95.
+// 256 x 256 tiles (8 waves of 128 x 64) read 1/128 of an operand byte per flop
+// and fill one CU each; 128 x 128 tiles (4 waves of 64 x 64, two blocks a CU)
+// fill the card with a quarter of the work.  Four waves of 128 x 128 each,
+// and tiles of 128 x 256, were slower at every size tried.
 #pragma once
 #include <type_traits>
 
@@ -15,7 +32,6 @@
 namespace moe {
 
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
-typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kMmK = 64;                          // contraction per stage
@@ -383,8 +399,8 @@ __device__ __forceinline__ void mm_plain_tile(const MatmulArgs& p, int i, MmTile
 // which wait for their weights' bytes, or only large ones (4096 x 1536, 65536
 // rows over 128 experts whose loads fall as rank^-1.2: 859 -> 814 us; evenly
 // filled 803 -> 797).  Dense lists keep the eighths, whose cut
-// slices then meet their operands in L2 (linear gradients of 16384 x 4096 x
-// 1536: 427 us against 444).
+// slices then meet their operands in L2 (both linear gradients of 4000 x 5120 x
+// 5120: 427 us against 444).
 template <bool WG, int BM, int BN>
 __device__ __forceinline__ bool mm_find_tile(const MatmulArgs& p, int lane, int step, MmTile& t) {
   const int x = blockIdx.x & 7;

@@ -43,8 +43,10 @@ hipError_t launch_join(const MatmulArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
-// act'(z) in fp32.
+// act'(z) in fp32.  Past |z| = 128 every form is 0 or 1 to the last bit, and z
+// is cut there: powers of a larger z overflow, and inf times 0 is no number.
 __device__ __forceinline__ float act_grad(float z, int act) {
+  if (fabsf(z) > 128.f) z = copysignf(128.f, z);
   switch (act) {
     case kActRelu: return z > 0.f ? 1.f : 0.f;
     case kActGelu:

@@ -2,6 +2,8 @@
  * moe_ffn.h - C ABI of one Mixture-of-Experts FFN layer on an AMD Instinct
  * MI355X (gfx950): router -> softmax -> top-k -> dispatch / permutation ->
  * grouped SwiGLU expert GEMM (+ shared experts) -> combine / unpermutation.
+ * The last section holds what stands around it in a block and in training:
+ * layer norm, linear layers and products grouped by expert, with gradients.
  *
  * Sources.  The steps are those the page "MoE 少算 FLOPs，延迟反而涨了：慢在搬
  * token 的路上" (wink.run) lays out in its sections "dense 和 MoE 的差别" (the router
@@ -361,11 +363,14 @@ int moe_set_stage_events(void* const* events, int n);
  * by expert, each with its gradients: what a block needs beside moe_layer, and
  * what training its experts needs.  The conventions above hold, except:
  *  - types are given per call (moe_dtype); pointers need only their element's
- *    alignment.  Rows may be strided: ld_* is the distance of two rows in
- *    elements (0 = packed), at least the row's width and at most 2^20;
- *    elements of a row are contiguous.  Rows of 16-byte pitch and alignment
- *    whose widths are multiples of 8 take the fast loads, all others a path
- *    that loads element by element.
+ *    alignment (the workspace 16 bytes).  Rows may be strided: ld_* is the
+ *    distance of two rows in elements (0 = packed), at least the row's width
+ *    and at most 2^20; elements of a row are contiguous.  The products' fast
+ *    loads need operands whose pointer and row pitch are multiples of 16 bytes
+ *    and whose width is a multiple of 8; others are copied into the workspace
+ *    with padded rows where that pays (dense forms and weight gradients), or
+ *    take a slower path.  Results differ between those only in the order of
+ *    their fp32 sums.  The norms and the stores take any alignment.
  *  - rows = 0 is allowed: outputs with a row per input row are left alone,
  *    gradients summed over rows are set to zero.
  *  - outputs must not overlap inputs unless stated.

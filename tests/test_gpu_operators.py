@@ -285,6 +285,29 @@ def test_linear_gradient_against_differences():
         check(db, G.sum(0), 1e-4 * (1 + dy.double().abs().sum(0)), "dbias " + act)
 
 
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("act", ACTS[1:])
+def test_linear_activation_at_large_values(act, dtype):
+    """Far out an activation is z or 0 and its slope 1 or 0, exactly; NaN stays NaN."""
+    top = float(torch.finfo(dtype).max)
+    z = torch.tensor([129.0, 300.0, 1e4, 6e4, min(1e20, top), top, top / 3, 200.0], device=DEV).to(dtype)
+    z = torch.stack([z, -z])
+    eye = torch.eye(8, dtype=dtype, device=DEV)
+    y, pre = moe.moe_linear(z, eye, act=act, want_pre=True)
+    assert torch.equal(pre, z) and torch.equal(y, z.clamp(min=0))
+    pre = torch.cat([z, torch.full_like(z[:1], float("inf")), torch.full_like(z[:1], float("-inf"))])
+    dx, dw, db = moe.moe_linear_backward(torch.ones_like(pre), pre.clamp(-1, 1), eye, pre, act=act, want_dbias=True,
+                                         bias_dtype=F32)
+    slope = (pre > 0).to(dtype)
+    assert torch.equal(dx, slope) and torch.equal(db, slope.float().sum(0))
+    assert torch.equal(dw, torch.full_like(eye, 2.0))     # two rows of slope 1 and x = 1
+    pre[1, 3] = float("nan")
+    dx = moe.moe_linear_backward(torch.ones_like(pre), pre.clamp(-1, 1), eye, pre, act=act)[0]
+    if act != "relu":                             # whose slope is that of z > 0
+        assert torch.isnan(dx[1, 3])
+    assert torch.equal(dx[0], slope[0])
+
+
 @pytest.mark.parametrize("n_in,n_out,pad,shift", [(128, 192, 8, 0), (128, 192, 3, 0), (136, 72, 16, 8), (96, 64, 8, 1),
                                                   (77, 51, 2, 3)])
 def test_linear_strides(n_in, n_out, pad, shift):
