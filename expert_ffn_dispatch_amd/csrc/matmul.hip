@@ -32,7 +32,7 @@ __global__ __launch_bounds__(256) void matmul_join_kernel(MatmulArgs p) {
   }
   float bias[8];
   mm_bias8<F16>(p, col, bias);
-  mm_finish8<F16>(p, v, bias, (int64_t)t.row0 + row, col, WG ? (int64_t)t.e * p.out_group : 0);
+  mm_finish8<F16, !WG>(p, v, bias, (int64_t)t.row0 + row, col, WG ? (int64_t)t.e * p.out_group : 0);
 }
 
 template <bool WG, int B>
@@ -52,19 +52,15 @@ __device__ __forceinline__ void logistic(float u, float& s, float& c) {
 
 // act'(z) in fp32.  Past |z| = 128 every form is 0 or 1 to the last bit, and z
 // is cut there: powers of a larger z overflow, and inf times 0 is no number.
-// The normal distribution of gelu is the fifth-order form of Abramowitz and
-// Stegun 7.1.26 (absolute error 0.75e-7, a rounding of fp32), which shares the
-// density's exponential (gradients of 4000 x 5120 x 64: 84.0 us with the library's
-// error function, 72.7 so, relu 69.7).
+// Gelu's distribution and density share an exponential (gradients of 4000 x
+// 5120 x 64: 84.0 us with the library's error function, 72.7 so, relu 69.7).
 __device__ __forceinline__ float act_grad(float z, int act) {
   if (fabsf(z) > 128.f) z = copysignf(128.f, z);
   switch (act) {
     case kActRelu: return z > 0.f ? 1.f : 0.f;
     case kActGelu: {
-      const float e = __expf(-0.5f * z * z), t = __builtin_amdgcn_rcpf(1.f + 0.23164189f * fabsf(z));
-      const float h = t * (0.127414796f + t * (-0.142248368f + t * (0.710706871f + t * (-0.726576014f + t * 0.530702715f))));
-      const float tail = h * e;                   // distribution at -|z|
-      return (z < 0.f ? tail : 1.f - tail) + z * 0.39894228040143268f * e;
+      const float e = __expf(-0.5f * z * z);
+      return mm_normal(z, e) + z * 0.39894228040143268f * e;
     }
     case kActGeluTanh: {
       // z s(2u), s the logistic function: s + z s (1 - s) 2u'

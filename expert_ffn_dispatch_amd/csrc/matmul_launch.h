@@ -4,7 +4,7 @@
 #include "matmul.h"
 namespace moe {
 
-template <bool F16, bool AKC, bool BKC, int BM, int BN, int WM, int WN, bool ALIGNED>
+template <bool F16, bool AKC, bool BKC, int BM, int BN, int WM, int WN, bool ALIGNED, bool EPI>
 hipError_t launch_matmul_tile(const MatmulArgs& a, hipStream_t st) {
   constexpr bool WG = !AKC;
   const long long NT = ceil_div(a.n, BN);
@@ -20,16 +20,25 @@ hipError_t launch_matmul_tile(const MatmulArgs& a, hipStream_t st) {
   constexpr long long kResident = 256 * (BM * BN > 128 * 128 ? 1 : 2);
   if (grid > kResident) grid = kResident;
   if (grid <= 0) return hipSuccess;
-  hipLaunchKernelGGL((matmul_tile_kernel<F16, AKC, BKC, BM, BN, WM, WN, ALIGNED>), dim3((unsigned)grid),
+  hipLaunchKernelGGL((matmul_tile_kernel<F16, AKC, BKC, BM, BN, WM, WN, ALIGNED, EPI>), dim3((unsigned)grid),
                      dim3(64 * WM * WN), 0, st, a);
   return hipGetLastError();
 }
 
+template <bool F16, bool AKC, bool BKC, bool EPI>
+hipError_t launch_matmul_sizes(const MatmulArgs& a, hipStream_t st) {
+  if (!a.aligned) return launch_matmul_tile<F16, AKC, BKC, 128, 128, 2, 2, false, EPI>(a, st);
+  if (a.big) return launch_matmul_tile<F16, AKC, BKC, 256, 256, 2, 4, true, EPI>(a, st);
+  return launch_matmul_tile<F16, AKC, BKC, 128, 128, 2, 2, true, EPI>(a, st);
+}
+
 template <bool F16, bool AKC, bool BKC>
 hipError_t launch_matmul_form(const MatmulArgs& a, hipStream_t st) {
-  if (!a.aligned) return launch_matmul_tile<F16, AKC, BKC, 128, 128, 2, 2, false>(a, st);
-  if (a.big) return launch_matmul_tile<F16, AKC, BKC, 256, 256, 2, 4, true>(a, st);
-  return launch_matmul_tile<F16, AKC, BKC, 128, 128, 2, 2, true>(a, st);
+  if constexpr (AKC && BKC) {                     // gradients have nothing to apply
+    if (a.bias != nullptr || a.pre != nullptr || a.act != kActNone || a.residual != nullptr)
+      return launch_matmul_sizes<F16, AKC, BKC, true>(a, st);
+  }
+  return launch_matmul_sizes<F16, AKC, BKC, false>(a, st);
 }
 
 }  // namespace moe

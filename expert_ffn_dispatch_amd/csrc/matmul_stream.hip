@@ -24,7 +24,9 @@ __device__ __forceinline__ void finish1(const MatmulArgs& p, float v, int64_t ro
   if (p.bias != nullptr)
     v += p.bias_f32 ? static_cast<const float*>(p.bias)[col] : mm_load1<F16>(static_cast<const uint16_t*>(p.bias)[col]);
   if (p.pre != nullptr) p.pre[row * p.ldp + col] = mm_store1<F16>(v);
-  v = mm_act(v, p.act);
+  float z[1] = {v};
+  mm_act(z, p.act);
+  v = z[0];
   if (p.residual != nullptr) v += mm_load1<F16>(p.residual[row * p.ldr + col]);
   static_cast<uint16_t*>(p.out)[row * p.ldo + col] = mm_store1<F16>(v);
 }
