@@ -95,6 +95,9 @@ __device__ __forceinline__ u32x4_t load8(const uint16_t* p, int n) {
 // keep fp32 sums of their columns, which the waves add up in LDS; partial sums
 // [runs][n], and dbias_join_kernel adds the runs in order.
 // g has a row pitch of ldg; columns n..ldg-1 become zeros.
+// g is rounded to the operands' 16 bits, which is what the matrix instruction
+// takes (a second term for the rest would double both products); the bias
+// gradient sums the unrounded values.
 template <bool F16>
 __global__ __launch_bounds__(256) void act_grad_kernel(ActGradArgs p, float* part, int run) {
   __shared__ float s_sum[4][512];
