@@ -248,11 +248,32 @@ Plan matmul_plan(MatmulForm f, int E, int64_t rows, int64_t m, int64_t n, int64_
 namespace {
 
 // out[r] = in[r], widened to `pitch` with zeros; a thread moves eight columns.
+// With groups (offsets [E+1], as mm_bounds clamps them) only the rows from the
+// first group's first to the last group's last: the others belong to no
+// product, and are neither read nor worth the time.
 __global__ __launch_bounds__(256) void pack_kernel(const uint16_t* in, int64_t ld, int64_t rows, int width,
-                                                   uint16_t* out, int pitch) {
+                                                   uint16_t* out, int pitch, const int32_t* offsets, int E) {
   const int chunks = pitch / 8;
-  const int64_t total = rows * chunks;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+  int64_t first = 0, end = rows;
+  if (offsets != nullptr) {
+    // every wave looks through the offsets itself (at most five a lane); where
+    // they decrease the groups' rows still lie between the least and the greatest
+    int lo = (int)rows, hi = 0;
+    for (int e = threadIdx.x & 63; e <= E; e += 64) {
+      const int o = min(max(offsets[e], 0), (int)rows);
+      if (e < E) lo = min(lo, o);
+      hi = max(hi, o);
+    }
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) {
+      lo = min(lo, __shfl_xor(lo, d));
+      hi = max(hi, __shfl_xor(hi, d));
+    }
+    first = lo;
+    end = hi;
+  }
+  for (int64_t i = first * chunks + (int64_t)blockIdx.x * 256 + threadIdx.x; i < end * chunks;
+       i += (int64_t)gridDim.x * 256) {
     const int64_t r = i / chunks;
     const int c = (int)(i - r * chunks) * 8;
     *reinterpret_cast<u32x4_t*>(out + r * pitch + c) = load8(in + r * ld + c, width - c);
@@ -295,10 +316,11 @@ Packing packing(MatmulForm f, const MatmulArgs& q) {
   k.bytes_b = b ? up256(nb) : 0;
   return k;
 }
-hipError_t launch_pack(const uint16_t* in, int64_t ld, int64_t rows, int width, void* out, int pitch, hipStream_t st) {
+hipError_t launch_pack(const uint16_t* in, int64_t ld, int64_t rows, int width, void* out, int pitch,
+                       const int32_t* offsets, int E, hipStream_t st) {
   const int64_t blocks = (rows * (pitch / 8) + 255) / 256;
   hipLaunchKernelGGL(pack_kernel, dim3((unsigned)(blocks < 16384 ? blocks : 16384)), dim3(256), 0, st, in, ld, rows,
-                     width, static_cast<uint16_t*>(out), pitch);
+                     width, static_cast<uint16_t*>(out), pitch, offsets, E);
   return hipGetLastError();
 }
 bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -323,12 +345,12 @@ hipError_t launch_matmul(MatmulForm f, MatmulArgs a, void* ws, hipStream_t st) {
   char* w = static_cast<char*>(ws);
   if (a.aligned && a.rows > 0) {
     if (k.a) {
-      if (hipError_t e = launch_pack(a.a, a.lda, k.ra, k.wa, w, k.pa, st)) return e;
+      if (hipError_t e = launch_pack(a.a, a.lda, k.ra, k.wa, w, k.pa, a.offsets, a.E, st)) return e;
       a.a = reinterpret_cast<const uint16_t*>(w);
       a.lda = k.pa;
     }
     if (k.b) {
-      if (hipError_t e = launch_pack(a.b, a.ldb, k.rb, k.wb, w + k.bytes_a, k.pb, st)) return e;
+      if (hipError_t e = launch_pack(a.b, a.ldb, k.rb, k.wb, w + k.bytes_a, k.pb, a.offsets, a.E, st)) return e;
       a.b = reinterpret_cast<const uint16_t*>(w + k.bytes_a);
       a.ldb = k.pb;
     }

@@ -1,0 +1,50 @@
+"""Layer norm, linear layers and products grouped by expert on the paths that
+calls of ordinary sizes take, against the formulas in 64 bits.  Tolerances
+count roundings as in test_gpu_operators.py."""
+import ctypes
+
+import pytest
+import torch
+
+import expert_ffn_dispatch_amd as moe
+from expert_ffn_dispatch_amd import _lib
+from test_gpu_operators import ACC, DEV, check, gen, randn
+
+pytestmark = pytest.mark.gpu
+
+
+def call(fn, query, d, args, ws):
+    """A C entry point with a workspace of the caller's."""
+    n = ctypes.c_size_t(0)
+    _lib.check(query(ctypes.byref(d), ctypes.byref(n)))
+    assert n.value <= ws.numel()
+    _lib.check(fn(ctypes.byref(d), *args, ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream))
+
+
+@pytest.mark.parametrize("offsets", [[1000, 2500, 2500, 5000, 6000], [0, 20000, 20000, 20000, 20000], [7] * 5, [6000, 100, 4000, 50, 9000]])
+def test_weight_gradient_leaves_rows_outside_the_groups_unread(offsets):
+    """Odd widths: the operands are copied with padded rows, the rows of the groups alone."""
+    g = gen(sum(offsets))
+    rows, E, n_in, n_out = 20000, 4, 1001, 1003
+    x, dy = randn(g, rows, n_in), randn(g, rows, n_out)
+    off = torch.tensor(offsets, dtype=torch.int32, device=DEV)
+    dw = torch.empty(E, n_out, n_in, device=DEV)
+    d = _lib.MoeGroupedDims(rows, E, n_in, n_out, _lib.MOE_DTYPE_BF16, _lib.MOE_DTYPE_F32, 0, 0)
+    lib = _lib.load()
+    ws = torch.full((1 << 28,), 0x5A, dtype=torch.uint8, device=DEV)
+    call(lib.moe_grouped_matmul_wgrad, lib.moe_grouped_matmul_wgrad_workspace_bytes, d,
+         (dy.data_ptr(), x.data_ptr(), off.data_ptr(), dw.data_ptr()), ws)
+    spans = []
+    for e in range(E):
+        lo = offsets[e]
+        spans.append((lo, max(lo, offsets[e + 1])))
+    first, end = min(lo for lo, _ in spans), max(hi for _, hi in spans)
+    # rows of 1024 at the front of the workspace: dy's copy, then x's
+    copies = ws[:2 * rows * 2048].view(torch.int16).view(2, rows, 1024)
+    for t, w in ((copies[0], dy), (copies[1], x)):
+        assert torch.equal(t[first:end, :w.shape[1]], w[first:end].view(torch.int16)), "the operands are not copied as this test takes it"
+        assert (t[:first] == 0x5A5A).all() and (t[end:] == 0x5A5A).all(), "rows outside the groups were read"
+    for e, (lo, hi) in enumerate(spans):
+        D, X = dy[lo:hi].double(), x[lo:hi].double()
+        ref = D.T @ X
+        check(dw[e], ref, 2.0 ** -24 * ref.abs() + (hi - lo + 1) * ACC * D.abs().T @ X.abs() + 1e-30, f"dw {e}")
