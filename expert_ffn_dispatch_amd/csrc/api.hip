@@ -81,7 +81,7 @@ int check_dims(const char* fn, const moe_dims* d, bool need_router_shape) {
   return MOE_OK;
 }
 
-size_t align_up(size_t v) { return (v + 255) & ~size_t(255); }
+size_t align_up(size_t v) { return (v + MOE_WORKSPACE_ALIGN - 1) & ~size_t(MOE_WORKSPACE_ALIGN - 1); }
 
 struct Carver {
   char* base;
@@ -192,8 +192,8 @@ int num_cus() {
 int check_ws(const char* fn, void* ws, size_t ws_bytes, size_t need) {
   if (need == 0) return MOE_OK;
   if (ws == nullptr) return fail(MOE_ERR_WORKSPACE, "%s: workspace is NULL (%zu bytes needed)", fn, need);
-  if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
-    return fail(MOE_ERR_WORKSPACE, "%s: workspace must be 256-byte aligned", fn);
+  if (reinterpret_cast<uintptr_t>(ws) % MOE_WORKSPACE_ALIGN != 0)
+    return fail(MOE_ERR_WORKSPACE, "%s: workspace must be %d-byte aligned", fn, MOE_WORKSPACE_ALIGN);
   if (ws_bytes < need)
     return fail(MOE_ERR_WORKSPACE, "%s: workspace has %zu bytes, %zu needed", fn, ws_bytes, need);
   return MOE_OK;

@@ -20,7 +20,7 @@
  * Conventions for every entry point:
  *  - Pointers are DEVICE pointers unless marked host.  The caller owns every
  *    buffer; the library allocates and frees nothing.  All pointers must be
- *    16-byte aligned.
+ *    16-byte aligned, workspaces MOE_WORKSPACE_ALIGN bytes.
  *  - bf16 arrays are raw bfloat16 bit patterns (moe_bf16).  Matrices are
  *    row-major.  Expert weights are [out, in] (the contraction dimension is
  *    contiguous): w_gate/w_up [E][H][M], w_down [E][M][H].  The router is
@@ -54,6 +54,9 @@ extern "C" {
 
 #define MOE_FFN_ABI_VERSION 1
 
+/* Alignment of every workspace, in bytes. */
+#define MOE_WORKSPACE_ALIGN 256
+
 typedef uint16_t moe_bf16;   /* raw bfloat16 bits */
 typedef uint8_t moe_fp8;     /* raw OCP FP8 E4M3 bits */
 typedef void* moe_stream;    /* a hipStream_t */
@@ -72,7 +75,7 @@ enum moe_status {
   MOE_OK = 0,
   MOE_ERR_INVALID = 1,      /* a NULL/misaligned pointer or out-of-range size      */
   MOE_ERR_UNSUPPORTED = 2,  /* a valid request this build does not implement       */
-  MOE_ERR_WORKSPACE = 3,    /* workspace missing or smaller than required          */
+  MOE_ERR_WORKSPACE = 3,    /* workspace missing, misaligned or too small          */
   MOE_ERR_DEVICE = 4        /* HIP reported an error (launch or device query)      */
 };
 
@@ -363,14 +366,15 @@ int moe_set_stage_events(void* const* events, int n);
  * by expert, each with its gradients: what a block needs beside moe_layer, and
  * what training its experts needs.  The conventions above hold, except:
  *  - types are given per call (moe_dtype); pointers need only their element's
- *    alignment (the workspace 16 bytes).  Rows may be strided: ld_* is the
- *    distance of two rows in elements (0 = packed), at least the row's width
- *    and at most 2^20; elements of a row are contiguous.  The products' fast
- *    loads need operands whose pointer and row pitch are multiples of 16 bytes
- *    and whose width is a multiple of 8; others are copied into the workspace
- *    with padded rows where that pays (dense forms and weight gradients), or
- *    take a slower path.  Results differ between those only in the order of
- *    their fp32 sums.  The norms and the stores take any alignment.
+ *    alignment (workspaces MOE_WORKSPACE_ALIGN bytes as above).  Rows may be
+ *    strided: ld_* is the distance of two rows in elements (0 = packed), at
+ *    least the row's width and at most 2^20; elements of a row are contiguous.
+ *    The products' fast loads need operands whose pointer and row pitch are
+ *    multiples of 16 bytes and whose width is a multiple of 8; others are
+ *    copied into the workspace with padded rows where that pays (dense forms
+ *    and weight gradients), or take a slower path.  Results differ between
+ *    those only in the order of their fp32 sums.  The norms and the stores take
+ *    any alignment.
  *  - rows = 0 is allowed: outputs with a row per input row are left alone,
  *    gradients summed over rows are set to zero.
  *  - outputs must not overlap inputs unless stated.
