@@ -53,7 +53,7 @@ __device__ __forceinline__ void logistic(float u, float& s, float& c) {
 // act'(z) in fp32.  Past |z| = 128 every form is 0 or 1 to the last bit, and z
 // is cut there: powers of a larger z overflow, and inf times 0 is no number.
 // Gelu's distribution and density share an exponential (gradients of 4000 x
-// 5120 x 64: 84.0 us with the library's error function, 72.7 so, relu 69.7).
+// 64 -> 5120: 68 us, relu 64; with the library's error function 11 more).
 __device__ __forceinline__ float act_grad(float z, int act) {
   if (fabsf(z) > 128.f) z = copysignf(128.f, z);
   switch (act) {

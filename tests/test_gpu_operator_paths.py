@@ -2,13 +2,14 @@
 calls of ordinary sizes take, against the formulas in 64 bits.  Tolerances
 count roundings as in test_gpu_operators.py."""
 import ctypes
+import math
 
 import pytest
 import torch
 
 import expert_ffn_dispatch_amd as moe
 from expert_ffn_dispatch_amd import _lib
-from test_gpu_operators import ACC, DEV, check, gen, randn
+from test_gpu_operators import ACC, BF, DEV, F32, check, gen, randn, u
 
 pytestmark = pytest.mark.gpu
 
@@ -48,3 +49,39 @@ def test_weight_gradient_leaves_rows_outside_the_groups_unread(offsets):
         D, X = dy[lo:hi].double(), x[lo:hi].double()
         ref = D.T @ X
         check(dw[e], ref, 2.0 ** -24 * ref.abs() + (hi - lo + 1) * ACC * D.abs().T @ X.abs() + 1e-30, f"dw {e}")
+
+
+# ------------------------------------------------------------------- gelu
+
+def normal(z):
+    """Distribution and density in 64 bits, the distribution without 1 + erf."""
+    return 0.5 * torch.special.erfc(-z * 0.5 ** 0.5), torch.exp(-0.5 * z * z) * (2 * math.pi) ** -0.5
+
+
+def gelu_rel(z):
+    """Relative error of the distribution and density in fp32: the tail's eight powers 2^-20, the fast exponential of
+    z^2 / 2 twice 2^-24 of its argument, and four roundings."""
+    return 2.0 ** -20 + (z * z / 2 + 4) * 2.0 ** -23
+
+
+@pytest.mark.parametrize("rows", [50, 400])
+def test_gelu_keeps_its_bits_far_out(rows):
+    """Values from -12.5 to 12.5, down to 1e-34, each within its rounding (the kernels for few rows and of tiles)."""
+    z = torch.linspace(-12.5, 12.5, rows * 16, device=DEV).to(BF).view(rows, 16)
+    y = moe.moe_linear(z, torch.eye(16, dtype=BF, device=DEV), act="gelu")
+    Z = z.double()
+    ref = Z * normal(Z)[0]
+    check(y, ref, (u(BF) + gelu_rel(Z)) * ref.abs(), "gelu")
+
+
+def test_gelu_slope_keeps_its_bits_far_out():
+    """The bias gradient of one row is the slope itself, in fp32."""
+    n = 4000
+    z = torch.linspace(-12.5, 12.5, n, device=DEV).to(BF)[None]
+    one = torch.ones_like(z)
+    dx, dw, db = moe.moe_linear_backward(one, z[:, :8].contiguous(), one.view(n, 1).expand(n, 8).contiguous(), z, act="gelu",
+                                         want_dx=False, want_dw=False, want_dbias=True, bias_dtype=F32)
+    assert dx is None and dw is None
+    Z = z[0].double()
+    P, p = normal(Z)
+    check(db, P + Z * p, gelu_rel(Z) * (P + Z.abs() * p), "slope")
