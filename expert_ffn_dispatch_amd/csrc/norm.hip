@@ -251,17 +251,25 @@ __global__ __launch_bounds__(BLK) void norm_backward_kernel(NormArgs p, float* p
     if constexpr (kAhead) fetch(row + step, xn, dn, mun, rsn);
     else fetch(row, x, d, mu, rs);
     float s1 = 0.f, s2 = 0.f;
+    auto add = [&](int i, int q) __attribute__((always_inline)) {
+      const float dyv = d.get(i, q), n = (x.get(i, q) - mu) * rs, gv = dyv * g[i][q];
+      s1 += gv;
+      s2 += gv * n;
+      dg[i][q] += dyv * n;
+      db[i][q] += dyv;
+    };
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
+      // nothing past the last column: dy is zero there, but -mu rstd, and so
+      // what it adds, need not be finite where n is; a row past the end adds zeros
+      const int left = p.cols - norm_col(i, t, tpr);
+      if (left >= 8) {
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        // past the last column and row dy is zero, and so is what it adds (n
-        // is finite there unless the whole row's gradient is not)
-        const float dyv = d.get(i, q), n = (x.get(i, q) - mu) * rs, gv = dyv * g[i][q];
-        s1 += gv;
-        s2 += gv * n;
-        dg[i][q] += dyv * n;
-        db[i][q] += dyv;
+        for (int q = 0; q < 8; ++q) add(i, q);
+      } else if (left > 0) {
+#pragma unroll
+        for (int q = 0; q < 7; ++q)
+          if (q < left) add(i, q);
       }
     }
     float m1 = wave_sum(s1), m2 = wave_sum(s2);

@@ -85,3 +85,35 @@ def test_gelu_slope_keeps_its_bits_far_out():
     Z = z[0].double()
     P, p = normal(Z)
     check(db, P + Z * p, gelu_rel(Z) * (P + Z.abs() * p), "slope")
+
+
+# ------------------------------------------------------------------- norm
+
+@pytest.mark.parametrize("rms", [False, True])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("cols", [3, 33, 100, 264])
+def test_norm_gradient_of_far_rows(cols, dtype, rms):
+    """A row of one value near the top of the range: n is 0 at every column, though -mean * rstd overflows; with the
+    root-mean-square form, whose mean is 0, a NaN mean is ignored."""
+    g = gen(cols)
+    far = 1.5 * 2.0 ** 120
+    x, dy, gamma = randn(g, 5, cols, dtype=dtype), randn(g, 5, cols, dtype=dtype), randn(g, cols, dtype=F32)
+    x[2] = 0.0 if rms else far
+    mean = torch.full((5,), float("nan"), device=DEV) if rms else x.float().mean(1)
+    if not rms:
+        mean[2] = far
+    rstd = torch.full((5,), 300.0, device=DEV)
+    dx, dgamma, dbeta = moe.moe_layer_norm_backward(dy, x, gamma, mean, rstd, rms=rms)
+    D, r = dy.double(), 300.0
+    n = (x.double() - (0 if rms else mean.double()[:, None])) * r
+    gg = D * gamma.double()
+    ref = r * (gg - (0 if rms else gg.mean(1, keepdim=True)) - n * (gg * n).mean(1, keepdim=True))
+    mag = r * (gg.abs() + gg.abs().mean(1, keepdim=True) + n.abs() * (gg * n).abs().mean(1, keepdim=True))
+    # sums of up to 264 terms and six roundings a term, each of n's own size (|x - mean| is exact to 2^-23 of |x| + |mean|)
+    en = 4 * ACC * (x.double().abs() + (0 if rms else mean.double().abs()[:, None])) * r
+    en[2] = 0
+    far_n = r * en * (gg * n).abs().mean(1, keepdim=True) + r * n.abs() * (gg.abs() * en).mean(1, keepdim=True)
+    check(dx, ref, u(dtype) * ref.abs() + (cols + 8) * ACC * mag + 2 * far_n, "dx")
+    acc = (cols + 8) * ACC
+    check(dgamma, (D * n).sum(0), acc * (D * n).abs().sum(0) + (D.abs() * en).sum(0) + 1e-30, "dgamma")
+    check(dbeta, D.sum(0), acc * D.abs().sum(0) + 1e-30, "dbeta")
