@@ -434,9 +434,9 @@ __device__ __forceinline__ void mm_plain_tile(const MatmulArgs& p, int i, MmTile
 // XCD a run of them: an eighth of the whole list may hold only small groups,
 // which wait for their weights' bytes, or only large ones (4096 x 1536, 65536
 // rows over 128 experts whose loads fall as rank^-1.2: 859 -> 814 us; evenly
-// filled 803 -> 797).  Dense lists keep the eighths, whose cut
-// slices then meet their operands in L2 (both linear gradients of 4000 x 5120 x
-// 5120: 427 us against 444).
+// filled 803 -> 797; with a kernel of its own for plain products 779 and 688).
+// Dense lists keep the eighths, whose cut slices then meet their operands in L2
+// (both linear gradients of 4000 x 5120 x 5120: 427 us against 444).
 template <bool WG, int BM, int BN>
 __device__ __forceinline__ bool mm_find_tile(const MatmulArgs& p, int lane, int step, MmTile& t) {
   const int x = blockIdx.x & 7;
@@ -449,8 +449,8 @@ __device__ __forceinline__ bool mm_find_tile(const MatmulArgs& p, int lane, int 
     const int64_t w0 = whole * x >> 3, w1 = whole * (x + 1) >> 3;
     // Weight gradients of several groups: every XCD takes its eighth of each
     // group's tiles, since a tile's time goes with its group's rows (16 groups
-    // of 32768 rows, the largest with four times the smallest's, 1536 x 4096:
-    // 439 -> 374 us).
+    // of 32768 rows, 1536 x 4096, fp32: the largest with four times the
+    // smallest's 500 us by eighths of the list, 402 so; equal groups 373 and 384).
     const int per = ceil_div(p.m, BM) * ceil_div(p.n, BN);
     if (WG && p.E > 1 && p.tail == 0 && per >= 64) {
       const int lo = (int)((int64_t)per * x >> 3), n = (int)((int64_t)per * (x + 1) >> 3) - lo;
@@ -871,7 +871,7 @@ __global__ __launch_bounds__(64 * WM * WN, BM * BN > 128 * 128 ? 1 : 2) void mat
         if (t.split >= 0 || p.out_f32) {
           // fp32, nothing to apply: sixteen lanes to a row, so that each store
           // covers whole lines (16 weight gradients of 1536 x 4096, 2048 rows
-          // each: 430 -> 374 us)
+          // each: 401 us by eight columns a lane, 384 so)
           const int c4 = lane & 15, at = wn * 16 * FN + 64 * h + 4 * c4;
 #pragma unroll
           for (int s = 0; s < 4; ++s) {

@@ -186,7 +186,10 @@ hipError_t stream_rows(const MatmulArgs& a, hipStream_t st) {
 // 4096 x 4096 22.5 us against 21.9).  Groups: where few experts have a row at
 // all, up to half as many rows as experts (8 rows over 128 experts of 2048 ->
 // 768 10.0 us against 18.1 by tiles, 64 rows 24.2 against 24.0, 256 rows 52
-// against 50, 1024 rows 86 against 85, 4096 rows 143 against 100).
+// against 50, 1024 rows 86 against 85, 4096 rows 143 against 100).  The bound
+// is that shape's: 64 experts of it cross a little earlier (32 rows 21.3 us
+// against 19.3), wider ones later (rows over 8 experts of 4096 -> 1536: 4 rows
+// 13.5 against 30.2, 8 rows 18.3 against the tiles' 31.3 that they take).
 bool matmul_streams(const MatmulArgs& a) {
   if (!a.aligned) return false;
   return a.offsets != nullptr ? 2 * (long long)a.rows <= a.E : a.rows <= 64;

