@@ -28,6 +28,9 @@ EXPORTS = (
     "moe_linear_workspace_bytes", "moe_linear", "moe_linear_backward_workspace_bytes", "moe_linear_backward",
     "moe_grouped_matmul", "moe_grouped_matmul_dgrad", "moe_grouped_matmul_wgrad_workspace_bytes",
     "moe_grouped_matmul_wgrad",
+    "moe_gated_linear_workspace_bytes", "moe_gated_linear", "moe_grouped_gated",
+    "moe_gated_linear_backward_workspace_bytes", "moe_gated_linear_backward",
+    "moe_grouped_gated_backward_workspace_bytes", "moe_grouped_gated_backward",
 )
 # bytes of the library's own workspace array (moe_layer_noalloc)
 MOE_NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -68,6 +71,11 @@ class MoeGroupedDims(ctypes.Structure):
     _fields_ = ([(n, ctypes.c_int32) for n in ("rows", "n_experts", "in_features", "out_features", "dtype",
                                                "dw_dtype")]
                 + [(n, ctypes.c_int64) for n in ("ld_x", "ld_y")])
+
+
+class MoeGatedDims(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("rows", "n_experts", "in_features", "width", "dtype", "act", "dw_dtype")]
+                + [(n, ctypes.c_int64) for n in ("ld_x", "ld_dx", "ld_w", "ld_h", "ld_pre")])
 
 
 class MoeError(RuntimeError):
@@ -123,6 +131,14 @@ def load() -> ctypes.CDLL:
     lib.moe_grouped_matmul_dgrad.argtypes = [GRP] + [P] * 5
     lib.moe_grouped_matmul_wgrad_workspace_bytes.argtypes = [GRP, OUT]
     lib.moe_grouped_matmul_wgrad.argtypes = [GRP] + [P] * 5 + [SIZE, P]
+    GAT = ctypes.POINTER(MoeGatedDims)
+    lib.moe_gated_linear_workspace_bytes.argtypes = [GAT, OUT]
+    lib.moe_gated_linear.argtypes = [GAT] + [P] * 7 + [SIZE, P]
+    lib.moe_grouped_gated.argtypes = [GAT] + [P] * 8
+    lib.moe_gated_linear_backward_workspace_bytes.argtypes = [GAT, OUT]
+    lib.moe_gated_linear_backward.argtypes = [GAT] + [P] * 10 + [SIZE, P]
+    lib.moe_grouped_gated_backward_workspace_bytes.argtypes = [GAT, OUT]
+    lib.moe_grouped_gated_backward.argtypes = [GAT] + [P] * 11 + [SIZE, P]
     for name in EXPORTS[2:]:
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib

@@ -597,3 +597,133 @@ def moe_grouped_matmul_wgrad(dy, x, expert_offsets, dtype=None, dw=None, stream=
         ws, pws, nws = _ws_for(lib.moe_grouped_matmul_wgrad_workspace_bytes, d, dev)
         _lib.check(lib.moe_grouped_matmul_wgrad(ctypes.byref(d), pd, px, po, pw, pws, nws, st))
     return dw
+
+
+def _gated(x, w_gate, w_up, offsets, act, want_pre, h, gate, up, stream):
+    _is_matrix(x, "x")
+    dev, dt = x.device, x.dtype
+    rows, n_in = x.shape
+    px, ldx = _mat(x, "x", dev, _HALVES)
+    code = _act(act)
+    if offsets is None:
+        E, po = 1, None
+        pg, ldw = _mat(w_gate, "w_gate", dev, (dt,), None, n_in)
+        width = w_gate.shape[0]
+        pu, ldu = _mat(w_up, "w_up", dev, (dt,), width, n_in)
+        if ldu != ldw:
+            raise ValueError(f"w_gate and w_up: row strides {ldw} and {ldu} differ")
+    else:
+        pg, ldw = _experts(w_gate, "w_gate", dev, (dt,), None), 0
+        E, width = w_gate.shape[0], w_gate.shape[1]
+        if w_gate.shape[2] != n_in:
+            raise ValueError(f"w_gate: shape {tuple(w_gate.shape)} beside rows of {n_in}")
+        pu = _experts(w_up, "w_up", dev, (dt,), (E, width, n_in))
+        po = _vec(offsets, "expert_offsets", dev, (torch.int32,), E + 1)
+    if (gate is None) != (up is None):
+        raise ValueError("gate and up: both or neither")
+    lib = _lib.load()
+    with _On(dev, stream) as st:
+        if h is None:
+            h = torch.empty((rows, width), dtype=dt, device=dev)
+        ph, ldh = _mat(h, "h", dev, (dt,), rows, width)
+        if gate is None and want_pre:
+            gate, up = (torch.empty((rows, width), dtype=dt, device=dev) for _ in range(2))
+        pa, pb, ldp = _pair(gate, up, dev, dt, rows, width)
+        d = _lib.MoeGatedDims(rows, E, n_in, width, _DTYPES[dt], code, _DTYPES[dt], ldx, 0, ldw, ldh, ldp)
+        if offsets is None:
+            ws, pws, nws = _ws_for(lib.moe_gated_linear_workspace_bytes, d, dev)
+            _lib.check(lib.moe_gated_linear(ctypes.byref(d), px, pg, pu, ph, pa, pb, pws, nws, st))
+        else:
+            _lib.check(lib.moe_grouped_gated(ctypes.byref(d), px, po, pg, pu, ph, pa, pb, st))
+    return (h, gate, up) if gate is not None else h
+
+
+def _pair(gate, up, dev, dt, rows, width):
+    """Addresses and the one row stride of the saved products (None: absent)."""
+    if gate is None:
+        return None, None, 0
+    pa, lda = _mat(gate, "gate", dev, (dt,), rows, width)
+    pb, ldb = _mat(up, "up", dev, (dt,), rows, width)
+    if lda != ldb:
+        raise ValueError(f"gate and up: row strides {lda} and {ldb} differ")
+    return pa, pb, lda
+
+
+def moe_gated_linear(x, w_gate, w_up, act: str = "silu", want_pre: bool = False, h=None, gate=None, up=None,
+                     stream=None):
+    """act(x w_gate^T) * (x w_up^T) for x [rows][in] and w_gate, w_up
+    [width][in].  Returns h, or (h, gate, up) with want_pre (or given gate and
+    up): both products, for moe_gated_linear_backward."""
+    return _gated(x, w_gate, w_up, None, act, want_pre, h, gate, up, stream)
+
+
+def moe_grouped_gated(x, expert_offsets, w_gate, w_up, act: str = "silu", want_pre: bool = False, h=None, gate=None,
+                      up=None, stream=None):
+    """moe_gated_linear by expert (moe_permute's offsets): w_gate, w_up
+    [E][width][in].  Rows outside every group are left as they are."""
+    if expert_offsets is None:
+        raise ValueError("expert_offsets: expected [E+1]")
+    return _gated(x, w_gate, w_up, expert_offsets, act, want_pre, h, gate, up, stream)
+
+
+def _gated_backward(dh, x, w_gate, w_up, gate, up, offsets, act, want_dx, want_dw, dw_dtype, dx, stream):
+    _is_matrix(dh, "dh")
+    dev, dt = dh.device, dh.dtype
+    rows, width = dh.shape
+    pd, ldh = _mat(dh, "dh", dev, _HALVES)
+    px, ldx = _mat(x, "x", dev, (dt,), rows, None)
+    n_in = x.shape[1]
+    code = _act(act)
+    if gate is None or up is None:
+        raise ValueError("gate and up: required")
+    pa, pb, ldp = _pair(gate, up, dev, dt, rows, width)
+    if offsets is None:
+        E, po, lead = 1, None, ()
+        pg, ldw = _mat(w_gate, "w_gate", dev, (dt,), width, n_in)
+        pu, ldu = _mat(w_up, "w_up", dev, (dt,), width, n_in)
+        if ldu != ldw:
+            raise ValueError(f"w_gate and w_up: row strides {ldw} and {ldu} differ")
+    else:
+        pg, ldw = _experts(w_gate, "w_gate", dev, (dt,), None), 0
+        E = w_gate.shape[0]
+        if tuple(w_gate.shape[1:]) != (width, n_in):
+            raise ValueError(f"w_gate: shape {tuple(w_gate.shape)} beside gradients of {width} and rows of {n_in}")
+        pu = _experts(w_up, "w_up", dev, (dt,), (E, width, n_in))
+        po, lead = _vec(offsets, "expert_offsets", dev, (torch.int32,), E + 1), (E,)
+    wt = dw_dtype or dt
+    if wt not in (dt, torch.float32):
+        raise TypeError(f"gradients of {wt} beside {dt} data")
+    lib = _lib.load()
+    with _On(dev, stream) as st:
+        if dx is None and want_dx:
+            dx = torch.empty((rows, n_in), dtype=dt, device=dev)
+        pdx, lddx = _mat(dx, "dx", dev, (dt,), rows, n_in) if dx is not None else (None, 0)
+        dwg, dwu = ((torch.empty((*lead, width, n_in), dtype=wt, device=dev) for _ in range(2)) if want_dw
+                    else (None, None))
+        pwg, pwu = (dwg.data_ptr(), dwu.data_ptr()) if want_dw else (None, None)
+        d = _lib.MoeGatedDims(rows, E, n_in, width, _DTYPES[dt], code, _DTYPES[wt], ldx, lddx, ldw, ldh, ldp)
+        if offsets is None:
+            ws, pws, nws = _ws_for(lib.moe_gated_linear_backward_workspace_bytes, d, dev)
+            _lib.check(lib.moe_gated_linear_backward(ctypes.byref(d), pd, px, pg, pu, pa, pb, pdx, pwg, pwu, pws, nws, st))
+        else:
+            ws, pws, nws = _ws_for(lib.moe_grouped_gated_backward_workspace_bytes, d, dev)
+            _lib.check(lib.moe_grouped_gated_backward(ctypes.byref(d), pd, px, po, pg, pu, pa, pb, pdx, pwg, pwu, pws,
+                                                      nws, st))
+    return dx, dwg, dwu
+
+
+def moe_gated_linear_backward(dh, x, w_gate, w_up, gate, up, act: str = "silu", want_dx: bool = True,
+                              want_dw: bool = True, dw_dtype=None, dx=None, stream=None):
+    """Gradients of moe_gated_linear: (dx, dw_gate, dw_up), None where not
+    wanted.  gate and up are what the forward pass returned.  The weights'
+    gradients have dh's type unless dw_dtype is torch.float32."""
+    return _gated_backward(dh, x, w_gate, w_up, gate, up, None, act, want_dx, want_dw, dw_dtype, dx, stream)
+
+
+def moe_grouped_gated_backward(dh, x, expert_offsets, w_gate, w_up, gate, up, act: str = "silu",
+                               want_dx: bool = True, want_dw: bool = True, dw_dtype=None, dx=None, stream=None):
+    """Gradients of moe_grouped_gated: (dx, dw_gate, dw_up), zero for the
+    weights of an expert without rows."""
+    if expert_offsets is None:
+        raise ValueError("expert_offsets: expected [E+1]")
+    return _gated_backward(dh, x, w_gate, w_up, gate, up, expert_offsets, act, want_dx, want_dw, dw_dtype, dx, stream)

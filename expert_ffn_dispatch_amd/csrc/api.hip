@@ -841,6 +841,200 @@ size_t grouped_wgrad_ws_bytes(const moe_grouped_dims& d) {
                                            d.in_features, d.out_features, d.dtype)));
 }
 
+int check_gated(const char* fn, moe_gated_dims& d, bool grouped) {
+  if (int r = check_rows(fn, d.rows)) return r;
+  if (d.width < 1 || d.width > kMaxWidth)
+    return fail(MOE_ERR_INVALID, "%s: width=%d outside [1, %d]", fn, d.width, kMaxWidth);
+  if (int r = check_product(fn, d.rows, d.in_features, d.width, d.dtype)) return r;
+  if (d.n_experts < 1) return fail(MOE_ERR_INVALID, "%s: n_experts=%d must be >= 1", fn, d.n_experts);
+  if (!grouped && d.n_experts != 1)
+    return fail(MOE_ERR_INVALID, "%s: n_experts=%d must be 1 without groups", fn, d.n_experts);
+  if (d.n_experts > kMaxE)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: n_experts=%d above the supported %d", fn, d.n_experts, kMaxE);
+  if (d.act < MOE_ACT_NONE || d.act > MOE_ACT_SILU) return fail(MOE_ERR_INVALID, "%s: unknown act %d", fn, d.act);
+  if (d.dw_dtype != d.dtype && d.dw_dtype != MOE_DTYPE_F32)
+    return fail(MOE_ERR_INVALID, "%s: dw_dtype=%d must be dtype or MOE_DTYPE_F32", fn, d.dw_dtype);
+  REQ_LD(d.ld_x, d.in_features);
+  REQ_LD(d.ld_dx, d.in_features);
+  REQ_LD(d.ld_w, d.in_features);
+  REQ_LD(d.ld_h, d.width);
+  REQ_LD(d.ld_pre, d.width);
+  if (grouped && d.ld_w != d.in_features) return fail(MOE_ERR_INVALID, "%s: grouped weights are packed, ld_w=%lld", fn, (long long)d.ld_w);
+  // a group's last row tile may be short: one more tile per group
+  const int64_t rows = grouped ? d.rows + 128LL * d.n_experts : d.rows;
+  if (int r = check_tiles(fn, 1, rows, 2LL * d.width)) return r;
+  if (int r = check_tiles(fn, 1, rows, d.in_features)) return r;
+  return check_tiles(fn, 2LL * d.n_experts, d.width, d.in_features);
+}
+
+// The two halves of the gradient's buffer, in whole stages of a contraction.
+int gated_half(const moe_gated_dims& d) { return (d.width + 63) / 64 * 64; }
+
+moe::MatmulArgs gated_args(const moe_gated_dims& d, bool grouped, const void* x, const void* w_gate, const void* w_up,
+                           void* h) {
+  moe::MatmulArgs a{};
+  a.gated = 1;
+  a.a = static_cast<const uint16_t*>(x);
+  a.lda = d.ld_x;
+  a.b = static_cast<const uint16_t*>(w_gate);
+  a.b2 = static_cast<const uint16_t*>(w_up);
+  a.ldb = d.ld_w;
+  a.b_group = (int64_t)d.width * d.in_features;
+  a.out = h;
+  a.ldo = d.ld_h;
+  a.E = d.n_experts;
+  a.rows = a.m = d.rows;
+  a.n = d.width;
+  a.k = d.in_features;
+  a.act = d.act;
+  a.f16 = d.dtype == MOE_DTYPE_F16;
+  a.whole = !grouped && d.rows <= 64 && d.in_features % 8 == 0 && d.ld_x % 8 == 0 && d.ld_w % 8 == 0;
+  return a;
+}
+moe::MatmulArgs gated_row_grad_args(const moe_gated_dims& d, const void* g, const void* w_gate, const void* w_up, void* dx) {
+  moe::MatmulArgs a = row_grad_args(g, 2LL * gated_half(d), w_gate, d.ld_w, dx, d.ld_dx, d.rows, d.in_features, d.width,
+                                    d.dtype, true);
+  a.gated = 1;
+  a.E = d.n_experts;
+  a.b2 = static_cast<const uint16_t*>(w_up);
+  a.b_group = (int64_t)d.width * d.in_features;
+  return a;
+}
+moe::MatmulArgs gated_weight_grad_args(const moe_gated_dims& d, const void* g, const void* x, void* dw_gate, void* dw_up) {
+  moe::MatmulArgs a = weight_grad_args(g, 2LL * gated_half(d), x, d.ld_x, dw_gate, d.dw_dtype, 2 * d.n_experts, d.rows,
+                                       d.in_features, d.width, d.dtype, true);
+  a.gated = a.b2_half = 1;
+  a.a_half = gated_half(d);
+  a.out2 = dw_up;
+  return a;
+}
+size_t gated_ws_bytes(const moe_gated_dims& d) {
+  return align_up(moe::matmul_workspace_bytes(moe::kMmForward, gated_args(d, false, nullptr, nullptr, nullptr, nullptr)));
+}
+struct GatedBackwardWs {
+  uint16_t* g;               // [rows][2 half]: dgate | dup
+  void* products;            // workspace of either product, one after the other
+};
+GatedBackwardWs carve_gated_backward(Carver& c, const moe_gated_dims& d, const int32_t* offsets) {
+  GatedBackwardWs w;
+  w.g = c.take<uint16_t>((size_t)d.rows * 2 * gated_half(d));
+  moe::MatmulArgs r = gated_row_grad_args(d, nullptr, nullptr, nullptr, nullptr);
+  moe::MatmulArgs g = gated_weight_grad_args(d, nullptr, nullptr, nullptr, nullptr);
+  r.offsets = g.offsets = offsets;
+  const size_t a = moe::matmul_workspace_bytes(moe::kMmRowGrad, r), b = moe::matmul_workspace_bytes(moe::kMmWeightGrad, g);
+  w.products = c.take<char>(a > b ? a : b);
+  return w;
+}
+
+int run_gated(const char* fn, const moe_gated_dims* dims, bool grouped, const void* x, const int32_t* expert_offsets,
+              const void* w_gate, const void* w_up, void* h, void* gate, void* up, void* ws, size_t ws_bytes,
+              moe_stream stream) {
+  if (dims == nullptr) return fail(MOE_ERR_INVALID, "%s: dims is NULL", fn);
+  moe_gated_dims d = *dims;
+  if (int r = check_gated(fn, d, grouped)) return r;
+  if ((gate == nullptr) != (up == nullptr)) return fail(MOE_ERR_INVALID, "%s: gate and up are saved both or not at all", fn);
+  if (d.rows == 0) return ok();
+  REQ_ELEM(x, d.dtype);
+  if (grouped) REQ_ELEM(expert_offsets, MOE_DTYPE_F32);
+  REQ_ELEM(w_gate, d.dtype);
+  REQ_ELEM(w_up, d.dtype);
+  REQ_ELEM(h, d.dtype);
+  OPT_ELEM(gate, d.dtype);
+  OPT_ELEM(up, d.dtype);
+  for (const void* o : {(const void*)h, (const void*)gate, (const void*)up})
+    if (o != nullptr && (o == x || o == w_gate || o == w_up)) return fail(MOE_ERR_INVALID, "%s: an output is an input", fn);
+  if (h == gate || h == up || (gate != nullptr && gate == up))
+    return fail(MOE_ERR_INVALID, "%s: two outputs are one", fn);
+  if (!grouped)
+    if (int r = check_ws(fn, ws, ws_bytes, gated_ws_bytes(d))) return r;
+  moe::MatmulArgs a = gated_args(d, grouped, x, w_gate, w_up, h);
+  a.offsets = expert_offsets;
+  a.pre = static_cast<uint16_t*>(gate);
+  a.pre2 = static_cast<uint16_t*>(up);
+  a.ldp = a.ldp2 = d.ld_pre;
+  if (hipError_t e = moe::launch_matmul(moe::kMmForward, a, ws, static_cast<hipStream_t>(stream)))
+    return device_error(fn, e);
+  return ok();
+}
+
+// Sizes of a backward call's workspace; the grouped form's products are not
+// cut, whatever the offsets say: any address stands for them here.
+int gated_backward_ws(const char* fn, const moe_gated_dims* dims, bool grouped, size_t* bytes) {
+  static const int32_t some = 0;
+  if (dims == nullptr) return fail(MOE_ERR_INVALID, "%s: dims is NULL", fn);
+  moe_gated_dims d = *dims;
+  if (int r = check_gated(fn, d, grouped)) return r;
+  if (bytes == nullptr) return fail(MOE_ERR_INVALID, "%s: bytes is NULL", fn);
+  Carver c(nullptr);
+  carve_gated_backward(c, d, grouped ? &some : nullptr);
+  *bytes = c.off;
+  return ok();
+}
+
+int run_gated_backward(const char* fn, const moe_gated_dims* dims, bool grouped, const void* dh, const void* x,
+                       const int32_t* expert_offsets, const void* w_gate, const void* w_up, const void* gate,
+                       const void* up, void* dx, void* dw_gate, void* dw_up, void* ws, size_t ws_bytes,
+                       moe_stream stream) {
+  size_t need = 0;
+  if (int r = gated_backward_ws(fn, dims, grouped, &need)) return r;
+  moe_gated_dims d = *dims;
+  if (int r = check_gated(fn, d, grouped)) return r;
+  if ((dw_gate == nullptr) != (dw_up == nullptr))
+    return fail(MOE_ERR_INVALID, "%s: dw_gate and dw_up are wanted both or not at all", fn);
+  if (dx == nullptr && dw_gate == nullptr) return ok();
+  if (d.rows > 0) {
+    REQ_ELEM(dh, d.dtype);
+    REQ_ELEM(gate, d.dtype);
+    REQ_ELEM(up, d.dtype);
+    if (dw_gate != nullptr) REQ_ELEM(x, d.dtype);
+    if (dx != nullptr) {
+      REQ_ELEM(w_gate, d.dtype);
+      REQ_ELEM(w_up, d.dtype);
+    }
+  }
+  if (grouped) REQ_ELEM(expert_offsets, MOE_DTYPE_F32);
+  OPT_ELEM(dx, d.dtype);
+  OPT_ELEM(dw_gate, d.dw_dtype);
+  OPT_ELEM(dw_up, d.dw_dtype);
+  for (const void* o : {(const void*)dx, (const void*)dw_gate, (const void*)dw_up})
+    if (o != nullptr && (o == dh || o == x || o == w_gate || o == w_up || o == gate || o == up))
+      return fail(MOE_ERR_INVALID, "%s: an output is an input", fn);
+  if ((dw_gate != nullptr && dw_gate == dw_up) || (dx != nullptr && (dx == dw_gate || dx == dw_up)))
+    return fail(MOE_ERR_INVALID, "%s: two outputs are one", fn);
+  if (int r = check_ws(fn, ws, ws_bytes, need)) return r;
+  Carver c(ws);
+  const GatedBackwardWs b = carve_gated_backward(c, d, expert_offsets);
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  if (d.rows > 0) {
+    moe::GatedGradArgs g{};
+    g.dh = static_cast<const uint16_t*>(dh);
+    g.gate = static_cast<const uint16_t*>(gate);
+    g.up = static_cast<const uint16_t*>(up);
+    g.g = b.g;
+    g.ldd = d.ld_h;
+    g.ldg = g.ldu = d.ld_pre;
+    g.offsets = expert_offsets;
+    g.E = d.n_experts;
+    g.rows = d.rows;
+    g.n = d.width;
+    g.half = gated_half(d);
+    g.act = d.act;
+    g.f16 = d.dtype == MOE_DTYPE_F16;
+    if (hipError_t e = moe::launch_gated_grad(g, st)) return device_error(fn, e);
+  }
+  if (dx != nullptr) {
+    moe::MatmulArgs a = gated_row_grad_args(d, b.g, w_gate, w_up, dx);
+    a.offsets = expert_offsets;
+    if (hipError_t e = moe::launch_matmul(moe::kMmRowGrad, a, b.products, st)) return device_error(fn, e);
+  }
+  if (dw_gate != nullptr) {
+    moe::MatmulArgs a = gated_weight_grad_args(d, b.g, x, dw_gate, dw_up);
+    a.offsets = expert_offsets;
+    if (hipError_t e = moe::launch_matmul(moe::kMmWeightGrad, a, b.products, st)) return device_error(fn, e);
+  }
+  return ok();
+}
+
 // A copy of the caller's dims to resolve strides in.
 #define COPY_DIMS(type, d)                                                                \
   if (dims == nullptr) return fail(MOE_ERR_INVALID, "%s: dims is NULL", fn);             \
@@ -1398,6 +1592,48 @@ int moe_grouped_matmul_wgrad(const moe_grouped_dims* dims, const void* dy, const
   if (hipError_t e = moe::launch_matmul(moe::kMmWeightGrad, a, ws, static_cast<hipStream_t>(stream)))
     return device_error(fn, e);
   return ok();
+}
+
+int moe_gated_linear_workspace_bytes(const moe_gated_dims* dims, size_t* bytes) {
+  const char* fn = "moe_gated_linear_workspace_bytes";
+  COPY_DIMS(moe_gated_dims, d);
+  if (int r = check_gated(fn, d, false)) return r;
+  if (bytes == nullptr) return fail(MOE_ERR_INVALID, "%s: bytes is NULL", fn);
+  *bytes = gated_ws_bytes(d);
+  return ok();
+}
+
+int moe_gated_linear(const moe_gated_dims* dims, const void* x, const void* w_gate, const void* w_up, void* h,
+                     void* gate, void* up, void* ws, size_t ws_bytes, moe_stream stream) {
+  return run_gated("moe_gated_linear", dims, false, x, nullptr, w_gate, w_up, h, gate, up, ws, ws_bytes, stream);
+}
+
+int moe_grouped_gated(const moe_gated_dims* dims, const void* x, const int32_t* expert_offsets, const void* w_gate,
+                      const void* w_up, void* h, void* gate, void* up, moe_stream stream) {
+  return run_gated("moe_grouped_gated", dims, true, x, expert_offsets, w_gate, w_up, h, gate, up, nullptr, 0, stream);
+}
+
+int moe_gated_linear_backward_workspace_bytes(const moe_gated_dims* dims, size_t* bytes) {
+  return gated_backward_ws("moe_gated_linear_backward_workspace_bytes", dims, false, bytes);
+}
+
+int moe_gated_linear_backward(const moe_gated_dims* dims, const void* dh, const void* x, const void* w_gate,
+                              const void* w_up, const void* gate, const void* up, void* dx, void* dw_gate, void* dw_up,
+                              void* ws, size_t ws_bytes, moe_stream stream) {
+  return run_gated_backward("moe_gated_linear_backward", dims, false, dh, x, nullptr, w_gate, w_up, gate, up, dx,
+                            dw_gate, dw_up, ws, ws_bytes, stream);
+}
+
+int moe_grouped_gated_backward_workspace_bytes(const moe_gated_dims* dims, size_t* bytes) {
+  return gated_backward_ws("moe_grouped_gated_backward_workspace_bytes", dims, true, bytes);
+}
+
+int moe_grouped_gated_backward(const moe_gated_dims* dims, const void* dh, const void* x,
+                               const int32_t* expert_offsets, const void* w_gate, const void* w_up, const void* gate,
+                               const void* up, void* dx, void* dw_gate, void* dw_up, void* ws, size_t ws_bytes,
+                               moe_stream stream) {
+  return run_gated_backward("moe_grouped_gated_backward", dims, true, dh, x, expert_offsets, w_gate, w_up, gate, up, dx,
+                            dw_gate, dw_up, ws, ws_bytes, stream);
 }
 
 }  // extern "C"

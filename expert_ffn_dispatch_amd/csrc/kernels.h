@@ -175,6 +175,14 @@ struct MatmulArgs {
   int64_t ldr;
   uint16_t* pre;
   int64_t ldp;
+  // the gated projections (GATED in matmul.h)
+  int gated;
+  const uint16_t* b2;        // forward, row grad: W_up beside W_gate (b), of the same shape
+  uint16_t* pre2;            // forward: the up products beside the gates (pre)
+  int64_t ldp2;
+  void* out2;                // weight grad: W_up's gradient beside W_gate's (out)
+  int64_t a_half;            // weight grad: elements from dgate's columns to dup's
+  int b2_half;               // weight grad: E counts both gradients of every group of rows
   int a_padded;              // a's last piece of a row may be read whole and is zero past the width
   int f16;                   // operands are fp16 (else bf16)
   int whole;                 // no contraction slices (no workspace for them)
@@ -198,6 +206,9 @@ hipError_t launch_matmul_stream(const MatmulArgs& a, hipStream_t st);
 hipError_t launch_matmul_forward(const MatmulArgs& a, hipStream_t st);
 hipError_t launch_matmul_row_grad(const MatmulArgs& a, hipStream_t st);
 hipError_t launch_matmul_weight_grad(const MatmulArgs& a, hipStream_t st);
+hipError_t launch_matmul_gated_forward(const MatmulArgs& a, hipStream_t st);
+hipError_t launch_matmul_gated_row_grad(const MatmulArgs& a, hipStream_t st);
+hipError_t launch_matmul_gated_weight_grad(const MatmulArgs& a, hipStream_t st);
 
 // g = dy * act'(pre) in the operands' type and, if dbias is set, its column
 // sums from the unrounded fp32 values.  g null: sums only.
@@ -213,6 +224,20 @@ struct ActGradArgs {
 };
 size_t act_grad_workspace_bytes(int64_t rows, int64_t n);
 hipError_t launch_act_grad(const ActGradArgs& a, void* ws, hipStream_t st);
+
+// g = [dgate | dup] of the gated projections, from dh and the saved products.
+struct GatedGradArgs {
+  const uint16_t* dh;
+  const uint16_t* gate;
+  const uint16_t* up;
+  uint16_t* g;               // [rows][2 half], 16-byte aligned
+  int64_t ldd, ldg, ldu;
+  const int32_t* offsets;    // rows outside the groups are left alone; null: all rows
+  int E, rows, n;
+  int half;                  // dup's first column: n to the next multiple of 64
+  int act, f16;
+};
+hipError_t launch_gated_grad(const GatedGradArgs& a, hipStream_t st);
 
 // ---- layer norm ----
 enum : int { kTypeBf16 = 0, kTypeF16 = 1, kTypeF32 = 2 };

@@ -189,11 +189,19 @@ __device__ __forceinline__ int mm_kswz(int krow) { return ((krow & 3) << 2) | ((
 // stage and written to LDS at its end.
 // Rows, columns and k past the ends become zeros (ALIGNED: by an offset past
 // the buffer, which reads no memory).
-template <bool KC, int R, int NW, bool ALIGNED>
+// TWO: the operand is two matrices of one shape, W_gate and W_up.  KC: of
+// every 32 rows of the stage the first sixteen are the first matrix's and the
+// others the second's, so that a wave ends with both products of a column in
+// one lane (8 rows to a load: a load is of one matrix).  KS: the second follows
+// the first along k, each in whole stages.
+template <bool KC, int R, int NW, bool ALIGNED, bool TWO = false>
 struct MmOperand {
   static constexpr int NI = R / (8 * NW);
   static constexpr int C = KC ? 8 : R / 8;        // chunks per LDS row
+  static_assert(!(TWO && KC) || NI % 4 == 0, "which matrix a load is of is known at compile time");
   uint64_t base;                                  // byte address of the tile's first element
+  uint64_t base2;                                 // TWO: in the second matrix
+  int first, half, len;                           // TWO, KS: stage of kt = 0; stages and k of one matrix
   uint32_t pitch;                                 // row pitch in bytes
   uint32_t off[NI];                               // per lane: byte offset within a stage
   int kk[NI];                                     // per lane: first k of the piece within a stage
@@ -216,7 +224,8 @@ struct MmOperand {
       if constexpr (KC) {
         const int r = 8 * piece + (lane >> 3);
         const int ch = (lane & 7) ^ mm_swz(r);
-        off[i] = r < ext ? (uint32_t)r * pitch + (uint32_t)(ch * 16) : kMmOut;
+        const int wr = TWO ? ((r >> 5) << 4) + (r & 15) : r;      // the matrix's row
+        off[i] = wr < ext ? (uint32_t)wr * pitch + (uint32_t)(ch * 16) : kMmOut;
         kk[i] = ch * 8;
       } else {
         const int kr = piece * (64 / C) + lane / C;
@@ -228,14 +237,28 @@ struct MmOperand {
   }
   // k is contiguous (KC) or steps by the pitch (KS).  The advance to stage kt
   // goes into the 64-bit scalar base, so lane offsets stay within one stage.
-  __device__ __forceinline__ uint64_t at(int kt) const {
+  // (TWO: for piece i)
+  __device__ __forceinline__ uint64_t at(int kt, int i) const {
+    if constexpr (TWO && KC) return ((i & 2) ? base2 : base) + (uint64_t)kt * (2 * kMmK);
+    if constexpr (TWO) {
+      const int s = first + kt;
+      return s < half ? base + (uint64_t)s * kMmK * (uint64_t)pitch : base2 + (uint64_t)(s - half) * kMmK * (uint64_t)pitch;
+    }
     return base + (KC ? (uint64_t)kt * (2 * kMmK) : (uint64_t)kt * kMmK * (uint64_t)pitch);
+  }
+  // k left in the matrix at stage kt
+  __device__ __forceinline__ int left(int kt, int kend) const {
+    if constexpr (TWO && !KC) {
+      const int s = first + kt;
+      return min(kend - kt * kMmK, len - (s < half ? s : s - half) * kMmK);
+    }
+    return kend - kt * kMmK;
   }
   // ALIGNED: pieces I0..I1-1 of stage kt into `buf`; kend: the contraction's length
   template <int I0, int I1>
   __device__ __forceinline__ void loads(uint16_t* buf, int kt, int kend) const {
     if constexpr (ALIGNED && I0 < I1) {
-      mm_dma16(mm_rsrc(reinterpret_cast<const void*>(at(kt))), kk[I0] < kend - kt * kMmK ? off[I0] : kMmOut, 0,
+      mm_dma16(mm_rsrc(reinterpret_cast<const void*>(at(kt, I0))), kk[I0] < left(kt, kend) ? off[I0] : kMmOut, 0,
                buf + (wave * NI + I0) * 512);
       loads<I0 + 1, I1>(buf, kt, kend);
     }
@@ -244,12 +267,14 @@ struct MmOperand {
   // none, at least 8: all)
   __device__ __forceinline__ int inside(int i, int kt, int kend, int lane) const {
     if (off[i] == kMmOut) return 0;
-    const int left = kend - kt * kMmK;
-    if constexpr (KC) return left - kk[i];
-    else return kk[i] < left ? lim - chunk(i, lane) * 8 : 0;
+    const int n = left(kt, kend);
+    if constexpr (KC) return n - kk[i];
+    else return kk[i] < n ? lim - chunk(i, lane) * 8 : 0;
   }
   // every piece of the stage is whole (the same for the whole block)
-  __device__ __forceinline__ bool interior(int kt, int kend) const { return lim >= R && kend - kt * kMmK >= kMmK; }
+  __device__ __forceinline__ bool interior(int kt, int kend) const {
+    return lim >= (TWO && KC ? R / 2 : R) && left(kt, kend) >= kMmK;
+  }
   __device__ __forceinline__ int chunk(int i, int lane) const {
     return (lane % C) ^ mm_kswz((wave * NI + i) * (64 / C) + lane / C);
   }
@@ -264,17 +289,16 @@ struct MmOperand {
   // 320 over 20110 rows of 4 groups 53 us.)
   __device__ __forceinline__ void fetch(u32x4_t (&v)[NI], int kt, int kend, int lane) const {
     if constexpr (!ALIGNED) {
-      const uint64_t b = at(kt);
       if (interior(kt, kend)) {
 #pragma unroll
-        for (int i = 0; i < NI; ++i) v[i] = mm_global16(b + off[i]);
+        for (int i = 0; i < NI; ++i) v[i] = mm_global16(at(kt, i) + off[i]);
         return;
       }
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         const int n = inside(i, kt, kend, lane);
         v[i] = u32x4_t{0, 0, 0, 0};
-        if (n >= 8 || (n > 0 && back(i, kt, n, lane))) v[i] = mm_global16(b + off[i] - (n < 8 ? 2 * (8 - n) : 0));
+        if (n >= 8 || (n > 0 && back(i, kt, n, lane))) v[i] = mm_global16(at(kt, i) + off[i] - (n < 8 ? 2 * (8 - n) : 0));
       }
     }
   }
@@ -290,7 +314,7 @@ struct MmOperand {
             lo = sh < 64 ? (lo >> sh) | (hi << (64 - sh)) : hi >> (sh - 64);
             hi = sh < 64 ? hi >> sh : 0;
           } else {                                // a row of fewer than eight elements
-            const uint64_t src = at(kt) + off[i];
+            const uint64_t src = at(kt, i) + off[i];
 #pragma nounroll
             for (int j = 0; j < n; ++j) {
               const uint64_t e = (uint64_t)mm_global2(src + 2 * j) << (16 * (j & 3));
@@ -415,7 +439,7 @@ __device__ __forceinline__ void mm_plain_tile(const MatmulArgs& p, int i, MmTile
   if constexpr (WG) {
     t.e = i / per;
     i -= t.e * per;
-    mm_bounds(p, t.e, t.g0, t.gn);
+    mm_bounds(p, p.b2_half ? t.e >> 1 : t.e, t.g0, t.gn);
     t.gn -= t.g0;
   }
   int rt, ct;
@@ -608,6 +632,33 @@ __device__ __forceinline__ void mm_bias8(const MatmulArgs& p, int col, float (&b
   }
 }
 
+// Eight consecutive columns of one row of the gated projections: h = act(gate)
+// up, with both saved for the backward pass if wanted.  All from the fp32 sums,
+// each rounded once.
+template <bool F16>
+__device__ __forceinline__ void mm_put8(uint16_t* o, const float (&v)[8], int n) {
+  if (n >= 8) {
+    mm_store16(o, u32x4_t{mm_pack2<F16>(v[0], v[1]), mm_pack2<F16>(v[2], v[3]), mm_pack2<F16>(v[4], v[5]),
+                          mm_pack2<F16>(v[6], v[7])});
+  } else {
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (q < n) o[q] = mm_store1<F16>(v[q]);
+  }
+}
+template <bool F16>
+__device__ __forceinline__ void mm_gate8(const MatmulArgs& p, float (&g)[8], float (&u)[8], int64_t row, int col) {
+  const int n = p.n - col;                        // columns left
+  if (p.pre != nullptr) {
+    mm_put8<F16>(p.pre + row * p.ldp + col, g, n);
+    mm_put8<F16>(p.pre2 + row * p.ldp2 + col, u, n);
+  }
+  mm_act(g, p.act);
+#pragma unroll
+  for (int q = 0; q < 8; ++q) u[q] *= g[q];
+  mm_put8<F16>(static_cast<uint16_t*>(p.out) + row * p.ldo + col, u, n);
+}
+
 // -------------------------------------------------------------- the kernel
 
 // The kernel's arguments, read again from the kernarg segment at each use of
@@ -652,13 +703,21 @@ __device__ __forceinline__ void mm_order() {
 // the saved pre-activation; without any of them a kernel of its own, as the
 // epilogue's instructions cost a plain product their fetches (16384 x 1536 ->
 // 4096: 195 us with one kernel for both, 170 so).
-template <bool F16, bool AKC, bool BKC, int BM, int BN, int WM, int WN, bool ALIGNED, bool EPI>
+// GATED: the gated projections.  Forward: the columns' operand is W_gate and
+// W_up side by side (MmOperand's TWO), and the epilogue is their activation and
+// product.  Row grad: dgate W_gate + dup W_up is one contraction over both, the
+// rows' operand holding dgate and dup side by side.  Weight grad: two groups,
+// the gate's and the up's, for every group of rows.
+template <bool F16, bool AKC, bool BKC, int BM, int BN, int WM, int WN, bool ALIGNED, bool EPI, bool GATED = false>
 __global__ __launch_bounds__(64 * WM * WN, BM * BN > 128 * 128 ? 1 : 2) void matmul_tile_kernel(MatmulArgs) {
   constexpr int NW = WM * WN;
   constexpr int FM = BM / (32 * WM);              // a wave's 32-row blocks
   constexpr int FN = BN / (16 * WN);              // and 16-column blocks
   static_assert(FM <= 4 && FN % 4 == 0, "a wave covers whole runs of 64 columns");
   constexpr bool WG = !AKC;                       // weight grad: the contraction runs over rows
+  constexpr bool TWO = GATED && !WG;              // the columns' operand is two matrices
+  constexpr bool PAIR = GATED && AKC && BKC;      // a tile's columns are pairs, gate and up
+  constexpr int BO = PAIR ? BN / 2 : BN;          // output columns of a tile
   constexpr int STA = BM * kMmK, STB = BN * kMmK;
   // Every buffer an array of its own, so that the compiler knows that loads
   // into one leave reads of another alone.
@@ -671,12 +730,12 @@ __global__ __launch_bounds__(64 * WM * WN, BM * BN > 128 * 128 ? 1 : 2) void mat
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
   MmTile t;
-  if (!mm_find_tile<WG, BM, BN>(mm_args(), lane, 0, t)) return;
+  if (!mm_find_tile<WG, BM, BO>(mm_args(), lane, 0, t)) return;
   mm_scalar(t);
 
   MmOperand<AKC, BM, NW, ALIGNED> la;
-  MmOperand<BKC, BN, NW, ALIGNED> lb;
-  constexpr int AI = MmOperand<AKC, BM, NW, ALIGNED>::NI, BI = MmOperand<BKC, BN, NW, ALIGNED>::NI;
+  MmOperand<BKC, BN, NW, ALIGNED, TWO> lb;
+  constexpr int AI = MmOperand<AKC, BM, NW, ALIGNED>::NI, BI = MmOperand<BKC, BN, NW, ALIGNED, TWO>::NI;
   constexpr int B2 = (BI + 2) / 3, B3 = (2 * BI + 2) / 3;
   int kend, KT;                                   // the tile's contraction, and its stages
   // a tile's operands, and its first loads: columns of stages 0 and 1, rows of
@@ -686,6 +745,7 @@ __global__ __launch_bounds__(64 * WM * WN, BM * BN > 128 * 128 ? 1 : 2) void mat
     const int lane = mm_lane(tid & 63);
     int kbeg = 0;
     kend = WG ? q.gn : p.k;
+    if constexpr (TWO && !BKC) kend = 2 * ceil_div(p.k, kMmK) * kMmK;
     if (q.split >= 0) {                           // whole stages to a slice
       const int per = ceil_div(ceil_div(kend, kMmK), p.splits) * kMmK;
       kbeg = min(q.split * per, kend);
@@ -695,10 +755,18 @@ __global__ __launch_bounds__(64 * WM * WN, BM * BN > 128 * 128 ? 1 : 2) void mat
     if constexpr (AKC)
       la.init(p.a + (int64_t)(q.g0 + q.row0) * p.lda + kbeg, p.lda, q.nrows, kbeg, wave, lane);
     else
-      la.init(p.a + (int64_t)(q.g0 + kbeg) * p.lda + q.row0, p.lda, p.m - q.row0, q.row0, wave, lane);
+      la.init(p.a + (GATED && (q.e & 1) ? p.a_half : 0) + (int64_t)(q.g0 + kbeg) * p.lda + q.row0, p.lda,
+              p.m - q.row0, q.row0, wave, lane);
     const uint16_t* bp = WG ? p.b + (int64_t)q.g0 * p.ldb : p.b + (int64_t)q.e * p.b_group;
     if constexpr (BKC) lb.init(bp + (int64_t)q.col0 * p.ldb + kbeg, p.ldb, p.n - q.col0, kbeg, wave, lane);
-    else lb.init(bp + (int64_t)kbeg * p.ldb + q.col0, p.ldb, p.n - q.col0, q.col0, wave, lane);
+    else lb.init(bp + (int64_t)(TWO ? 0 : kbeg) * p.ldb + q.col0, p.ldb, p.n - q.col0, q.col0, wave, lane);
+    if constexpr (TWO) {
+      // the same place in the second matrix
+      lb.base2 = lb.base + (reinterpret_cast<uint64_t>(p.b2) - reinterpret_cast<uint64_t>(p.b));
+      lb.first = kbeg / kMmK;
+      lb.half = ceil_div(p.k, kMmK);
+      lb.len = p.k;
+    }
     lb.template loads<0, BI>(sb0, 0, kend);
     la.template loads<0, AI>(sa0, 0, kend);
     lb.template loads<0, BI>(sb1, 1, kend);
@@ -719,7 +787,7 @@ __global__ __launch_bounds__(64 * WM * WN, BM * BN > 128 * 128 ? 1 : 2) void mat
 
   for (int step = 1;; ++step) {
   MmTile tn;
-  const bool more = __builtin_amdgcn_readfirstlane(mm_find_tile<WG, BM, BN>(mm_args(), mm_lane(lane), step, tn));
+  const bool more = __builtin_amdgcn_readfirstlane(mm_find_tile<WG, BM, BO>(mm_args(), mm_lane(lane), step, tn));
   mm_scalar(tn);
 
   // NBLK: this wave's 32-row blocks with live rows; the others are neither
@@ -849,12 +917,15 @@ __global__ __launch_bounds__(64 * WM * WN, BM * BN > 128 * 128 ? 1 : 2) void mat
     // back as row segments of eight columns, so that loads and stores cover
     // whole 128-byte segments.  Chunk c (four columns) of row r sits at c ^ r:
     // no bank conflicts.
-    const MatmulArgs p = mm_args();
+    MatmulArgs p = mm_args();
+    if constexpr (GATED && WG) {
+      if (t.e & 1) p.out = p.out2;
+    }
     const int lane = mm_lane(tid & 63);
     static_assert(STB * 2 >= NW * 4096, "the waves' staging slots");
     float* blk = reinterpret_cast<float*>(sb2) + wave * 1024;
     const int fr = lane & 15, fg = lane >> 4, ch = lane & 7;
-    const int64_t out_off = WG ? (int64_t)t.e * p.out_group : 0;
+    const int64_t out_off = WG ? (int64_t)(GATED ? t.e >> 1 : t.e) * p.out_group : 0;
     const int64_t row_base = (int64_t)(WG ? 0 : t.g0) + t.row0;
 #pragma unroll
     for (int h = 0; h < FN / 4; ++h) {
@@ -868,7 +939,23 @@ __global__ __launch_bounds__(64 * WM * WN, BM * BN > 128 * 128 ? 1 : 2) void mat
         for (int j = 0; j < 4; ++j)
           *reinterpret_cast<f32x4_t*>(blk + fr * 64 + (((4 * j + fg) ^ fr) << 2)) = acc[i < NA ? i : 0][4 * h + j];
         __builtin_amdgcn_wave_barrier();          // a wave's LDS operations complete in order
-        if (t.split >= 0 || p.out_f32) {
+        if (PAIR && t.split < 0) {
+          // four lanes to a row: eight gates and their ups, 32 columns on
+          const int r = lane >> 2, c = lane & 3, cg = 8 * (c >> 1) + 2 * (c & 1);
+          const int row = wm * 32 * FM + 16 * i + r, col = t.col0 + wn * 8 * FN + 32 * h + 8 * c;
+          float g[8], v[8];
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const f32x4_t a = *reinterpret_cast<const f32x4_t*>(blk + r * 64 + (((cg + q) ^ r) << 2));
+            const f32x4_t b = *reinterpret_cast<const f32x4_t*>(blk + r * 64 + (((cg + 4 + q) ^ r) << 2));
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              g[4 * q + k] = a[k];
+              v[4 * q + k] = b[k];
+            }
+          }
+          if (row < t.nrows && col < p.n) mm_gate8<F16>(p, g, v, row_base + row, col);
+        } else if (t.split >= 0 || p.out_f32) {
           // fp32, nothing to apply: sixteen lanes to a row, so that each store
           // covers whole lines (16 weight gradients of 1536 x 4096, 2048 rows
           // each: 401 us by eight columns a lane, 384 so)
@@ -877,7 +964,8 @@ __global__ __launch_bounds__(64 * WM * WN, BM * BN > 128 * 128 ? 1 : 2) void mat
           for (int s = 0; s < 4; ++s) {
             const int r = 4 * s + fg, row = wm * 32 * FM + 16 * i + r;
             const f32x4_t v = *reinterpret_cast<const f32x4_t*>(blk + r * 64 + ((c4 ^ r) << 2));
-            if (row >= t.nrows || t.col0 + at >= p.n) continue;
+            const int oc = PAIR ? ((at >> 5) << 4) + (at & 15) : at;
+            if (row >= t.nrows || t.col0 + oc >= p.n) continue;
             if (t.split >= 0) {                   // partial tile [BM][BN], read again by the join
               *reinterpret_cast<f32x4_t*>(p.parts + ((int64_t)t.part * BM + row) * BN + at) = v;
             } else {

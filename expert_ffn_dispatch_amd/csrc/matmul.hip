@@ -1,5 +1,6 @@
 // What the three forms share: the choice of contraction slices, the sum of
-// their partial results, and the activation's gradient with the bias gradient.
+// their partial results, and the gradients of the activation (with the bias
+// gradient) and of the gated projections' activation and product.
 #include "matmul.h"
 
 namespace moe {
@@ -32,7 +33,50 @@ __global__ __launch_bounds__(256) void matmul_join_kernel(MatmulArgs p) {
   }
   float bias[8];
   mm_bias8<F16>(p, col, bias);
-  mm_finish8<F16, !WG>(p, v, bias, (int64_t)t.row0 + row, col, WG ? (int64_t)t.e * p.out_group : 0);
+  int e = t.e;
+  if (WG && p.b2_half) {
+    if (e & 1) p.out = p.out2;
+    e >>= 1;
+  }
+  mm_finish8<F16, !WG>(p, v, bias, (int64_t)t.row0 + row, col, WG ? (int64_t)e * p.out_group : 0);
+}
+
+// The same for the gated projections, forward: of every 32 columns of a part
+// the first sixteen are gates, the others their ups.  A thread takes eight
+// columns of a row, a block 1024 values of a tile's output.
+template <bool F16, int B>
+__global__ __launch_bounds__(128) void matmul_join_gated_kernel(MatmulArgs p) {
+  constexpr int kPer = B * B / 2048, kRow = B / 16;
+  const int j = blockIdx.x / kPer;
+  MmTile t;
+  const int64_t tiles = (int64_t)ceil_div(p.m, B) * ceil_div(p.n, B / 2);
+  mm_plain_tile<false, B, B / 2>(p, (int)(tiles - p.tail) + j, t);
+  const int i = (blockIdx.x - j * kPer) * 128 + threadIdx.x;
+  const int row = i / kRow, c = i % kRow, col = t.col0 + 8 * c;
+  if (row >= t.nrows || col >= p.n) return;
+  const float* src = p.parts + (int64_t)j * p.splits * (B * B) + row * B + 32 * (c >> 1) + 8 * (c & 1);
+  float g[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, u[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int s = 0; s < p.splits; ++s, src += B * B) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const f32x4_t a = *reinterpret_cast<const f32x4_t*>(src + 4 * h), b = *reinterpret_cast<const f32x4_t*>(src + 16 + 4 * h);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        g[4 * h + q] += a[q];
+        u[4 * h + q] += b[q];
+      }
+    }
+  }
+  mm_gate8<F16>(p, g, u, (int64_t)t.row0 + row, col);
+}
+
+template <int B>
+hipError_t launch_join_gated(const MatmulArgs& a, hipStream_t st) {
+  const dim3 grid((unsigned)(a.tail * (B * B / 2048)));
+  if (a.f16) hipLaunchKernelGGL((matmul_join_gated_kernel<true, B>), grid, dim3(128), 0, st, a);
+  else hipLaunchKernelGGL((matmul_join_gated_kernel<false, B>), grid, dim3(128), 0, st, a);
+  return hipGetLastError();
 }
 
 template <bool WG, int B>
@@ -75,6 +119,59 @@ __device__ __forceinline__ float act_grad(float z, int act) {
     }
     default: return 1.f;
   }
+}
+
+// act(z) and act'(z) together: one exponential and one reciprocal.
+__device__ __forceinline__ void act_both(float z, int act, float& value, float& slope) {
+  const float w = fabsf(z) > 128.f ? copysignf(128.f, z) : z;     // as above
+  switch (act) {
+    case kActRelu:
+      slope = z > 0.f ? 1.f : 0.f;
+      value = z > 0.f || z != z ? z : 0.f;
+      break;
+    case kActGelu: {
+      const float e = __expf(-0.5f * w * w), n = mm_normal(w, e);
+      value = z * n;
+      slope = n + w * 0.39894228040143268f * e;
+      break;
+    }
+    case kActGeluTanh: {
+      float s, c;
+      logistic(1.5957691216057307f * (w + 0.044715f * w * w * w), s, c);
+      value = z * s;
+      slope = s + w * s * c * 1.5957691216057307f * (1.f + 0.134145f * w * w);
+      break;
+    }
+    case kActSilu: {
+      float s, c;
+      logistic(w, s, c);
+      value = z * s;
+      slope = s + w * s * c;
+      break;
+    }
+    default:
+      value = z;
+      slope = 1.f;
+  }
+}
+
+// The rows of the groups (offsets as mm_bounds clamps them): where they
+// decrease they still lie between the least and the greatest.  Every wave looks
+// through the offsets itself (at most five a lane).
+__device__ __forceinline__ void group_rows(const int32_t* offsets, int E, int64_t rows, int64_t& first, int64_t& end) {
+  int lo = (int)rows, hi = 0;
+  for (int e = threadIdx.x & 63; e <= E; e += 64) {
+    const int o = min(max(offsets[e], 0), (int)rows);
+    if (e < E) lo = min(lo, o);
+    hi = max(hi, o);
+  }
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) {
+    lo = min(lo, __shfl_xor(lo, d));
+    hi = max(hi, __shfl_xor(hi, d));
+  }
+  first = lo;
+  end = hi;
 }
 
 // Eight 16-bit values from p on, zeros from the n-th on.
@@ -166,6 +263,39 @@ __global__ __launch_bounds__(1024) void dbias_join_kernel(ActGradArgs p, const f
   }
 }
 
+// dgate = dh up act'(gate) and dup = dh act(gate), rounded to the operands' 16
+// bits (as g above), side by side: g [rows][2 half], dup from column `half`
+// on (whole stages of the contraction), zeros past n.  A thread takes eight
+// columns of a row.  Bound by its five passes over rows x n.
+template <bool F16>
+__global__ __launch_bounds__(256) void gated_grad_kernel(GatedGradArgs p) {
+  const uint32_t chunks = (uint32_t)p.half / 8;
+  int64_t first = 0, end = p.rows;
+  if (p.offsets != nullptr) group_rows(p.offsets, p.E, p.rows, first, end);
+  const int64_t last = (end - first) * chunks;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < last; i += (int64_t)gridDim.x * 256) {
+    const int64_t k = last <= 0xffffffffLL ? (int64_t)((uint32_t)i / chunks) : i / chunks;
+    const int64_t r = first + k;
+    const int c = (int)(i - k * chunks) * 8, n = p.n - c;
+    float d[8], z[8], u[8];
+    mm_unpack8<F16>(load8(p.dh + r * p.ldd + c, n), d);
+    mm_unpack8<F16>(load8(p.gate + r * p.ldg + c, n), z);
+    mm_unpack8<F16>(load8(p.up + r * p.ldu + c, n), u);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      float value, slope;
+      act_both(z[q], p.act, value, slope);
+      u[q] *= d[q] * slope;
+      z[q] = d[q] * value;
+    }
+    uint16_t* o = p.g + r * 2 * p.half + c;
+    *reinterpret_cast<u32x4_t*>(o) = u32x4_t{mm_pack2<F16>(u[0], u[1]), mm_pack2<F16>(u[2], u[3]),
+                                             mm_pack2<F16>(u[4], u[5]), mm_pack2<F16>(u[6], u[7])};
+    *reinterpret_cast<u32x4_t*>(o + p.half) = u32x4_t{mm_pack2<F16>(z[0], z[1]), mm_pack2<F16>(z[2], z[3]),
+                                                      mm_pack2<F16>(z[4], z[5]), mm_pack2<F16>(z[6], z[7])};
+  }
+}
+
 // Rows per run: about 1024 blocks over the card, at least 16 rows each.
 int act_grad_run(int64_t rows, int64_t n) {
   const int64_t col_blocks = (n + 511) / 512;
@@ -198,6 +328,15 @@ hipError_t launch_act_grad(const ActGradArgs& a, void* ws, hipStream_t st) {
     return hipGetLastError();
   }
   return hipSuccess;
+}
+
+hipError_t launch_gated_grad(const GatedGradArgs& a, hipStream_t st) {
+  const int64_t blocks = ((int64_t)a.rows * (a.half / 8) + 255) / 256;
+  const dim3 grid((unsigned)(blocks < 16384 ? blocks : 16384));
+  if (a.rows <= 0) return hipSuccess;
+  if (a.f16) hipLaunchKernelGGL(gated_grad_kernel<true>, grid, dim3(256), 0, st, a);
+  else hipLaunchKernelGGL(gated_grad_kernel<false>, grid, dim3(256), 0, st, a);
+  return hipGetLastError();
 }
 
 namespace {
@@ -256,21 +395,7 @@ __global__ __launch_bounds__(256) void pack_kernel(const uint16_t* in, int64_t l
   const int chunks = pitch / 8;
   int64_t first = 0, end = rows;
   if (offsets != nullptr) {
-    // every wave looks through the offsets itself (at most five a lane); where
-    // they decrease the groups' rows still lie between the least and the greatest
-    int lo = (int)rows, hi = 0;
-    for (int e = threadIdx.x & 63; e <= E; e += 64) {
-      const int o = min(max(offsets[e], 0), (int)rows);
-      if (e < E) lo = min(lo, o);
-      hi = max(hi, o);
-    }
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) {
-      lo = min(lo, __shfl_xor(lo, d));
-      hi = max(hi, __shfl_xor(hi, d));
-    }
-    first = lo;
-    end = hi;
+    group_rows(offsets, E, rows, first, end);
   }
   for (int64_t i = first * chunks + (int64_t)blockIdx.x * 256 + threadIdx.x; i < end * chunks;
        i += (int64_t)gridDim.x * 256) {
@@ -289,7 +414,8 @@ struct Packing {
   bool a, b;
   int wa, wb, pa, pb;        // widths, pitches
   int64_t ra, rb;            // rows
-  size_t bytes_a, bytes_b;
+  size_t bytes_a, bytes_b;   // bytes_b: of each matrix
+  int mats;
 };
 size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
 Packing packing(MatmulForm f, const MatmulArgs& q) {
@@ -299,21 +425,24 @@ Packing packing(MatmulForm f, const MatmulArgs& q) {
   k.ra = q.rows;
   k.rb = f == kMmForward ? q.n : f == kMmRowGrad ? q.k : q.rows;
   if (q.whole || (f != kMmWeightGrad && q.offsets != nullptr)) return k;
+  const int mats = q.gated && f != kMmWeightGrad ? 2 : 1;   // of the columns' operand
+  const int groups = q.b2_half ? q.E / 2 : q.E;
   const bool a = !(q.lda % 8 == 0 && (q.a_padded || k.wa % 8 == 0)), b = !(q.ldb % 8 == 0 && k.wb % 8 == 0);
   if (!a && !b) return k;
   auto pitch = [](int w) { return w >= 512 ? (w + 63) / 64 * 64 : (w + 7) / 8 * 8; };
   k.pa = pitch(k.wa);
   k.pb = pitch(k.wb);
   const size_t na = (size_t)k.ra * k.pa * 2, nb = (size_t)k.rb * k.pb * 2;
-  const int64_t len = f == kMmWeightGrad ? q.rows / q.E : q.k, stages = len / kMmK;
-  const double flops = 2.0 * q.rows * (f == kMmForward ? (double)q.n * q.k : f == kMmRowGrad ? (double)q.k * q.n : (double)q.m * q.n);
+  const int64_t len = f == kMmWeightGrad ? q.rows / groups : q.k, stages = len / kMmK;
+  const double flops = (q.gated ? 4.0 : 2.0) * q.rows * (f == kMmForward ? (double)q.n * q.k : f == kMmRowGrad ? (double)q.k * q.n : (double)q.m * q.n);
   const double gain = flops * 1.2e-9 + (stages < 16 ? stages : 16);
-  const double cost = (a ? na * 2 / 4e6 + 4 : 0) + (b ? nb * 2 / 4e6 + 4 : 0);
+  const double cost = (a ? na * 2 / 4e6 + 4 : 0) + (b ? mats * (nb * 2 / 4e6 + 4) : 0);
   if (gain <= cost) return k;
   k.a = a;
   k.b = b;
   k.bytes_a = a ? up256(na) : 0;
   k.bytes_b = b ? up256(nb) : 0;
+  k.mats = mats;
   return k;
 }
 hipError_t launch_pack(const uint16_t* in, int64_t ld, int64_t rows, int width, void* out, int pitch,
@@ -325,56 +454,74 @@ hipError_t launch_pack(const uint16_t* in, int64_t ld, int64_t rows, int width, 
 }
 bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// The plan of a call.  Gated: a tile's columns are gates and ups, the rows'
+// gradient has both contractions one after the other, and every group of rows
+// two weight gradients.
+Plan plan_of(MatmulForm f, const MatmulArgs& a, bool aligned) {
+  const bool g = a.gated != 0;
+  return matmul_plan(f, a.E, (int64_t)a.rows * (a.b2_half ? 2 : 1), a.m, (int64_t)a.n * (g && f == kMmForward ? 2 : 1),
+                     g && f == kMmRowGrad ? 2 * (((int64_t)a.k + kMmK - 1) / kMmK * kMmK) : a.k, aligned, a.whole != 0);
+}
+
 }  // namespace
 
 size_t matmul_workspace_bytes(MatmulForm f, const MatmulArgs& a) {
   if (a.whole || (f != kMmWeightGrad && a.offsets != nullptr)) return 0;
   const Packing k = packing(f, a);
   // the pointers' alignment is not known here: either plan may run
-  const size_t x = matmul_plan(f, a.E, a.rows, a.m, a.n, a.k, true, false).bytes;
-  const size_t y = matmul_plan(f, a.E, a.rows, a.m, a.n, a.k, false, false).bytes;
-  return k.bytes_a + k.bytes_b + up256(x > y ? x : y);
+  const size_t x = plan_of(f, a, true).bytes, y = plan_of(f, a, false).bytes;
+  return k.bytes_a + k.mats * k.bytes_b + up256(x > y ? x : y);
 }
 
 hipError_t launch_matmul(MatmulForm f, MatmulArgs a, void* ws, hipStream_t st) {
   if (a.m == 0 || (f != kMmWeightGrad && a.rows == 0)) return hipSuccess;
   const Packing k = packing(f, a);
   const bool a16 = al16(a.a) && a.lda % 8 == 0 && (a.a_padded || k.wa % 8 == 0);
-  const bool b16 = al16(a.b) && a.ldb % 8 == 0 && k.wb % 8 == 0;
+  const bool b16 = al16(a.b) && (a.b2 == nullptr || al16(a.b2)) && a.ldb % 8 == 0 && k.wb % 8 == 0;
   a.aligned = (a16 || k.a) && (b16 || k.b);
   char* w = static_cast<char*>(ws);
+  const int groups = a.b2_half ? a.E / 2 : a.E;
   if (a.aligned && a.rows > 0) {
     if (k.a) {
-      if (hipError_t e = launch_pack(a.a, a.lda, k.ra, k.wa, w, k.pa, a.offsets, a.E, st)) return e;
+      if (hipError_t e = launch_pack(a.a, a.lda, k.ra, k.wa, w, k.pa, a.offsets, groups, st)) return e;
       a.a = reinterpret_cast<const uint16_t*>(w);
       a.lda = k.pa;
     }
     if (k.b) {
-      if (hipError_t e = launch_pack(a.b, a.ldb, k.rb, k.wb, w + k.bytes_a, k.pb, a.offsets, a.E, st)) return e;
+      if (hipError_t e = launch_pack(a.b, a.ldb, k.rb, k.wb, w + k.bytes_a, k.pb, a.offsets, groups, st)) return e;
       a.b = reinterpret_cast<const uint16_t*>(w + k.bytes_a);
+      if (k.mats == 2) {
+        char* w2 = w + k.bytes_a + k.bytes_b;
+        if (hipError_t e = launch_pack(a.b2, a.ldb, k.rb, k.wb, w2, k.pb, a.offsets, groups, st)) return e;
+        a.b2 = reinterpret_cast<const uint16_t*>(w2);
+      }
       a.ldb = k.pb;
     }
   }
-  a.parts = reinterpret_cast<float*>(w + k.bytes_a + k.bytes_b);
+  a.parts = reinterpret_cast<float*>(w + k.bytes_a + k.mats * k.bytes_b);
   if (f == kMmForward && matmul_streams(a)) return launch_matmul_stream(a, st);
   if (f != kMmWeightGrad && a.offsets != nullptr) {
     // ragged: 256 x 256 tiles where the mean group would fill the card with
     // them, else 128 x 128
-    const int64_t mean = (a.rows + a.E - 1) / a.E;
-    a.big = mean > 128 && a.n > 128 && a.E * ((mean + 255) / 256) * ((a.n + 255) / 256) >= 192;
+    const int64_t mean = (a.rows + a.E - 1) / a.E, n = (int64_t)a.n * (a.gated && f == kMmForward ? 2 : 1);
+    a.big = mean > 128 && n > 128 && a.E * ((mean + 255) / 256) * ((n + 255) / 256) >= 192;
     a.tail = 0;
     a.splits = 1;
   } else {
-    const Plan plan = matmul_plan(f, a.E, a.rows, a.m, a.n, a.k, a.aligned != 0, a.whole != 0);
+    const Plan plan = plan_of(f, a, a.aligned != 0);
     a.big = plan.big;
     a.tail = plan.tail;
     a.splits = plan.splits;
   }
-  if (hipError_t e = f == kMmForward ? launch_matmul_forward(a, st)
+  if (hipError_t e = a.gated ? (f == kMmForward   ? launch_matmul_gated_forward(a, st)
+                                : f == kMmRowGrad ? launch_matmul_gated_row_grad(a, st)
+                                                  : launch_matmul_gated_weight_grad(a, st))
+                     : f == kMmForward ? launch_matmul_forward(a, st)
                      : f == kMmRowGrad ? launch_matmul_row_grad(a, st)
                                        : launch_matmul_weight_grad(a, st))
     return e;
   if (a.tail == 0) return hipSuccess;
+  if (a.gated && f == kMmForward) return a.big ? launch_join_gated<256>(a, st) : launch_join_gated<128>(a, st);
   if (f == kMmWeightGrad) return a.big ? launch_join<true, 256>(a, st) : launch_join<true, 128>(a, st);
   return a.big ? launch_join<false, 256>(a, st) : launch_join<false, 128>(a, st);
 }

@@ -4,10 +4,10 @@
 #include "matmul.h"
 namespace moe {
 
-template <bool F16, bool AKC, bool BKC, int BM, int BN, int WM, int WN, bool ALIGNED, bool EPI>
+template <bool F16, bool AKC, bool BKC, int BM, int BN, int WM, int WN, bool ALIGNED, bool EPI, bool GATED = false>
 hipError_t launch_matmul_tile(const MatmulArgs& a, hipStream_t st) {
   constexpr bool WG = !AKC;
-  const long long NT = ceil_div(a.n, BN);
+  const long long NT = ceil_div(a.n, GATED && AKC && BKC ? BN / 2 : BN);
   long long ub;                                   // at least the tiles of the list
   if (!WG && a.offsets != nullptr)
     ub = ((long long)a.rows / BM + (a.E < a.rows ? a.E : a.rows)) * NT;
@@ -20,16 +20,16 @@ hipError_t launch_matmul_tile(const MatmulArgs& a, hipStream_t st) {
   constexpr long long kResident = 256 * (BM * BN > 128 * 128 ? 1 : 2);
   if (grid > kResident) grid = kResident;
   if (grid <= 0) return hipSuccess;
-  hipLaunchKernelGGL((matmul_tile_kernel<F16, AKC, BKC, BM, BN, WM, WN, ALIGNED, EPI>), dim3((unsigned)grid),
+  hipLaunchKernelGGL((matmul_tile_kernel<F16, AKC, BKC, BM, BN, WM, WN, ALIGNED, EPI, GATED>), dim3((unsigned)grid),
                      dim3(64 * WM * WN), 0, st, a);
   return hipGetLastError();
 }
 
-template <bool F16, bool AKC, bool BKC, bool EPI>
+template <bool F16, bool AKC, bool BKC, bool EPI, bool GATED = false>
 hipError_t launch_matmul_sizes(const MatmulArgs& a, hipStream_t st) {
-  if (!a.aligned) return launch_matmul_tile<F16, AKC, BKC, 128, 128, 2, 2, false, EPI>(a, st);
-  if (a.big) return launch_matmul_tile<F16, AKC, BKC, 256, 256, 2, 4, true, EPI>(a, st);
-  return launch_matmul_tile<F16, AKC, BKC, 128, 128, 2, 2, true, EPI>(a, st);
+  if (!a.aligned) return launch_matmul_tile<F16, AKC, BKC, 128, 128, 2, 2, false, EPI, GATED>(a, st);
+  if (a.big) return launch_matmul_tile<F16, AKC, BKC, 256, 256, 2, 4, true, EPI, GATED>(a, st);
+  return launch_matmul_tile<F16, AKC, BKC, 128, 128, 2, 2, true, EPI, GATED>(a, st);
 }
 
 template <bool F16, bool AKC, bool BKC>

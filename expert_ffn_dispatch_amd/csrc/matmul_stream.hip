@@ -31,11 +31,26 @@ __device__ __forceinline__ void finish1(const MatmulArgs& p, float v, int64_t ro
   static_cast<uint16_t*>(p.out)[row * p.ldo + col] = mm_store1<F16>(v);
 }
 
+template <bool F16>
+__device__ __forceinline__ void gate1(const MatmulArgs& p, float g, float u, int64_t row, int col) {
+  if (p.pre != nullptr) {
+    p.pre[row * p.ldp + col] = mm_store1<F16>(g);
+    p.pre2[row * p.ldp2 + col] = mm_store1<F16>(u);
+  }
+  float z[1] = {g};
+  mm_act(z, p.act);
+  static_cast<uint16_t*>(p.out)[row * p.ldo + col] = mm_store1<F16>(z[0] * u);
+}
+
 // NT: the weights are loaded with the non-temporal hint: one group, which reads
 // them once (6144 -> 16384, one row: 36.5 -> 33.4 us; among groups some are read
 // in several passes, 64 rows over 128 experts of 2048 -> 768 23.8 -> 25.1).
-template <bool F16, int RB, int NC, int NW, bool NT>
+// GATED: the block's columns are pairs, sixteen of W_gate and their sixteen of
+// W_up, joined by the activation and the product where the sums are added.
+template <bool F16, int RB, int NC, int NW, bool NT, bool GATED>
 __global__ __launch_bounds__(64 * NW, RB * NC == 1 ? 4 : NW / 4) void matmul_stream_kernel(MatmulArgs p) {
+  constexpr int kOut = GATED ? 8 * NC : 16 * NC;  // output columns of a block
+  static_assert(!GATED || NC % 2 == 0, "pairs of columns");
   // an array per slot: loads into one do not hold up reads of the other
   constexpr int kSlot = 16 * NC * kStK;
   __shared__ __align__(16) uint16_t s0[NW * kSlot];
@@ -46,18 +61,20 @@ __global__ __launch_bounds__(64 * NW, RB * NC == 1 ? 4 : NW / 4) void matmul_str
   uint16_t* w0 = s0 + wave * kSlot;
   uint16_t* w1 = s1 + wave * kSlot;
   MmTile t;
-  for (int step = 0; mm_find_tile<false, 16 * RB, 16 * NC>(p, lane, step, t); ++step) {
+  for (int step = 0; mm_find_tile<false, 16 * RB, kOut>(p, lane, step, t); ++step) {
     mm_scalar(t);
     const int chunks = ceil_div(p.k, kStK);
     const int n = wave < chunks ? (chunks - wave + NW - 1) / NW : 0;   // this wave's
     const __amdgpu_buffer_rsrc_t wr = mm_rsrc(p.b + (int64_t)t.e * p.b_group + (int64_t)t.col0 * p.ldb);
+    const __amdgpu_buffer_rsrc_t wr2 =
+        GATED ? mm_rsrc(p.b2 + (int64_t)t.e * p.b_group + (int64_t)t.col0 * p.ldb) : wr;
     const __amdgpu_buffer_rsrc_t xr = mm_rsrc(p.a + (int64_t)(t.g0 + t.row0) * p.lda);
     // weight rows 4 i + (lane >> 4) of load i, 16-byte piece (lane & 15) ^ (row & 15)
     uint32_t wo[4 * NC];
     int wk[4];
 #pragma unroll
     for (int i = 0; i < 4 * NC; ++i) {
-      const int r = 4 * i + fg;
+      const int r = GATED ? 16 * (i >> 3) + 4 * (i & 3) + fg : 4 * i + fg;    // of its matrix
       wk[i & 3] = (fr ^ (r & 15)) * 8;
       wo[i] = t.col0 + r < p.n ? (uint32_t)r * (uint32_t)(2 * p.ldb) + (uint32_t)(wk[i & 3] * 2) : kMmOut;
     }
@@ -77,8 +94,9 @@ __global__ __launch_bounds__(64 * NW, RB * NC == 1 ? 4 : NW / 4) void matmul_str
 #pragma unroll
       for (int i = 0; i < 4 * NC; ++i) {
         const uint32_t o = k0 + wk[i & 3] < p.k ? wo[i] : kMmOut;
-        if constexpr (NT) mm_dma16_nt(wr, o, (uint32_t)(2 * k0), dst + 512 * i);
-        else mm_dma16(wr, o, (uint32_t)(2 * k0), dst + 512 * i);
+        const __amdgpu_buffer_rsrc_t w = GATED && (i & 4) ? wr2 : wr;
+        if constexpr (NT) mm_dma16_nt(w, o, (uint32_t)(2 * k0), dst + 512 * i);
+        else mm_dma16(w, o, (uint32_t)(2 * k0), dst + 512 * i);
       }
     };
     auto load_x = [&](u32x4_t (&x)[RB][4], int c) __attribute__((always_inline)) {
@@ -138,6 +156,19 @@ __global__ __launch_bounds__(64 * NW, RB * NC == 1 ? 4 : NW / 4) void matmul_str
       for (int j = 0; j < NC; ++j)
         *reinterpret_cast<f32x4_t*>(part + (16 * b + fr) * 16 * NC + 16 * j + 4 * (fg ^ (fr & 3))) = acc[j][b];
     __syncthreads();
+    if constexpr (GATED) {
+      for (int i = tid; i < RB * NC * 128; i += 64 * NW) {
+        const int row = i / kOut, c = i % kOut, col = t.col0 + c;
+        const int at = row * 16 * NC + 32 * (c >> 4) + ((c & 15) ^ (4 * (row & 3)));
+        float g = 0.f, u = 0.f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+          g += reinterpret_cast<const float*>(s0 + w * kSlot)[at];
+          u += reinterpret_cast<const float*>(s0 + w * kSlot)[at + 16];
+        }
+        if (row < t.nrows && col < p.n) gate1<F16>(p, g, u, (int64_t)t.g0 + t.row0 + row, col);
+      }
+    } else
     for (int i = tid; i < RB * NC * 256; i += 64 * NW) {
       const int row = i / (16 * NC), c = i % (16 * NC), col = t.col0 + (c ^ (4 * (row & 3)));
       float v = 0.f;
@@ -149,13 +180,13 @@ __global__ __launch_bounds__(64 * NW, RB * NC == 1 ? 4 : NW / 4) void matmul_str
   }
 }
 
-template <bool F16, int RB, int NC, int NW, bool NT>
+template <bool F16, int RB, int NC, int NW, bool NT, bool GATED = false>
 hipError_t stream_go(const MatmulArgs& a, hipStream_t st) {
   const long long groups = a.offsets != nullptr ? (a.E < a.rows ? a.E : a.rows) : 1;
-  long long grid = ((long long)a.rows / (16 * RB) + groups) * ceil_div(a.n, 16 * NC);
+  long long grid = ((long long)a.rows / (16 * RB) + groups) * ceil_div(a.n, GATED ? 8 * NC : 16 * NC);
   grid = (grid + 7) / 8 * 8;
   if (grid > (1 << 20)) grid = 1 << 20;
-  hipLaunchKernelGGL((matmul_stream_kernel<F16, RB, NC, NW, NT>), dim3((unsigned)grid), dim3(64 * NW), 0, st, a);
+  hipLaunchKernelGGL((matmul_stream_kernel<F16, RB, NC, NW, NT, GATED>), dim3((unsigned)grid), dim3(64 * NW), 0, st, a);
   return hipGetLastError();
 }
 // Columns per block: sixteen (eight waves) for up to sixteen rows; above, as
@@ -169,8 +200,20 @@ hipError_t stream_dense(const MatmulArgs& a, hipStream_t st) {
   if (a.n < 192 * 64) return stream_go<F16, RB, 2, 4, true>(a, st);
   return stream_go<F16, RB, 4, 4, true>(a, st);
 }
+template <bool F16, int RB>
+hipError_t stream_gated(const MatmulArgs& a, hipStream_t st) {
+  if (a.n < 192 * 32) return stream_go<F16, RB, 2, 4, true, true>(a, st);
+  return stream_go<F16, RB, 4, 4, true, true>(a, st);
+}
 template <bool F16>
 hipError_t stream_rows(const MatmulArgs& a, hipStream_t st) {
+  if (a.gated) {
+    if (a.offsets != nullptr) return stream_go<F16, 1, 2, 4, false, true>(a, st);
+    if (a.rows <= 16) return stream_gated<F16, 1>(a, st);
+    if (a.rows <= 32) return stream_gated<F16, 2>(a, st);
+    if (a.rows <= 48) return stream_gated<F16, 3>(a, st);
+    return stream_gated<F16, 4>(a, st);
+  }
   // groups of a row or two: 32 columns (64 rows over 128 experts of 2048 ->
   // 768 24.2 us, 31.9 with sixteen)
   if (a.offsets != nullptr) return stream_go<F16, 1, 2, 4, false>(a, st);

@@ -494,6 +494,57 @@ int moe_grouped_matmul_wgrad_workspace_bytes(const moe_grouped_dims* dims, size_
 int moe_grouped_matmul_wgrad(const moe_grouped_dims* dims, const void* dy, const void* x,
                              const int32_t* expert_offsets, void* dw, void* ws, size_t ws_bytes, moe_stream stream);
 
+typedef struct moe_gated_dims {
+  int32_t rows;           /* rows of x and h (grouped: at least expert_offsets[E])     */
+  int32_t n_experts;      /* moe_grouped_gated*; 1 in moe_gated_linear*                */
+  int32_t in_features, width;
+  int32_t dtype;          /* x, w_*, h, gate, up, dh, dx: bf16 or fp16                 */
+  int32_t act;            /* moe_act, of the gate                                      */
+  int32_t dw_dtype;       /* dw_gate, dw_up: dtype or MOE_DTYPE_F32                    */
+  int64_t ld_x, ld_dx;
+  int64_t ld_w;           /* moe_gated_linear*: w_gate, w_up (grouped: 0 or packed)    */
+  int64_t ld_h;           /* h, dh                                                     */
+  int64_t ld_pre;         /* gate, up                                                  */
+} moe_gated_dims;
+
+/*
+ * The gated projections of a feed-forward block, in training and alone:
+ *   gate = x w_gate^T,  up = x w_up^T,  h = act(gate) * up
+ * in one pass: both products of a column end in one lane, and h is made of the
+ * fp32 sums.  x [rows][in]; w_gate / w_up [width][in] (grouped: [E][width][in],
+ * rows by expert as above); h [rows][width]; gate / up [rows][width] or both
+ * NULL: the products rounded to dtype, for the backward pass.
+ * (moe_grouped_ffn fuses the same with the down projection's launch and keeps
+ * nothing.)
+ * ws: moe_gated_linear_workspace_bytes (may be 0); the grouped form needs none.
+ */
+int moe_gated_linear_workspace_bytes(const moe_gated_dims* dims, size_t* bytes);
+int moe_gated_linear(const moe_gated_dims* dims, const void* x, const void* w_gate, const void* w_up, void* h,
+                     void* gate, void* up, void* ws, size_t ws_bytes, moe_stream stream);
+int moe_grouped_gated(const moe_gated_dims* dims, const void* x, const int32_t* expert_offsets, const void* w_gate,
+                      const void* w_up, void* h, void* gate, void* up, moe_stream stream);
+
+/*
+ * Their gradients, from dh and the saved products:
+ *   dgate = dh * up * act'(gate),  dup = dh * act(gate)
+ * (rounded to dtype as operands of the products; relu's slope at 0 is 0),
+ *   dx = dgate w_gate + dup w_up,  dw_gate = dgate^T x,  dw_up = dup^T x.
+ * dx [rows][in], dw_gate / dw_up [width][in] packed (grouped: [E][width][in],
+ * zero for an expert without rows): outputs; dx or both of dw_gate and dw_up
+ * may be NULL (x may be NULL without dw_*, w_* without dx).  Grouped: rows
+ * outside every group are neither read nor written, offsets are clamped as above.
+ * ws: the function of the same name with _workspace_bytes.
+ */
+int moe_gated_linear_backward_workspace_bytes(const moe_gated_dims* dims, size_t* bytes);
+int moe_gated_linear_backward(const moe_gated_dims* dims, const void* dh, const void* x, const void* w_gate,
+                              const void* w_up, const void* gate, const void* up, void* dx, void* dw_gate,
+                              void* dw_up, void* ws, size_t ws_bytes, moe_stream stream);
+int moe_grouped_gated_backward_workspace_bytes(const moe_gated_dims* dims, size_t* bytes);
+int moe_grouped_gated_backward(const moe_gated_dims* dims, const void* dh, const void* x,
+                               const int32_t* expert_offsets, const void* w_gate, const void* w_up, const void* gate,
+                               const void* up, void* dx, void* dw_gate, void* dw_up, void* ws, size_t ws_bytes,
+                               moe_stream stream);
+
 #ifdef __cplusplus
 }
 #endif
