@@ -3,7 +3,7 @@ permutation, grouped SwiGLU expert GEMMs, shared experts and combine as HIP
 kernels behind a C ABI (include/moe_ffn.h), with the layer norm, linear layers
 and products grouped by expert around it and their gradients.  This package holds the kernels
 (csrc/), their build step and a thin ctypes binding."""
-from .api import (Fp8Weights, dims, moe_combine, moe_gated_linear, moe_gated_linear_backward, moe_grouped_ffn, moe_grouped_ffn_fp8,
+from .api import (AdamWTensors, Fp8Moment, Fp8Weights, dims, moe_adamw, moe_combine, moe_gated_linear, moe_gated_linear_backward, moe_grouped_ffn, moe_grouped_ffn_fp8,
                   moe_grouped_ffn_workspace_bytes, moe_grouped_gated, moe_grouped_gated_backward, moe_grouped_matmul, moe_grouped_matmul_dgrad,
                   moe_grouped_matmul_wgrad, moe_layer, moe_layer_fp8, moe_layer_noalloc, moe_layer_pipelined,
                   moe_layer_norm, moe_layer_norm_backward, moe_layer_pipelined_workspace_bytes,

@@ -30,7 +30,7 @@ EXPORTS = (
     "moe_grouped_matmul_wgrad",
     "moe_gated_linear_workspace_bytes", "moe_gated_linear", "moe_grouped_gated",
     "moe_gated_linear_backward_workspace_bytes", "moe_gated_linear_backward",
-    "moe_grouped_gated_backward_workspace_bytes", "moe_grouped_gated_backward",
+    "moe_grouped_gated_backward_workspace_bytes", "moe_grouped_gated_backward", "moe_adamw",
 )
 # bytes of the library's own workspace array (moe_layer_noalloc)
 MOE_NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -76,6 +76,23 @@ class MoeGroupedDims(ctypes.Structure):
 class MoeGatedDims(ctypes.Structure):
     _fields_ = ([(n, ctypes.c_int32) for n in ("rows", "n_experts", "in_features", "width", "dtype", "act", "dw_dtype")]
                 + [(n, ctypes.c_int64) for n in ("ld_x", "ld_dx", "ld_w", "ld_h", "ld_pre")])
+
+
+MOE_ADAMW_FP8 = 1
+MOE_ADAMW_BLOCK = 128
+
+
+class MoeAdamWArgs(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_double) for n in ("lr", "beta1", "beta2", "eps", "weight_decay")]
+                + [("step", ctypes.c_int32), ("flags", ctypes.c_uint32)]
+                + [(n, ctypes.c_void_p) for n in ("lr_device", "step_device", "grad_scale")])
+
+
+class MoeAdamWTensor(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("param", "grad", "exp_avg", "exp_avg_sq", "exp_avg_exp",
+                                                "exp_avg_sq_exp", "copy")]
+                + [("numel", ctypes.c_int64)]
+                + [(n, ctypes.c_int32) for n in ("param_dtype", "grad_dtype", "copy_dtype")])
 
 
 class MoeError(RuntimeError):
@@ -139,6 +156,7 @@ def load() -> ctypes.CDLL:
     lib.moe_gated_linear_backward.argtypes = [GAT] + [P] * 10 + [SIZE, P]
     lib.moe_grouped_gated_backward_workspace_bytes.argtypes = [GAT, OUT]
     lib.moe_grouped_gated_backward.argtypes = [GAT] + [P] * 11 + [SIZE, P]
+    lib.moe_adamw.argtypes = [ctypes.POINTER(MoeAdamWArgs), ctypes.POINTER(MoeAdamWTensor), ctypes.c_int32, P]
     for name in EXPORTS[2:]:
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib

@@ -7,7 +7,7 @@ views of the same bits.  Output tensors are allocated with torch (device
 memory is torch's; the library never allocates).
 """
 import ctypes
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -727,3 +727,134 @@ def moe_grouped_gated_backward(dh, x, expert_offsets, w_gate, w_up, gate, up, ac
     if expert_offsets is None:
         raise ValueError("expert_offsets: expected [E+1]")
     return _gated_backward(dh, x, w_gate, w_up, gate, up, expert_offsets, act, want_dx, want_dw, dw_dtype, dx, stream)
+
+
+class Fp8Moment(NamedTuple):
+    """An 8-bit optimiser state: E4M3 codes [numel] (torch.float8_e4m3fn) and
+    one exponent (torch.uint8) for every 128 of them; value = code *
+    2^(exponent - 127).  All bytes zero is a state of zeros."""
+    codes: torch.Tensor
+    exps: torch.Tensor
+
+    @classmethod
+    def zeros(cls, param):
+        n = param.numel()
+        return cls(torch.zeros(n, dtype=torch.uint8, device=param.device).view(torch.float8_e4m3fn),
+                   torch.zeros(-(-n // _lib.MOE_ADAMW_BLOCK), dtype=torch.uint8, device=param.device))
+
+    def values(self):
+        """The state in fp32 (for the second moment: its square root)."""
+        n = self.codes.numel()
+        scale = torch.where(self.exps == 255, float("nan"), torch.exp2(self.exps.double() - 127)).float()
+        return self.codes.view(-1).float() * scale.repeat_interleave(_lib.MOE_ADAMW_BLOCK)[:n]
+
+
+class AdamWTensors:
+    """The tensors that moe_adamw updates, looked over once: params (bf16, fp16
+    or fp32), their first and second moments (fp32 tensors of the same sizes, or
+    Fp8Moment, all of one kind) and, where given, copies (bf16 or fp16, None for
+    a parameter without one) that receive the new parameters.  Contiguous, on
+    one device, without overlaps; the object keeps references to all."""
+
+    def __init__(self, params, exp_avg, exp_avg_sq, copies=None):
+        params, exp_avg, exp_avg_sq = list(params), list(exp_avg), list(exp_avg_sq)
+        copies = [None] * len(params) if copies is None else list(copies)
+        if not len(params) == len(exp_avg) == len(exp_avg_sq) == len(copies):
+            raise ValueError("params, exp_avg, exp_avg_sq and copies: different lengths")
+        self.fp8 = bool(params) and isinstance(exp_avg[0], Fp8Moment)
+        self.device = params[0].device if params else None
+        self.numels = [p.numel() for p in params]
+        self.count = len(params)
+        self._table = (_lib.MoeAdamWTensor * max(1, self.count))()
+        self._slots = []                        # (tensor, entry's index, field) of every address in the table
+        spans = []
+
+        def place(i, field, t, n, dtypes, name):
+            if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != self.device:
+                raise ValueError(f"{name} {i}: expected a tensor on {self.device}")
+            if t.dtype not in dtypes:
+                raise TypeError(f"{name} {i}: dtype {t.dtype} not in {tuple(dtypes)}")
+            if t.numel() != n or not t.is_contiguous():
+                raise ValueError(f"{name} {i}: expected {n} contiguous values, got shape {tuple(t.shape)}")
+            self._slots.append((t, i, field))
+            setattr(self._table[i], field, t.data_ptr())
+            if n:
+                spans.append((t.data_ptr(), t.data_ptr() + n * t.element_size(), f"{name} {i}"))
+
+        for i, (p, m, v, c) in enumerate(zip(params, exp_avg, exp_avg_sq, copies)):
+            n = self.numels[i]
+            place(i, "param", p, n, _DTYPES, "param")
+            for t, field in ((m, "exp_avg"), (v, "exp_avg_sq")):
+                if isinstance(t, Fp8Moment) != self.fp8:
+                    raise TypeError(f"{field} {i}: 8-bit and 32-bit states in one list")
+                if self.fp8:
+                    place(i, field, t.codes, n, (torch.float8_e4m3fn,), field + " codes")
+                    place(i, field + "_exp", t.exps, -(-n // _lib.MOE_ADAMW_BLOCK), (torch.uint8,), field + " exponents")
+                else:
+                    place(i, field, t, n, (torch.float32,), field)
+            if c is not None:
+                place(i, "copy", c, n, _HALVES, "copy")
+                self._table[i].copy_dtype = _DTYPES[c.dtype]
+            self._table[i].numel = n
+            self._table[i].param_dtype = _DTYPES[p.dtype]
+        spans.sort()
+        for a, b in zip(spans, spans[1:]):
+            if b[0] < a[1]:
+                raise ValueError(f"{a[2]} and {b[2]} overlap")
+        self._at = [t.data_ptr() for t, _, _ in self._slots]
+
+    def _entries(self, grads):
+        """The table with this step's gradients."""
+        at = [s[0].data_ptr() for s in self._slots]
+        if at != self._at:                      # a tensor was given other memory (param.data = ...)
+            raise ValueError("a tensor's memory has moved since the list was made")
+        table, numels, device = self._table, self.numels, self.device
+        if len(grads) != self.count:
+            raise ValueError(f"grads: {len(grads)} for {self.count} parameters")
+        for i, g in enumerate(grads):
+            e = table[i]
+            if g is None:
+                e.grad = None
+                continue
+            if g.device != device or g.numel() != numels[i] or not g.is_contiguous():
+                raise ValueError(f"grad {i}: expected {numels[i]} contiguous values on {device}, got shape "
+                                 f"{tuple(g.shape)} on {g.device}")
+            code = _DTYPES.get(g.dtype)
+            if code is None:
+                raise TypeError(f"grad {i}: dtype {g.dtype} not in {tuple(_DTYPES)}")
+            e.grad = g.data_ptr()
+            e.grad_dtype = code
+        return table
+
+
+def _scalar(t, name, dtype, device):
+    """(value, None) of a number, (0, address) of a one-element device tensor."""
+    if not isinstance(t, torch.Tensor):
+        return t, None
+    if t.device != device or t.dtype != dtype or t.numel() != 1:
+        raise ValueError(f"{name}: expected a number or one {dtype} on {device}")
+    return 0, t.data_ptr()
+
+
+def moe_adamw(tensors: AdamWTensors, grads, step, lr, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
+              weight_decay: float = 0.01, grad_scale=None, stream=None):
+    """One AdamW step in place over all tensors; grads: one for each (bf16, fp16
+    or fp32; None leaves its parameter as it is).  step (from 1) and lr: numbers,
+    or one-element device tensors (int32, fp32), which a captured call reads at
+    every replay.  grad_scale: a one-element fp32 device tensor that the
+    gradients are multiplied by, or None."""
+    dev = tensors.device
+    if dev is None:
+        return
+    step, p_step = _scalar(step, "step", torch.int32, dev)
+    lr, p_lr = _scalar(lr, "lr", torch.float32, dev)
+    p_scale = None
+    if grad_scale is not None:
+        if not isinstance(grad_scale, torch.Tensor):
+            raise TypeError("grad_scale: expected a one-element fp32 device tensor")
+        p_scale = _scalar(grad_scale, "grad_scale", torch.float32, dev)[1]
+    table = tensors._entries(grads)
+    a = _lib.MoeAdamWArgs(lr, beta1, beta2, eps, weight_decay, step, _lib.MOE_ADAMW_FP8 if tensors.fp8 else 0, p_lr,
+                          p_step, p_scale)
+    with _On(dev, stream) as st:
+        _lib.check(_lib.load().moe_adamw(ctypes.byref(a), table, tensors.count, st))

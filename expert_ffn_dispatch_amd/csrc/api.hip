@@ -1,5 +1,6 @@
 // C ABI of the MoE FFN layer: argument checks, workspace carving and the
 // launch sequence.  Every check runs on the host before anything is enqueued.
+#include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
 
@@ -1035,6 +1036,53 @@ int run_gated_backward(const char* fn, const moe_gated_dims* dims, bool grouped,
   return ok();
 }
 
+constexpr int64_t kMaxNumel = 1LL << 36;
+
+int check_adamw(const char* fn, const moe_adamw_args* a, const moe_adamw_tensor* tensors, int count) {
+  if (a == nullptr) return fail(MOE_ERR_INVALID, "%s: args is NULL", fn);
+  if (a->flags & ~uint32_t(MOE_ADAMW_FP8)) return fail(MOE_ERR_INVALID, "%s: unknown flags 0x%x", fn, a->flags);
+  if (!isfinite(a->lr) || !isfinite(a->weight_decay)) return fail(MOE_ERR_INVALID, "%s: lr and weight_decay must be finite", fn);
+  if (!(a->beta1 >= 0 && a->beta1 < 1) || !(a->beta2 >= 0 && a->beta2 < 1))
+    return fail(MOE_ERR_INVALID, "%s: beta1 and beta2 must be in [0, 1)", fn);
+  if (!(a->eps >= 0) || !isfinite(a->eps)) return fail(MOE_ERR_INVALID, "%s: eps must be finite and >= 0", fn);
+  if (a->step < 1 && a->step_device == nullptr) return fail(MOE_ERR_INVALID, "%s: step=%d must be >= 1", fn, a->step);
+  OPT_ELEM(a->lr_device, MOE_DTYPE_F32);
+  OPT_ELEM(a->step_device, MOE_DTYPE_F32);
+  OPT_ELEM(a->grad_scale, MOE_DTYPE_F32);
+  if (count < 0) return fail(MOE_ERR_INVALID, "%s: count=%d", fn, count);
+  if (count > 0 && tensors == nullptr) return fail(MOE_ERR_INVALID, "%s: tensors is NULL", fn);
+  const bool fp8 = (a->flags & MOE_ADAMW_FP8) != 0;
+  for (int i = 0; i < count; ++i) {
+    const moe_adamw_tensor& t = tensors[i];
+    if (t.numel < 0 || t.numel > kMaxNumel)
+      return fail(MOE_ERR_INVALID, "%s: numel=%lld of tensor %d outside [0, 2^36]", fn, (long long)t.numel, i);
+    if (t.param_dtype < MOE_DTYPE_BF16 || t.param_dtype > MOE_DTYPE_F32)
+      return fail(MOE_ERR_INVALID, "%s: unknown param_dtype %d of tensor %d", fn, t.param_dtype, i);
+    if (t.grad_dtype < MOE_DTYPE_BF16 || t.grad_dtype > MOE_DTYPE_F32)
+      return fail(MOE_ERR_INVALID, "%s: unknown grad_dtype %d of tensor %d", fn, t.grad_dtype, i);
+    if (t.copy != nullptr && t.copy_dtype != MOE_DTYPE_BF16 && t.copy_dtype != MOE_DTYPE_F16)
+      return fail(MOE_ERR_INVALID, "%s: copy_dtype=%d of tensor %d must be bf16 or fp16", fn, t.copy_dtype, i);
+    if (t.numel == 0 || t.grad == nullptr) continue;
+    REQ_ELEM(t.param, t.param_dtype);
+    REQ_ELEM(t.grad, t.grad_dtype);
+    OPT_ELEM(t.copy, t.copy_dtype);
+    if (t.exp_avg == nullptr || t.exp_avg_sq == nullptr)
+      return fail(MOE_ERR_INVALID, "%s: tensor %d has no exp_avg or exp_avg_sq", fn, i);
+    if (fp8) {
+      if (t.exp_avg_exp == nullptr || t.exp_avg_sq_exp == nullptr)
+        return fail(MOE_ERR_INVALID, "%s: tensor %d has no exponents of its 8-bit states", fn, i);
+    } else {
+      REQ_ELEM(t.exp_avg, MOE_DTYPE_F32);
+      REQ_ELEM(t.exp_avg_sq, MOE_DTYPE_F32);
+    }
+    const void* own[] = {t.param, t.exp_avg, t.exp_avg_sq, t.grad, t.copy};
+    for (int x = 0; x < 5; ++x)
+      for (int y = 0; y < x; ++y)
+        if (own[x] != nullptr && own[x] == own[y]) return fail(MOE_ERR_INVALID, "%s: two arrays of tensor %d are one", fn, i);
+  }
+  return MOE_OK;
+}
+
 // A copy of the caller's dims to resolve strides in.
 #define COPY_DIMS(type, d)                                                                \
   if (dims == nullptr) return fail(MOE_ERR_INVALID, "%s: dims is NULL", fn);             \
@@ -1634,6 +1682,47 @@ int moe_grouped_gated_backward(const moe_gated_dims* dims, const void* dh, const
                                moe_stream stream) {
   return run_gated_backward("moe_grouped_gated_backward", dims, true, dh, x, expert_offsets, w_gate, w_up, gate, up, dx,
                             dw_gate, dw_up, ws, ws_bytes, stream);
+}
+
+int moe_adamw(const moe_adamw_args* args, const moe_adamw_tensor* tensors, int32_t count, moe_stream stream) {
+  const char* fn = "moe_adamw";
+  if (int r = check_adamw(fn, args, tensors, count)) return r;
+  moe::AdamWArgs a{};
+  a.fp8 = (args->flags & MOE_ADAMW_FP8) != 0;
+  a.step = args->step;
+  a.b1 = (float)args->beta1;
+  a.a1 = (float)(1.0 - args->beta1);
+  a.b2 = (float)args->beta2;
+  a.a2 = (float)(1.0 - args->beta2);
+  a.eps = (float)args->eps;
+  a.lr = args->lr;
+  a.decay = args->weight_decay;
+  a.beta1 = args->beta1;
+  a.beta2 = args->beta2;
+  a.keep = (float)(1.0 - args->lr * args->weight_decay);
+  a.size = (float)(args->lr / (1.0 - pow(args->beta1, args->step)));
+  a.root = (float)(1.0 / sqrt(1.0 - pow(args->beta2, args->step)));
+  a.lr_dev = args->lr_device;
+  a.step_dev = args->step_device;
+  a.grad_scale = args->grad_scale;
+  int64_t total = 0;
+  auto flush = [&]() {
+    const hipError_t e = a.count > 0 ? moe::launch_adamw(a, static_cast<hipStream_t>(stream)) : hipSuccess;
+    a.count = 0;
+    total = 0;
+    return e;
+  };
+  for (int i = 0; i < count; ++i) {
+    const moe_adamw_tensor& t = tensors[i];
+    if (t.numel == 0 || t.grad == nullptr) continue;
+    if (a.count == moe::kAdamWTensors || total + t.numel > kMaxNumel)
+      if (hipError_t e = flush()) return device_error(fn, e);
+    a.tensor[a.count++] = moe::AdamWTensor{t.param, t.grad, t.exp_avg, t.exp_avg_sq, t.exp_avg_exp, t.exp_avg_sq_exp, t.copy,
+                                           t.numel, 0, (uint8_t)t.param_dtype, (uint8_t)t.grad_dtype, (uint8_t)t.copy_dtype};
+    total += t.numel;
+  }
+  if (hipError_t e = flush()) return device_error(fn, e);
+  return ok();
 }
 
 }  // extern "C"

@@ -263,4 +263,33 @@ hipError_t launch_norm_forward(const NormArgs& a, hipStream_t st);
 size_t norm_backward_workspace_bytes(int64_t rows, int64_t cols);
 hipError_t launch_norm_backward(const NormArgs& a, void* ws, hipStream_t st);
 
+// ---- AdamW ----
+struct AdamWTensor {
+  void* param;
+  const void* grad;
+  void* m;                   // fp32, or E4M3 codes
+  void* v;                   // fp32, or codes of sqrt(v)
+  uint8_t* m_exp;            // 8-bit states: an exponent for every 128 values
+  uint8_t* v_exp;
+  void* copy;                // or null
+  int64_t numel;             // > 0
+  uint32_t first_chunk;      // set by launch_adamw
+  uint8_t param_type, grad_type, copy_type;
+};
+constexpr int kAdamWTensors = 48;                 // of a launch: its arguments stay below 4 KB
+struct AdamWArgs {
+  AdamWTensor tensor[kAdamWTensors];
+  int count, step, fp8;
+  int chunk;                 // set by launch_adamw: values of a block
+  float b1, a1, b2, a2;      // beta1, 1 - beta1, beta2, 1 - beta2
+  float keep, size, root;    // 1 - lr decay, lr / (1 - beta1^step), 1 / sqrt(1 - beta2^step)
+  float eps;
+  double lr, decay, beta1, beta2;
+  const float* lr_dev;       // or null: lr
+  const int32_t* step_dev;   // or null: step
+  const float* grad_scale;   // or null: 1
+};
+static_assert(sizeof(AdamWArgs) <= 4096, "a kernel's arguments");
+hipError_t launch_adamw(AdamWArgs& a, hipStream_t st);
+
 }  // namespace moe

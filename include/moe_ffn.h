@@ -545,6 +545,63 @@ int moe_grouped_gated_backward(const moe_gated_dims* dims, const void* dh, const
                                const void* up, void* dx, void* dw_gate, void* dw_up, void* ws, size_t ws_bytes,
                                moe_stream stream);
 
+enum {
+  /* moe_adamw: the states are 8-bit codes with exponents */
+  MOE_ADAMW_FP8 = 1u
+};
+/* Values of an 8-bit state that share an exponent. */
+#define MOE_ADAMW_BLOCK 128
+
+typedef struct moe_adamw_args {
+  double lr, beta1, beta2, eps, weight_decay;
+  int32_t step;              /* >= 1: the number of this step                         */
+  uint32_t flags;            /* MOE_ADAMW_FP8 or 0                                    */
+  const float* lr_device;    /* device fp32, in place of lr; or NULL                  */
+  const int32_t* step_device; /* device int32, in place of step (1 if below); or NULL */
+  const float* grad_scale;   /* device fp32 that every gradient is multiplied by (an
+                                inverse loss scale, the clipping of a norm); or NULL  */
+} moe_adamw_args;
+
+/* One tensor, contiguous, of numel values.  The arrays must not overlap each
+ * other's or another tensor's. */
+typedef struct moe_adamw_tensor {
+  void* param;               /* updated in place: any moe_dtype                       */
+  const void* grad;          /* any moe_dtype; NULL: the tensor is left as it is      */
+  void* exp_avg;             /* m: fp32, or E4M3 codes                                */
+  void* exp_avg_sq;          /* v: fp32, or E4M3 codes of sqrt(v)                     */
+  uint8_t* exp_avg_exp;      /* 8-bit states: exponents, ceil(numel / 128); else NULL */
+  uint8_t* exp_avg_sq_exp;
+  void* copy;                /* the new parameters in bf16 or fp16; or NULL           */
+  int64_t numel;             /* 0..2^36                                               */
+  int32_t param_dtype, grad_dtype, copy_dtype;
+} moe_adamw_tensor;
+
+/*
+ * moe_adamw - one AdamW step (decoupled weight decay) over `count` tensors, up
+ * to 48 of them in a launch.  In fp32, with g = grad * grad_scale:
+ *   m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2,
+ *   p = p (1 - lr weight_decay) - lr / c1 * m / (sqrt(v) / sqrt(c2) + eps),
+ *   c1 = 1 - beta1^step,  c2 = 1 - beta2^step;
+ * p is rounded once to its own type and once to the copy's.
+ *
+ * MOE_ADAMW_FP8: m and r = sqrt(v) are E4M3 codes (as for FP8 expert weights)
+ * times 2^(exponent - 127), one exponent for every 128 values of a tensor (the
+ * last block may be short); all bytes zero is a state of zeros.  An exponent is
+ * the least that brings the block's largest magnitude to 448 or below (at least
+ * 1); a magnitude x 2^(127 - exponent) between two codes becomes the upper one
+ * if its part of the step, as the 16 bits below the code's last, plus u reaches
+ * 65536, where u is the low (m) or high (r) half of a hash of the value's
+ * index in its tensor and the step: right on average, since nearest rounding
+ * would hold an average still that moves by less than half a step.  r > 0
+ * keeps a code of at least 1.  A block with a value that is not finite becomes
+ * NaN (exponent 255).  The update itself takes the unrounded m and v.
+ *
+ * tensors: host array, read before the call returns.  With lr_device and
+ * step_device a captured call replays with their values of that time.
+ * beta1, beta2 in [0, 1), eps >= 0, all finite.
+ */
+int moe_adamw(const moe_adamw_args* args, const moe_adamw_tensor* tensors, int32_t count, moe_stream stream);
+
 #ifdef __cplusplus
 }
 #endif
