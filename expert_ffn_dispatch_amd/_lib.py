@@ -30,7 +30,10 @@ EXPORTS = (
     "moe_grouped_matmul_wgrad",
     "moe_gated_linear_workspace_bytes", "moe_gated_linear", "moe_grouped_gated",
     "moe_gated_linear_backward_workspace_bytes", "moe_gated_linear_backward",
-    "moe_grouped_gated_backward_workspace_bytes", "moe_grouped_gated_backward", "moe_adamw",
+    "moe_grouped_gated_backward_workspace_bytes", "moe_grouped_gated_backward", "moe_adamw", "moe_quantize_fp4",
+    "moe_linear_fp4_workspace_bytes", "moe_linear_fp4", "moe_grouped_matmul_fp4_workspace_bytes",
+    "moe_grouped_matmul_fp4", "moe_gated_linear_fp4_workspace_bytes", "moe_gated_linear_fp4",
+    "moe_grouped_gated_fp4_workspace_bytes", "moe_grouped_gated_fp4",
 )
 # bytes of the library's own workspace array (moe_layer_noalloc)
 MOE_NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -76,6 +79,11 @@ class MoeGroupedDims(ctypes.Structure):
 class MoeGatedDims(ctypes.Structure):
     _fields_ = ([(n, ctypes.c_int32) for n in ("rows", "n_experts", "in_features", "width", "dtype", "act", "dw_dtype")]
                 + [(n, ctypes.c_int64) for n in ("ld_x", "ld_dx", "ld_w", "ld_h", "ld_pre")])
+
+
+class MoeFp4Matrix(ctypes.Structure):
+    """struct moe_fp4_matrix: device pointers of 4-bit codes and their exponents."""
+    _fields_ = [("codes", ctypes.c_void_p), ("exps", ctypes.c_void_p)]
 
 
 MOE_ADAMW_FP8 = 1
@@ -156,6 +164,15 @@ def load() -> ctypes.CDLL:
     lib.moe_gated_linear_backward.argtypes = [GAT] + [P] * 10 + [SIZE, P]
     lib.moe_grouped_gated_backward_workspace_bytes.argtypes = [GAT, OUT]
     lib.moe_grouped_gated_backward.argtypes = [GAT] + [P] * 11 + [SIZE, P]
+    F4 = ctypes.POINTER(MoeFp4Matrix)
+    lib.moe_quantize_fp4.argtypes = [P, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, P, P, P]
+    for name, D in (("moe_linear_fp4", LIN), ("moe_grouped_matmul_fp4", GRP), ("moe_gated_linear_fp4", GAT),
+                    ("moe_grouped_gated_fp4", GAT)):
+        getattr(lib, name + "_workspace_bytes").argtypes = [D, OUT]
+    lib.moe_linear_fp4.argtypes = [LIN, P, F4, P, P, P, P, SIZE, P]
+    lib.moe_grouped_matmul_fp4.argtypes = [GRP, P, P, F4, P, P, SIZE, P]
+    lib.moe_gated_linear_fp4.argtypes = [GAT, P, F4, F4, P, P, SIZE, P]
+    lib.moe_grouped_gated_fp4.argtypes = [GAT, P, P, F4, F4, P, P, SIZE, P]
     lib.moe_adamw.argtypes = [ctypes.POINTER(MoeAdamWArgs), ctypes.POINTER(MoeAdamWTensor), ctypes.c_int32, P]
     for name in EXPORTS[2:]:
         getattr(lib, name).restype = ctypes.c_int

@@ -858,3 +858,140 @@ def moe_adamw(tensors: AdamWTensors, grads, step, lr, beta1: float = 0.9, beta2:
                           p_step, p_scale)
     with _On(dev, stream) as st:
         _lib.check(_lib.load().moe_adamw(ctypes.byref(a), table, tensors.count, st))
+
+
+class Fp4Weights(NamedTuple):
+    """4-bit weights [..][out][in]: E2M1 codes [..][out][in / 2], two to a byte
+    (the first in the low half), and one exponent [..][out][in / 32] for every
+    32 of a row, both torch.uint8; weight = code * 2^(exponent - 127)."""
+    codes: torch.Tensor
+    exps: torch.Tensor
+
+    def values(self):
+        """The weights in fp32."""
+        table = torch.tensor([0, .5, 1, 1.5, 2, 3, 4, 6, 0, -.5, -1, -1.5, -2, -3, -4, -6], device=self.codes.device)
+        w = table[torch.stack([self.codes & 15, self.codes >> 4], -1).int()]
+        scale = (self.exps.int() << 23).view(torch.float32)
+        return (w.view(*self.exps.shape, 32) * scale[..., None]).view(*self.exps.shape[:-1], -1)
+
+
+def moe_quantize_fp4(w, stream=None) -> Fp4Weights:
+    """4-bit codes and exponents of contiguous bf16 or fp16 weights
+    [..][out][in], in % 32 == 0."""
+    if not isinstance(w, torch.Tensor) or not w.is_cuda or w.dim() < 2 or not w.is_contiguous():
+        raise ValueError("w: expected a contiguous device tensor [..][out][in]")
+    if w.dtype not in _HALVES:
+        raise TypeError(f"w: dtype {w.dtype} not in {tuple(_HALVES)}")
+    cols = w.shape[-1]
+    rows = w.numel() // cols if cols else 0
+    with _On(w.device, stream) as st:
+        codes = torch.empty((*w.shape[:-1], cols // 2), dtype=torch.uint8, device=w.device)
+        exps = torch.empty((*w.shape[:-1], cols // 32), dtype=torch.uint8, device=w.device)
+        _lib.check(_lib.load().moe_quantize_fp4(w.data_ptr(), _DTYPES[w.dtype], rows, cols, codes.data_ptr(),
+                                                exps.data_ptr(), st))
+    return Fp4Weights(codes, exps)
+
+
+def _fp4(w, name, device, n_in, lead=None):
+    """The C descriptor of 4-bit weights with `lead` dimensions in front of the
+    contraction's n_in (None: any two or three)."""
+    if not isinstance(w, Fp4Weights):
+        raise TypeError(f"{name}: expected Fp4Weights, got {type(w).__name__}")
+    lead = tuple(w.codes.shape[:-1]) if lead is None else lead
+    for t, what, per in ((w.codes, "codes", 2), (w.exps, "exponents", 32)):
+        if t.device != device or t.dtype != torch.uint8:
+            raise ValueError(f"{name}: {what} must be torch.uint8 on {device}, got {t.dtype} on {t.device}")
+        if n_in % 32 or tuple(t.shape) != (*lead, n_in // per) or not t.is_contiguous():
+            raise ValueError(f"{name}: {what} of shape {tuple(t.shape)}, expected a contiguous "
+                             f"{(*lead, f'{n_in} / {per}')} with a multiple of 32 inputs")
+    return _lib.MoeFp4Matrix(w.codes.data_ptr(), w.exps.data_ptr())
+
+
+def moe_linear_fp4(x, w: Fp4Weights, bias=None, residual=None, act: str = "none", y=None, stream=None):
+    """moe_linear with 4-bit weights [out][in]."""
+    _is_matrix(x, "x")
+    dev, dt = x.device, x.dtype
+    rows, n_in = x.shape
+    px, ldx = _mat(x, "x", dev, _HALVES)
+    m = _fp4(w, "w", dev, n_in)
+    if w.codes.dim() != 2:
+        raise ValueError(f"w: codes of shape {tuple(w.codes.shape)}, expected [out][in / 2]")
+    n_out = w.codes.shape[0]
+    bt = _param_type(dt, bias)
+    pr, ldr = _mat(residual, "residual", dev, (dt,), rows, n_out) if residual is not None else (None, 0)
+    code = _act(act)
+    lib = _lib.load()
+    with _On(dev, stream) as st:
+        if y is None:
+            y = torch.empty((rows, n_out), dtype=dt, device=dev)
+        py, ldy = _mat(y, "y", dev, (dt,), rows, n_out)
+        d = _lib.MoeLinearDims(rows, n_in, n_out, _DTYPES[dt], code, _DTYPES[bt], _DTYPES[dt], ldx, 0, ldr, ldy, 0, 0, 0)
+        ws, pws, nws = _ws_for(lib.moe_linear_fp4_workspace_bytes, d, dev)
+        _lib.check(lib.moe_linear_fp4(ctypes.byref(d), px, ctypes.byref(m), _vec(bias, "bias", dev, (bt,), n_out), pr, py,
+                                      pws, nws, st))
+    return y
+
+
+def moe_grouped_matmul_fp4(x, expert_offsets, w: Fp4Weights, y=None, stream=None):
+    """moe_grouped_matmul with 4-bit weights [E][out][in]."""
+    _is_matrix(x, "x")
+    dev, dt = x.device, x.dtype
+    rows, n_in = x.shape
+    px, ldx = _mat(x, "x", dev, _HALVES)
+    m = _fp4(w, "w", dev, n_in)
+    if w.codes.dim() != 3:
+        raise ValueError(f"w: codes of shape {tuple(w.codes.shape)}, expected [E][out][in / 2]")
+    E, n_out = w.codes.shape[:2]
+    if expert_offsets is None:
+        raise ValueError("expert_offsets: expected [E+1]")
+    po = _vec(expert_offsets, "expert_offsets", dev, (torch.int32,), E + 1)
+    lib = _lib.load()
+    with _On(dev, stream) as st:
+        if y is None:
+            y = torch.empty((rows, n_out), dtype=dt, device=dev)
+        py, ldy = _mat(y, "y", dev, (dt,), rows, n_out)
+        d = _lib.MoeGroupedDims(rows, E, n_in, n_out, _DTYPES[dt], _DTYPES[dt], ldx, ldy)
+        ws, pws, nws = _ws_for(lib.moe_grouped_matmul_fp4_workspace_bytes, d, dev)
+        _lib.check(lib.moe_grouped_matmul_fp4(ctypes.byref(d), px, po, ctypes.byref(m), py, pws, nws, st))
+    return y
+
+
+def _gated_fp4(x, w_gate, w_up, offsets, act, h, stream):
+    _is_matrix(x, "x")
+    dev, dt = x.device, x.dtype
+    rows, n_in = x.shape
+    px, ldx = _mat(x, "x", dev, _HALVES)
+    code = _act(act)
+    g = _fp4(w_gate, "w_gate", dev, n_in)
+    shape = tuple(w_gate.codes.shape[:-1])
+    if len(shape) != (1 if offsets is None else 2):
+        raise ValueError(f"w_gate: codes of shape {tuple(w_gate.codes.shape)}")
+    u = _fp4(w_up, "w_up", dev, n_in, shape)
+    E, width = shape if offsets is not None else (1, shape[0])
+    po = _vec(offsets, "expert_offsets", dev, (torch.int32,), E + 1)
+    lib = _lib.load()
+    with _On(dev, stream) as st:
+        if h is None:
+            h = torch.empty((rows, width), dtype=dt, device=dev)
+        ph, ldh = _mat(h, "h", dev, (dt,), rows, width)
+        d = _lib.MoeGatedDims(rows, E, n_in, width, _DTYPES[dt], code, _DTYPES[dt], ldx, 0, 0, ldh, 0)
+        if offsets is None:
+            ws, pws, nws = _ws_for(lib.moe_gated_linear_fp4_workspace_bytes, d, dev)
+            _lib.check(lib.moe_gated_linear_fp4(ctypes.byref(d), px, ctypes.byref(g), ctypes.byref(u), ph, pws, nws, st))
+        else:
+            ws, pws, nws = _ws_for(lib.moe_grouped_gated_fp4_workspace_bytes, d, dev)
+            _lib.check(lib.moe_grouped_gated_fp4(ctypes.byref(d), px, po, ctypes.byref(g), ctypes.byref(u), ph, pws, nws, st))
+    return h
+
+
+def moe_gated_linear_fp4(x, w_gate: Fp4Weights, w_up: Fp4Weights, act: str = "silu", h=None, stream=None):
+    """moe_gated_linear with 4-bit weights [width][in]."""
+    return _gated_fp4(x, w_gate, w_up, None, act, h, stream)
+
+
+def moe_grouped_gated_fp4(x, expert_offsets, w_gate: Fp4Weights, w_up: Fp4Weights, act: str = "silu", h=None,
+                          stream=None):
+    """moe_grouped_gated with 4-bit weights [E][width][in]."""
+    if expert_offsets is None:
+        raise ValueError("expert_offsets: expected [E+1]")
+    return _gated_fp4(x, w_gate, w_up, expert_offsets, act, h, stream)

@@ -958,16 +958,18 @@ int run_gated(const char* fn, const moe_gated_dims* dims, bool grouped, const vo
   return ok();
 }
 
+// Any address, for a workspace's size: it goes by whether there are offsets.
+const int32_t kSomeOffsets = 0;
+
 // Sizes of a backward call's workspace; the grouped form's products are not
 // cut, whatever the offsets say: any address stands for them here.
 int gated_backward_ws(const char* fn, const moe_gated_dims* dims, bool grouped, size_t* bytes) {
-  static const int32_t some = 0;
   if (dims == nullptr) return fail(MOE_ERR_INVALID, "%s: dims is NULL", fn);
   moe_gated_dims d = *dims;
   if (int r = check_gated(fn, d, grouped)) return r;
   if (bytes == nullptr) return fail(MOE_ERR_INVALID, "%s: bytes is NULL", fn);
   Carver c(nullptr);
-  carve_gated_backward(c, d, grouped ? &some : nullptr);
+  carve_gated_backward(c, d, grouped ? &kSomeOffsets : nullptr);
   *bytes = c.off;
   return ok();
 }
@@ -1034,6 +1036,91 @@ int run_gated_backward(const char* fn, const moe_gated_dims* dims, bool grouped,
     if (hipError_t e = moe::launch_matmul(moe::kMmWeightGrad, a, b.products, st)) return device_error(fn, e);
   }
   return ok();
+}
+
+// ------------------------------------------------------- 4-bit weights
+
+int check_fp4_width(const char* fn, int n_in, int64_t ld_w) {
+  if (n_in % 32 != 0)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: in_features=%d must be a multiple of 32 with 4-bit weights", fn, n_in);
+  if (ld_w != n_in) return fail(MOE_ERR_INVALID, "%s: 4-bit weights are packed, ld_w=%lld", fn, (long long)ld_w);
+  return MOE_OK;
+}
+int check_fp4_matrix(const char* fn, const char* which, const moe_fp4_matrix* w) {
+  if (w == nullptr) return fail(MOE_ERR_INVALID, "%s: %s is NULL", fn, which);
+  if (w->codes == nullptr || w->exps == nullptr) return fail(MOE_ERR_INVALID, "%s: %s has a NULL array", fn, which);
+  if (!aligned(w->codes)) return fail(MOE_ERR_INVALID, "%s: %s's codes are not 16-byte aligned", fn, which);
+  return MOE_OK;
+}
+moe::MatmulArgs grouped_args(const moe_grouped_dims& d, const void* x, const int32_t* expert_offsets, const void* w, void* y) {
+  moe::MatmulArgs a{};
+  a.a = static_cast<const uint16_t*>(x);
+  a.lda = d.ld_x;
+  a.b = static_cast<const uint16_t*>(w);
+  a.ldb = d.in_features;
+  a.b_group = (int64_t)d.out_features * d.in_features;
+  a.out = y;
+  a.ldo = d.ld_y;
+  a.offsets = expert_offsets;
+  a.E = d.n_experts;
+  a.rows = a.m = d.rows;
+  a.n = d.out_features;
+  a.k = d.in_features;
+  a.f16 = d.dtype == MOE_DTYPE_F16;
+  return a;
+}
+moe::Fp4Args fp4_args(moe::MatmulArgs a, const moe_fp4_matrix* w, const moe_fp4_matrix* w2) {
+  moe::Fp4Args f{};
+  f.mm = a;
+  f.mm.whole = 0;
+  if (w != nullptr) {
+    f.codes[0] = w->codes;
+    f.exps[0] = w->exps;
+  }
+  if (w2 != nullptr) {
+    f.codes[1] = w2->codes;
+    f.exps[1] = w2->exps;
+  }
+  return f;
+}
+int fp4_bytes(const char* fn, const moe::MatmulArgs& a, size_t* bytes) {
+  if (bytes == nullptr) return fail(MOE_ERR_INVALID, "%s: bytes is NULL", fn);
+  *bytes = align_up(moe::fp4_workspace_bytes(fp4_args(a, nullptr, nullptr)));
+  return ok();
+}
+int run_fp4(const char* fn, const moe::MatmulArgs& a, const moe_fp4_matrix* w, const moe_fp4_matrix* w2, void* ws,
+            size_t ws_bytes, moe_stream stream) {
+  const moe::Fp4Args f = fp4_args(a, w, w2);
+  if (int r = check_ws(fn, ws, ws_bytes, align_up(moe::fp4_workspace_bytes(f)))) return r;
+  if (hipError_t e = moe::launch_fp4(f, ws, static_cast<hipStream_t>(stream))) return device_error(fn, e);
+  return ok();
+}
+int run_gated_fp4(const char* fn, const moe_gated_dims* dims, bool grouped, const void* x, const int32_t* expert_offsets,
+                  const moe_fp4_matrix* w_gate, const moe_fp4_matrix* w_up, void* h, void* ws, size_t ws_bytes,
+                  moe_stream stream) {
+  if (dims == nullptr) return fail(MOE_ERR_INVALID, "%s: dims is NULL", fn);
+  moe_gated_dims d = *dims;
+  if (int r = check_gated(fn, d, grouped)) return r;
+  if (int r = check_fp4_width(fn, d.in_features, d.ld_w)) return r;
+  if (d.rows == 0) return ok();
+  REQ_ELEM(x, d.dtype);
+  if (grouped) REQ_ELEM(expert_offsets, MOE_DTYPE_F32);
+  if (int r = check_fp4_matrix(fn, "w_gate", w_gate)) return r;
+  if (int r = check_fp4_matrix(fn, "w_up", w_up)) return r;
+  REQ_ELEM(h, d.dtype);
+  if (h == x) return fail(MOE_ERR_INVALID, "%s: h is x", fn);
+  moe::MatmulArgs a = gated_args(d, grouped, x, nullptr, nullptr, h);
+  a.offsets = expert_offsets;
+  return run_fp4(fn, a, w_gate, w_up, ws, ws_bytes, stream);
+}
+int gated_fp4_bytes(const char* fn, const moe_gated_dims* dims, bool grouped, size_t* bytes) {
+  if (dims == nullptr) return fail(MOE_ERR_INVALID, "%s: dims is NULL", fn);
+  moe_gated_dims d = *dims;
+  if (int r = check_gated(fn, d, grouped)) return r;
+  if (int r = check_fp4_width(fn, d.in_features, d.ld_w)) return r;
+  moe::MatmulArgs a = gated_args(d, grouped, nullptr, nullptr, nullptr, nullptr);
+  a.offsets = grouped ? &kSomeOffsets : nullptr;
+  return fp4_bytes(fn, a, bytes);
 }
 
 constexpr int64_t kMaxNumel = 1LL << 36;
@@ -1573,20 +1660,7 @@ int moe_grouped_matmul(const moe_grouped_dims* dims, const void* x, const int32_
   REQ_ELEM(w, d.dtype);
   REQ_ELEM(y, d.dtype);
   if (y == x || y == w) return fail(MOE_ERR_INVALID, "%s: y is an input", fn);
-  moe::MatmulArgs a{};
-  a.a = static_cast<const uint16_t*>(x);
-  a.lda = d.ld_x;
-  a.b = static_cast<const uint16_t*>(w);
-  a.ldb = d.in_features;
-  a.b_group = (int64_t)d.out_features * d.in_features;
-  a.out = y;
-  a.ldo = d.ld_y;
-  a.offsets = expert_offsets;
-  a.E = d.n_experts;
-  a.rows = a.m = d.rows;
-  a.n = d.out_features;
-  a.k = d.in_features;
-  a.f16 = d.dtype == MOE_DTYPE_F16;
+  const moe::MatmulArgs a = grouped_args(d, x, expert_offsets, w, y);
   if (hipError_t e = moe::launch_matmul(moe::kMmForward, a, nullptr, static_cast<hipStream_t>(stream)))
     return device_error(fn, e);
   return ok();
@@ -1723,6 +1797,97 @@ int moe_adamw(const moe_adamw_args* args, const moe_adamw_tensor* tensors, int32
   }
   if (hipError_t e = flush()) return device_error(fn, e);
   return ok();
+}
+
+int moe_quantize_fp4(const void* w, int32_t dtype, int64_t rows, int32_t cols, uint8_t* codes, uint8_t* exps,
+                     moe_stream stream) {
+  const char* fn = "moe_quantize_fp4";
+  if (dtype != MOE_DTYPE_BF16 && dtype != MOE_DTYPE_F16)
+    return fail(MOE_ERR_INVALID, "%s: dtype=%d must be bf16 or fp16", fn, dtype);
+  if (rows < 1 || rows > (1LL << 26)) return fail(MOE_ERR_INVALID, "%s: rows=%lld outside [1, 2^26]", fn, (long long)rows);
+  if (cols < 32 || cols > kMaxWidth || cols % 32 != 0)
+    return fail(MOE_ERR_INVALID, "%s: cols=%d must be a multiple of 32 in [32, %d]", fn, cols, kMaxWidth);
+  REQ_PTR(w);
+  REQ_PTR(codes);
+  if (exps == nullptr) return fail(MOE_ERR_INVALID, "%s: exps is NULL", fn);
+  if (hipError_t e = moe::launch_quantize_fp4(static_cast<const uint16_t*>(w), rows, cols, dtype == MOE_DTYPE_F16, codes, exps,
+                                              static_cast<hipStream_t>(stream)))
+    return device_error(fn, e);
+  return ok();
+}
+
+int moe_linear_fp4_workspace_bytes(const moe_linear_dims* dims, size_t* bytes) {
+  const char* fn = "moe_linear_fp4_workspace_bytes";
+  COPY_DIMS(moe_linear_dims, d);
+  if (int r = check_linear(fn, d)) return r;
+  if (int r = check_fp4_width(fn, d.in_features, d.ld_w)) return r;
+  return fp4_bytes(fn, linear_args(d, nullptr, nullptr, nullptr), bytes);
+}
+
+int moe_linear_fp4(const moe_linear_dims* dims, const void* x, const moe_fp4_matrix* w, const void* bias,
+                   const void* residual, void* y, void* ws, size_t ws_bytes, moe_stream stream) {
+  const char* fn = "moe_linear_fp4";
+  COPY_DIMS(moe_linear_dims, d);
+  if (int r = check_linear(fn, d)) return r;
+  if (int r = check_fp4_width(fn, d.in_features, d.ld_w)) return r;
+  if (d.rows == 0) return ok();
+  REQ_ELEM(x, d.dtype);
+  if (int r = check_fp4_matrix(fn, "w", w)) return r;
+  OPT_ELEM(bias, d.bias_dtype);
+  OPT_ELEM(residual, d.dtype);
+  REQ_ELEM(y, d.dtype);
+  if (y == x) return fail(MOE_ERR_INVALID, "%s: y is x", fn);
+  if (residual == y && d.ld_residual != d.ld_y)
+    return fail(MOE_ERR_INVALID, "%s: residual is y with another row stride", fn);
+  moe::MatmulArgs a = linear_args(d, x, nullptr, y);
+  a.bias = bias;
+  a.bias_f32 = d.bias_dtype == MOE_DTYPE_F32;
+  a.act = d.act;
+  a.residual = static_cast<const uint16_t*>(residual);
+  a.ldr = d.ld_residual;
+  return run_fp4(fn, a, w, nullptr, ws, ws_bytes, stream);
+}
+
+int moe_grouped_matmul_fp4_workspace_bytes(const moe_grouped_dims* dims, size_t* bytes) {
+  const char* fn = "moe_grouped_matmul_fp4_workspace_bytes";
+  COPY_DIMS(moe_grouped_dims, d);
+  if (int r = check_grouped(fn, d)) return r;
+  if (int r = check_fp4_width(fn, d.in_features, d.in_features)) return r;
+  return fp4_bytes(fn, grouped_args(d, nullptr, &kSomeOffsets, nullptr, nullptr), bytes);
+}
+
+int moe_grouped_matmul_fp4(const moe_grouped_dims* dims, const void* x, const int32_t* expert_offsets,
+                           const moe_fp4_matrix* w, void* y, void* ws, size_t ws_bytes, moe_stream stream) {
+  const char* fn = "moe_grouped_matmul_fp4";
+  COPY_DIMS(moe_grouped_dims, d);
+  if (int r = check_grouped(fn, d)) return r;
+  if (int r = check_fp4_width(fn, d.in_features, d.in_features)) return r;
+  if (d.rows == 0) return ok();
+  REQ_ELEM(x, d.dtype);
+  REQ_ELEM(expert_offsets, MOE_DTYPE_F32);
+  if (int r = check_fp4_matrix(fn, "w", w)) return r;
+  REQ_ELEM(y, d.dtype);
+  if (y == x) return fail(MOE_ERR_INVALID, "%s: y is x", fn);
+  return run_fp4(fn, grouped_args(d, x, expert_offsets, nullptr, y), w, nullptr, ws, ws_bytes, stream);
+}
+
+int moe_gated_linear_fp4_workspace_bytes(const moe_gated_dims* dims, size_t* bytes) {
+  return gated_fp4_bytes("moe_gated_linear_fp4_workspace_bytes", dims, false, bytes);
+}
+
+int moe_gated_linear_fp4(const moe_gated_dims* dims, const void* x, const moe_fp4_matrix* w_gate,
+                         const moe_fp4_matrix* w_up, void* h, void* ws, size_t ws_bytes, moe_stream stream) {
+  return run_gated_fp4("moe_gated_linear_fp4", dims, false, x, nullptr, w_gate, w_up, h, ws, ws_bytes, stream);
+}
+
+int moe_grouped_gated_fp4_workspace_bytes(const moe_gated_dims* dims, size_t* bytes) {
+  return gated_fp4_bytes("moe_grouped_gated_fp4_workspace_bytes", dims, true, bytes);
+}
+
+int moe_grouped_gated_fp4(const moe_gated_dims* dims, const void* x, const int32_t* expert_offsets,
+                          const moe_fp4_matrix* w_gate, const moe_fp4_matrix* w_up, void* h, void* ws, size_t ws_bytes,
+                          moe_stream stream) {
+  return run_gated_fp4("moe_grouped_gated_fp4", dims, true, x, expert_offsets, w_gate, w_up, h, ws, ws_bytes, stream);
 }
 
 }  // extern "C"

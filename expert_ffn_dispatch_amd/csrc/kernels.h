@@ -225,6 +225,20 @@ struct ActGradArgs {
 size_t act_grad_workspace_bytes(int64_t rows, int64_t n);
 hipError_t launch_act_grad(const ActGradArgs& a, void* ws, hipStream_t st);
 
+// ---- 4-bit weights (fp4.hip) ----
+// Codes [rows][cols / 2] and exponents [rows][cols / 32] of w [rows][cols].
+hipError_t launch_quantize_fp4(const uint16_t* w, long long rows, int cols, int f16, uint8_t* codes, uint8_t* exps,
+                               hipStream_t st);
+struct Fp4Args {
+  MatmulArgs mm;             // the product, forward, without b / b2 / ldb / b_group
+  const uint8_t* codes[2];   // [E][n][k / 2]; the second of gated products
+  const uint8_t* exps[2];    // [E][n][k / 32]
+};
+// Workspace of a call (0: none): where many rows share the weights, these are
+// widened there once, for the products of 16-bit weights.
+size_t fp4_workspace_bytes(const Fp4Args& a);
+hipError_t launch_fp4(const Fp4Args& a, void* ws, hipStream_t st);
+
 // g = [dgate | dup] of the gated projections, from dh and the saved products.
 struct GatedGradArgs {
   const uint16_t* dh;

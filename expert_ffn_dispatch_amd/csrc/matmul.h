@@ -659,6 +659,30 @@ __device__ __forceinline__ void mm_gate8(const MatmulArgs& p, float (&g)[8], flo
   mm_put8<F16>(static_cast<uint16_t*>(p.out) + row * p.ldo + col, u, n);
 }
 
+// One value of the kernels for a few rows: the same two epilogues.
+template <bool F16>
+__device__ __forceinline__ void finish1(const MatmulArgs& p, float v, int64_t row, int col) {
+  if (p.bias != nullptr)
+    v += p.bias_f32 ? static_cast<const float*>(p.bias)[col] : mm_load1<F16>(static_cast<const uint16_t*>(p.bias)[col]);
+  if (p.pre != nullptr) p.pre[row * p.ldp + col] = mm_store1<F16>(v);
+  float z[1] = {v};
+  mm_act(z, p.act);
+  v = z[0];
+  if (p.residual != nullptr) v += mm_load1<F16>(p.residual[row * p.ldr + col]);
+  static_cast<uint16_t*>(p.out)[row * p.ldo + col] = mm_store1<F16>(v);
+}
+
+template <bool F16>
+__device__ __forceinline__ void gate1(const MatmulArgs& p, float g, float u, int64_t row, int col) {
+  if (p.pre != nullptr) {
+    p.pre[row * p.ldp + col] = mm_store1<F16>(g);
+    p.pre2[row * p.ldp2 + col] = mm_store1<F16>(u);
+  }
+  float z[1] = {g};
+  mm_act(z, p.act);
+  static_cast<uint16_t*>(p.out)[row * p.ldo + col] = mm_store1<F16>(z[0] * u);
+}
+
 // -------------------------------------------------------------- the kernel
 
 // The kernel's arguments, read again from the kernarg segment at each use of

@@ -19,29 +19,6 @@ namespace {
 
 constexpr int kStK = 128;                         // contraction per chunk
 
-template <bool F16>
-__device__ __forceinline__ void finish1(const MatmulArgs& p, float v, int64_t row, int col) {
-  if (p.bias != nullptr)
-    v += p.bias_f32 ? static_cast<const float*>(p.bias)[col] : mm_load1<F16>(static_cast<const uint16_t*>(p.bias)[col]);
-  if (p.pre != nullptr) p.pre[row * p.ldp + col] = mm_store1<F16>(v);
-  float z[1] = {v};
-  mm_act(z, p.act);
-  v = z[0];
-  if (p.residual != nullptr) v += mm_load1<F16>(p.residual[row * p.ldr + col]);
-  static_cast<uint16_t*>(p.out)[row * p.ldo + col] = mm_store1<F16>(v);
-}
-
-template <bool F16>
-__device__ __forceinline__ void gate1(const MatmulArgs& p, float g, float u, int64_t row, int col) {
-  if (p.pre != nullptr) {
-    p.pre[row * p.ldp + col] = mm_store1<F16>(g);
-    p.pre2[row * p.ldp2 + col] = mm_store1<F16>(u);
-  }
-  float z[1] = {g};
-  mm_act(z, p.act);
-  static_cast<uint16_t*>(p.out)[row * p.ldo + col] = mm_store1<F16>(z[0] * u);
-}
-
 // NT: the weights are loaded with the non-temporal hint: one group, which reads
 // them once (6144 -> 16384, one row: 36.5 -> 33.4 us; among groups some are read
 // in several passes, 64 rows over 128 experts of 2048 -> 768 23.8 -> 25.1).

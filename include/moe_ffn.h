@@ -545,6 +545,57 @@ int moe_grouped_gated_backward(const moe_gated_dims* dims, const void* dh, const
                                const void* up, void* dx, void* dw_gate, void* dw_up, void* ws, size_t ws_bytes,
                                moe_stream stream);
 
+/*
+ * 4-bit weights: codes of four bits (sign, 2 exponent bits, 1 mantissa bit:
+ * the magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6) and one 8-bit exponent for every
+ * 32 consecutive weights of a row, as the OCP microscaling formats define
+ * them: weight[r][j] = value(code[r][j]) * 2^(exponent[r][j / 32] - 127).
+ * Matrices [out][in] (grouped: [E][out][in]) like the 16-bit ones, in % 32 ==
+ * 0 (else MOE_ERR_UNSUPPORTED): codes [..][out][in / 2] bytes, weight 2 i in the
+ * low half of byte i, and exponents [..][out][in / 32], both packed.
+ * Exponents 1..254; with fp16 data 104..140, at which every code is an fp16
+ * number (others are rounded to fp16).  Device pointers, codes 16-byte aligned.
+ */
+typedef struct moe_fp4_matrix {
+  const uint8_t* codes;
+  const uint8_t* exps;
+} moe_fp4_matrix;
+
+/*
+ * moe_quantize_fp4 - codes and exponents of w [rows][cols], bf16 or fp16: for
+ * every 32 weights the least exponent (within the bounds above; at most 252)
+ * that leaves no magnitude above 7 times its power of two, then the nearest
+ * codes, ties to the even code, 6 above.  Weights must be finite.  w, codes
+ * 16-byte aligned, w packed; 1 <= rows <= 2^26, 32 <= cols <= 65536,
+ * cols % 32 == 0.  A one-off conversion, like moe_quantize_fp8.
+ */
+int moe_quantize_fp4(const void* w, int32_t dtype, int64_t rows, int32_t cols, uint8_t* codes, uint8_t* exps,
+                     moe_stream stream);
+
+/*
+ * The products above with 4-bit weights (w, w_gate, w_up: host pointers to the
+ * pair of arrays): the same results as with 16-bit weights of these values, up
+ * to the order of fp32 sums.  Few rows to a weight read the codes themselves,
+ * 17/32 of a byte a weight, which is what bounds decode (page on MoE latency,
+ * section "router 之后还有一串动作"); for many rows the weights are widened into
+ * the workspace first.  dims as for the function without _fp4 (ld_w 0 or
+ * in_features; dw_dtype, ld_pre and gradients' strides unused), no saved
+ * products.  ws: the function of the same name with _workspace_bytes (may be 0).
+ */
+int moe_linear_fp4_workspace_bytes(const moe_linear_dims* dims, size_t* bytes);
+int moe_linear_fp4(const moe_linear_dims* dims, const void* x, const moe_fp4_matrix* w, const void* bias,
+                   const void* residual, void* y, void* ws, size_t ws_bytes, moe_stream stream);
+int moe_grouped_matmul_fp4_workspace_bytes(const moe_grouped_dims* dims, size_t* bytes);
+int moe_grouped_matmul_fp4(const moe_grouped_dims* dims, const void* x, const int32_t* expert_offsets,
+                           const moe_fp4_matrix* w, void* y, void* ws, size_t ws_bytes, moe_stream stream);
+int moe_gated_linear_fp4_workspace_bytes(const moe_gated_dims* dims, size_t* bytes);
+int moe_gated_linear_fp4(const moe_gated_dims* dims, const void* x, const moe_fp4_matrix* w_gate,
+                         const moe_fp4_matrix* w_up, void* h, void* ws, size_t ws_bytes, moe_stream stream);
+int moe_grouped_gated_fp4_workspace_bytes(const moe_gated_dims* dims, size_t* bytes);
+int moe_grouped_gated_fp4(const moe_gated_dims* dims, const void* x, const int32_t* expert_offsets,
+                          const moe_fp4_matrix* w_gate, const moe_fp4_matrix* w_up, void* h, void* ws,
+                          size_t ws_bytes, moe_stream stream);
+
 enum {
   /* moe_adamw: the states are 8-bit codes with exponents */
   MOE_ADAMW_FP8 = 1u
