@@ -4,15 +4,22 @@
 // their exponent to two 16-bit values in one instruction, exactly, so every
 // product is the one of 16-bit weights of these values.
 //
-// Few rows to a group of weights: fp4_stream_kernel.  A block owns 16 NC
-// columns and 16 RB rows; its NW waves take every NW-th 128-wide chunk of the
-// contraction and add their sums in LDS, in wave order.  A lane loads 16 bytes
-// of codes, 32 consecutive k of one weight row, so that it needs one exponent
-// for all of them; they are the operands of four matrix instructions, each
-// with 8 of every lane's 32 k.  That is a permutation of the chunk's k, which
-// the sums do not mind as long as the rows of x are read in the same one.
-// Nothing passes through LDS on the way and no wave waits for another.
-// Bound by the weights' 17/32 byte.
+// fp4_stream_kernel: a block owns 16 RB rows and 16 NC WN columns; its WK
+// groups of WN waves take every WK-th 128-wide chunk of the contraction and add
+// their sums in LDS, in order.  Codes (64 bytes of a row and chunk) and rows of
+// x go straight into LDS, each load in the order of memory: four lanes to 64
+// bytes, a quarter of the cache's work that loads in the order of the matrix
+// instruction's operands cost (one lane to 16 bytes, each of another row: 64
+// cache accesses a load, which bounded it: 4096 rows over 128 experts' gated
+// projections of 2048 -> 768 158 us with both operands loaded that way, 76 so).
+// A lane reads 16 bytes of codes of one weight row back, four lanes' 4 x 4
+// words are turned by two swaps of lane rows, and each word is a matrix
+// instruction's eight weights.  Exponents come four chunks at a time, spread
+// over the same four lanes.  Waves that share rows of x (WN > 1) meet at a
+// barrier a chunk; with WN = 1 no wave waits for another.
+// Bound by the weights' 17/32 byte for few rows (6144 -> 16384, one row: 12.4
+// us, 4.3 TB/s with the launch), by the conversions and the matrix pipe for
+// many (16384 rows over 32 experts of 4096 -> 1536: 258 us, 0.8 PFLOP/s).
 #include "matmul.h"
 
 namespace moe {
@@ -34,143 +41,281 @@ template <bool F16>
 __device__ __forceinline__ u32x4_t widen8(uint32_t codes, float s) {
   return u32x4_t{widen2<F16, 0>(codes, s), widen2<F16, 1>(codes, s), widen2<F16, 2>(codes, s), widen2<F16, 3>(codes, s)};
 }
+// Scale from byte s of four exponents.  The conversion takes the exponent field alone.
+__device__ __forceinline__ float exponent_of(uint32_t e, int s) { return __uint_as_float(s == 3 ? e >> 1 : e << (23 - 8 * s)); }
 __device__ __forceinline__ float exponent(uint32_t e) { return __uint_as_float(e << 23); }
 
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* base, int size) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, size, 0x00020000);
+}
 __device__ __forceinline__ u32x4_t load16(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff) {
   return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, voff, soff, 0));
 }
 
-// D chunks of codes and one of x are on their way while one is multiplied.
-template <bool F16, int RB, int NC, int NW, int D, bool GATED>
-__global__ __launch_bounds__(64 * NW) void fp4_stream_kernel(Fp4Args a) {
-  constexpr int kOut = GATED ? 8 * NC : 16 * NC;  // output columns of a block
-  static_assert(!GATED || NC % 2 == 0, "pairs of columns");
-  __shared__ __align__(16) float s_part[NW][RB * NC * 256];
+// Four registers by four rows of sixteen lanes, turned: register i of row r
+// becomes register r of row i.
+__device__ __forceinline__ u32x4_t turn(u32x4_t v) {
+#ifdef __HIP_DEVICE_COMPILE__
+  auto a = __builtin_amdgcn_permlane32_swap(v[0], v[2], false, false);
+  auto b = __builtin_amdgcn_permlane32_swap(v[1], v[3], false, false);
+  auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
+  auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+  return u32x4_t{(uint32_t)c[0], (uint32_t)c[1], (uint32_t)d[0], (uint32_t)d[1]};
+#else
+  return v;
+#endif
+}
+
+// NB buffers of a stage (a chunk for each group): NB - 1 stages, or with WN = 1
+// NB, are on their way while one is multiplied.  GATED: columns are pairs,
+// sixteen of W_gate and their sixteen of W_up.  XREG: rows of x of any
+// alignment, which pass through registers (they wait for every load under way).
+// (Registers stay below 256, without copies to the other half of the file.)
+template <bool F16, int RB, int NC, int WN, int WK, int NB, bool GATED, bool XREG>
+__global__ __launch_bounds__(64 * WN * WK, 2) void fp4_stream_kernel(Fp4Args a) {
+  constexpr int NW = WN * WK;
+  constexpr int kCols = 16 * NC * WN;             // columns of a block, pairs counted twice
+  constexpr int kOut = GATED ? kCols / 2 : kCols;
+  constexpr int AX = 4 * RB / WN;                 // loads of x of a wave and stage
+  constexpr int kLoads = NC + (XREG ? 0 : AX);    // of these and of codes that a later stage may leave under way
+  constexpr int XB = 16 * RB * kChunk, WB = NC * 512, STAGE = WK * XB + NW * WB;      // 16-bit words
+  constexpr int PART = NW * RB * NC * 512;
+  constexpr int G = NB == 3 ? 3 : 4;              // stages that share loaded exponents
+  static_assert((!GATED || NC % 2 == 0) && AX * WN == 4 * RB, "whole pairs and loads");
+  __shared__ __align__(16) uint16_t s0[STAGE > PART ? STAGE : PART];
+  __shared__ __align__(16) uint16_t s1[STAGE];
+  __shared__ __align__(16) uint16_t s2[NB > 2 ? STAGE : 8];
+  __shared__ __align__(16) uint16_t s3[NB > 3 ? STAGE : 8];
   const MatmulArgs& p = a.mm;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wk = wave / WN, wn = wave % WN;
   const int fr = lane & 15, fg = lane >> 4;
   const int cpitch = p.k / 2, epitch = p.k / 32;
   MmTile t;
   for (int step = 0; mm_find_tile<false, 16 * RB, kOut>(p, lane, step, t); ++step) {
     mm_scalar(t);
-    const int chunks = ceil_div(p.k, kChunk);
-    const int n = wave < chunks ? (chunks - wave + NW - 1) / NW : 0;   // this wave's
+    const int chunks = ceil_div(p.k, kChunk), n = ceil_div(chunks, WK);
     const int64_t row = (int64_t)t.e * p.n + t.col0;
-    const __amdgpu_buffer_rsrc_t cr = mm_rsrc(a.codes[0] + row * cpitch), er = mm_rsrc(a.exps[0] + row * epitch);
-    const __amdgpu_buffer_rsrc_t cr2 = GATED ? mm_rsrc(a.codes[1] + row * cpitch) : cr;
+    const uint8_t* w0 = a.codes[0] + row * cpitch;
+    const uint8_t* w1 = GATED ? a.codes[1] + row * cpitch : w0;
+    const uint16_t* x0 = p.a + (int64_t)(t.g0 + t.row0) * p.lda;
+    const __amdgpu_buffer_rsrc_t er = mm_rsrc(a.exps[0] + row * epitch);
     const __amdgpu_buffer_rsrc_t er2 = GATED ? mm_rsrc(a.exps[1] + row * epitch) : er;
-    const __amdgpu_buffer_rsrc_t xr = mm_rsrc(p.a + (int64_t)(t.g0 + t.row0) * p.lda);
-    uint32_t co[NC], eo[NC], xo[RB];
+    uint32_t co[NC], eo[NC], xo[AX];
+    const int wpiece = (lane & 3) ^ ((lane >> 4) & 3);
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
-      const int r = (GATED ? 16 * (j >> 1) : 16 * j) + fr;             // of its matrix
-      const bool in = t.col0 + r < p.n;
-      co[j] = in ? (uint32_t)(r * cpitch + fg * 16) : kMmOut;
-      eo[j] = in ? (uint32_t)(r * epitch + fg) : kMmOut;
+      const int first = GATED ? 16 * (wn * (NC / 2) + (j >> 1)) : 16 * (wn * NC + j);  // of its matrix
+      co[j] = t.col0 + first + (lane >> 2) < p.n ? (uint32_t)((first + (lane >> 2)) * cpitch + wpiece * 16) : kMmOut;
+      eo[j] = t.col0 + first + fr < p.n ? (uint32_t)((first + fr) * epitch) : kMmOut;
     }
 #pragma unroll
-    for (int b = 0; b < RB; ++b)
-      xo[b] = 16 * b + fr < t.nrows ? (uint32_t)(16 * b + fr) * (uint32_t)(2 * p.lda) + (uint32_t)(fg * 64) : kMmOut;
+    for (int i = 0; i < AX; ++i) {
+      const int r = 4 * (wn * AX + i) + fg;
+      xo[i] = r < t.nrows ? (uint32_t)r * (uint32_t)(2 * p.lda) + (uint32_t)((fr ^ (r & 15)) * 16) : kMmOut;
+    }
     f32x4_t acc[NC][RB];
 #pragma unroll
     for (int j = 0; j < NC; ++j)
 #pragma unroll
       for (int b = 0; b < RB; ++b) acc[j][b] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    // chunk c of this wave starts at k = 128 (wave + NW c); past the end lanes
-    // take zeros
-    u32x4_t w[D][NC];
-    uint32_t e[D][NC];
-    auto load_w = [&](u32x4_t (&cw)[NC], uint32_t (&ce)[NC], int c) __attribute__((always_inline)) {
-      const int at = wave + NW * c;
-      const bool in = at * kChunk + 32 * fg < p.k;
+    auto put_x = [&](__amdgpu_buffer_rsrc_t rx, uint32_t off, uint32_t at, uint16_t* to) __attribute__((always_inline)) {
+      if constexpr (XREG) *reinterpret_cast<u32x4_t*>(to + lane * 8) = load16(rx, off, at);
+      else mm_dma16(rx, off, at, to);
+    };
+    // stage c of this wave's part of the contraction is chunk wk + WK c
+    auto load = [&](uint16_t* buf, int c) __attribute__((always_inline)) {
+      const int k0 = (wk + WK * c) * kChunk;
+      // past the end: buffers of no bytes, which read as zeros
+      const int size = k0 < p.k ? (int)kMmBytes : 0;
+      const __amdgpu_buffer_rsrc_t rw = rsrc(w0, size), rw2 = GATED ? rsrc(w1, size) : rw, rx = rsrc(x0, size);
+      uint16_t* bw = buf + WK * XB + wave * WB;
+      uint16_t* bx = buf + wk * XB + wn * AX * 512;
+      if (k0 + kChunk <= p.k || size == 0) {
 #pragma unroll
-      for (int j = 0; j < NC; ++j) {
-        const bool second = GATED && (j & 1);
-        cw[j] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(second ? cr2 : cr, in ? co[j] : kMmOut,
-                                                                                  (uint32_t)at * (kChunk / 2), 0));
-        ce[j] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(second ? er2 : er, in ? eo[j] : kMmOut,
-                                                              (uint32_t)at * (kChunk / 32), 0);
+        for (int j = 0; j < NC; ++j) mm_dma16(GATED && (j & 1) ? rw2 : rw, co[j], (uint32_t)k0 / 2, bw + j * 512);
+#pragma unroll
+        for (int i = 0; i < AX; ++i) put_x(rx, xo[i], (uint32_t)k0 * 2, bx + i * 512);
+      } else {
+#pragma unroll
+        for (int j = 0; j < NC; ++j)
+          mm_dma16(GATED && (j & 1) ? rw2 : rw, k0 + wpiece * 32 < p.k ? co[j] : kMmOut, (uint32_t)k0 / 2, bw + j * 512);
+#pragma unroll
+        for (int i = 0; i < AX; ++i) {
+          const int xk = (fr ^ ((4 * (wn * AX + i) + fg) & 15)) * 8;
+          put_x(rx, k0 + xk < p.k ? xo[i] : kMmOut, (uint32_t)k0 * 2, bx + i * 512);
+        }
       }
     };
-    auto load_x = [&](u32x4_t (&x)[RB][4], int c) __attribute__((always_inline)) {
-      const int at = wave + NW * c;
-      const bool in = at * kChunk + 32 * fg < p.k;
+    uint32_t er4[NC];
+    u32x4_t ex[NC];
+    // exponents of four chunks from c on, the fg-th in the lanes of fg
+    auto load_e = [&](int c) __attribute__((always_inline)) {
+      const int at = (wk + WK * (c + fg)) * 4;
+      if ((epitch & 3) == 0) {
 #pragma unroll
-      for (int b = 0; b < RB; ++b)
+        for (int j = 0; j < NC; ++j)
+          er4[j] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(GATED && (j & 1) ? er2 : er, at < epitch ? eo[j] + at : kMmOut, 0, 0);
+      } else {
 #pragma unroll
-        for (int s = 0; s < 4; ++s) x[b][s] = load16(xr, in ? xo[b] + 16 * s : kMmOut, (uint32_t)at * (2 * kChunk));
+        for (int j = 0; j < NC; ++j) {
+          er4[j] = 0;
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            er4[j] |= (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(GATED && (j & 1) ? er2 : er,
+                                                                    at + q < epitch ? eo[j] + at + q : kMmOut, 0, 0) << (8 * q);
+        }
+      }
     };
-    auto multiply = [&](const u32x4_t (&cw)[NC], const uint32_t (&ce)[NC], const u32x4_t (&x)[RB][4]) __attribute__((always_inline)) {
+    u32x4_t x[RB][4], w[NC];
+    auto read = [&](const uint16_t* buf) __attribute__((always_inline)) {
+#pragma unroll
+      for (int j = 0; j < NC; ++j)
+        w[j] = *reinterpret_cast<const u32x4_t*>(buf + WK * XB + wave * WB + j * 512 + fr * 32 + ((fg ^ ((fr >> 2) & 3)) << 3));
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+#pragma unroll
+        for (int b = 0; b < RB; ++b)
+          x[b][s] = *reinterpret_cast<const u32x4_t*>(buf + wk * XB + (16 * b + fr) * kChunk + (((4 * s + fg) ^ fr) << 3));
+    };
+    auto multiply = [&](int q) __attribute__((always_inline)) {
 #pragma unroll
       for (int j = 0; j < NC; ++j) {
-        const float sc = exponent(ce[j]);
+        const u32x4_t k = turn(w[j]);
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
-          const u32x4_t f = widen8<F16>(cw[j][s], sc);
+          const u32x4_t f = widen8<F16>(k[s], exponent_of(ex[j][q], s));
 #pragma unroll
           for (int b = 0; b < RB; ++b) acc[j][b] = mm_mfma<F16>(f, x[b][s], acc[j][b]);
         }
       }
     };
-    u32x4_t xa[2][RB][4];
+#define FP4_WAIT(N) __builtin_amdgcn_s_waitcnt(((N) & 15) | (((N) >> 4) << 14) | 0x0F70)
+#define FP4_BUF(I) ((I) % NB == 0 ? s0 : (I) % NB == 1 ? s1 : (I) % NB == 2 ? s2 : s3)
+    load_e(0);
 #pragma unroll
-    for (int d = 0; d < D; ++d) load_w(w[d], e[d], d);
-    load_x(xa[0], 0);
-    static_assert(D % 2 == 0, "the rows' two buffers alternate with the codes'");
-    for (int c = 0; c < n; c += D) {
+    for (int i = 0; i < (WN == 1 ? NB : NB - 1); ++i) load(FP4_BUF(i), i);
+    for (int c = 0; c < n; c += G) {
 #pragma unroll
-      for (int d = 0; d < D; ++d) {
+      for (int j = 0; j < NC; ++j) ex[j] = turn(u32x4_t{er4[j], er4[j], er4[j], er4[j]});
+      load_e(c + G);
+#pragma unroll
+      for (int d = 0; d < G; ++d) {
         if (c + d >= n) break;
-        load_x(xa[(d + 1) & 1], c + d + 1);
-        multiply(w[d], e[d], xa[d & 1]);
-        load_w(w[d], e[d], c + d + D);
+        if constexpr (WN == 1) {
+          FP4_WAIT((NB - 1) * kLoads);
+          __builtin_amdgcn_sched_barrier(0);
+          read(FP4_BUF(d));
+          __builtin_amdgcn_s_waitcnt(0xC07F);
+          __builtin_amdgcn_sched_barrier(0);
+          load(FP4_BUF(d), c + d + NB);
+          multiply(d);
+        } else {
+          FP4_WAIT((NB - 2) * kLoads);
+          __builtin_amdgcn_s_waitcnt(0xC07F);
+          __builtin_amdgcn_s_barrier();
+          __builtin_amdgcn_sched_barrier(0);
+          load(FP4_BUF(d + NB - 1), c + d + NB - 1);
+          read(FP4_BUF(d));
+          multiply(d);
+        }
       }
     }
-    // partial sums [wave][16 RB rows][16 NC columns]; column c of row r at
-    // c ^ 4 (r & 3), for the banks
-    float* part = s_part[wave];
+    FP4_WAIT(0);                                  // loads past the last stage land
+    __syncthreads();
+    // partial sums [group][16 RB rows][columns of the block]; column c of row r
+    // at c ^ 4 (r & 3), for the banks
+    float* part = reinterpret_cast<float*>(s0) + wk * (RB * 16 * kCols);
 #pragma unroll
     for (int b = 0; b < RB; ++b)
 #pragma unroll
       for (int j = 0; j < NC; ++j)
-        *reinterpret_cast<f32x4_t*>(part + (16 * b + fr) * 16 * NC + 16 * j + 4 * (fg ^ (fr & 3))) = acc[j][b];
+        *reinterpret_cast<f32x4_t*>(part + (16 * b + fr) * kCols + 16 * (wn * NC + j) + 4 * (fg ^ (fr & 3))) = acc[j][b];
     __syncthreads();
-    for (int i = tid; i < RB * 16 * kOut; i += 64 * NW) {
-      const int row = i / kOut, c = i % kOut, col = t.col0 + c;
-      const int at = row * 16 * NC + (GATED ? 32 * (c >> 4) + ((c & 15) ^ (4 * (row & 3))) : c ^ (4 * (row & 3)));
-      float v = 0.f, u = 0.f;
+    // eight columns of a row to a thread
+    for (int i = tid; i < RB * 16 * (kOut / 8); i += 64 * NW) {
+      const int row = i / (kOut / 8), c = i % (kOut / 8), col = t.col0 + 8 * c, sw = 4 * (row & 3);
+      if (row >= t.nrows || col >= p.n) continue;
+      const int at = GATED ? 32 * (c >> 1) + 8 * (c & 1) : 8 * c;
+      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, u[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int q = 0; q < NW; ++q) {
-        v += s_part[q][at];
-        if constexpr (GATED) u += s_part[q][at + 16];
+      for (int q = 0; q < WK; ++q) {
+        const float* s = reinterpret_cast<const float*>(s0) + (q * RB * 16 + row) * kCols;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const f32x4_t f = *reinterpret_cast<const f32x4_t*>(s + ((at + 4 * h) ^ sw));
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[4 * h + k] += f[k];
+          if constexpr (GATED) {
+            const f32x4_t g = *reinterpret_cast<const f32x4_t*>(s + 16 + ((at + 4 * h) ^ sw));
+#pragma unroll
+            for (int k = 0; k < 4; ++k) u[4 * h + k] += g[k];
+          }
+        }
       }
-      if (row < t.nrows && col < p.n) {
-        if constexpr (GATED) gate1<F16>(p, v, u, (int64_t)t.g0 + t.row0 + row, col);
-        else finish1<F16>(p, v, (int64_t)t.g0 + t.row0 + row, col);
+      if constexpr (GATED) {
+        mm_gate8<F16>(p, v, u, (int64_t)t.g0 + t.row0 + row, col);
+      } else {
+        float bias[8];
+        mm_bias8<F16>(p, col, bias);
+        mm_finish8<F16, true>(p, v, bias, (int64_t)t.g0 + t.row0 + row, col, 0);
       }
     }
     __syncthreads();                              // the sums are read before they are written again
   }
+#undef FP4_WAIT
+#undef FP4_BUF
 }
 
-template <bool F16, int RB, int NC, int NW, int D, bool GATED>
+template <bool F16, int RB, int NC, int WN, int WK, int NB, bool GATED, bool XREG = false>
 hipError_t stream_go(const Fp4Args& a, hipStream_t st) {
   const MatmulArgs& p = a.mm;
   const long long groups = p.offsets != nullptr ? (p.E < p.rows ? p.E : p.rows) : 1;
-  const long long BM = 16 * RB, cols = ceil_div(p.n, GATED ? 8 * NC : 16 * NC);
+  const long long BM = 16 * RB, cols = ceil_div(p.n, (GATED ? 8 : 16) * NC * WN);
   long long grid = ((p.rows + BM - 1) / BM + (p.offsets != nullptr ? groups : 0)) * cols;
   grid = (grid + 7) / 8 * 8;
   if (grid > (1 << 20)) grid = 1 << 20;
-  hipLaunchKernelGGL((fp4_stream_kernel<F16, RB, NC, NW, D, GATED>), dim3((unsigned)grid), dim3(64 * NW), 0, st, a);
+  hipLaunchKernelGGL((fp4_stream_kernel<F16, RB, NC, WN, WK, NB, GATED, XREG>), dim3((unsigned)grid), dim3(64 * WN * WK), 0, st, a);
   return hipGetLastError();
 }
+int64_t mean_rows(const MatmulArgs& p) {
+  return p.offsets != nullptr ? ((int64_t)p.rows + p.E - 1) / p.E : p.rows;
+}
+
+// Groups go by their mean rows (128 experts of 2048 -> 768, 64 rows 12.5 us with
+// 16-row blocks; 4096 rows, gated, 76 us with 32-row blocks, 82 with 64; 6144 rows
+// 52 us with 64-row blocks, 55 with 32; 24576 rows 129 and 139).
+// Dense: up to sixteen rows take narrow blocks, with eight waves along the
+// contraction where that leaves fewer blocks than CUs (8 rows, 4096 x 4096 6.3 us
+// with 16 columns, 7.0 with 32; one row, 6144 -> 16384 17 and 12.3).  More rows
+// take the first of ever larger blocks of which the card holds all at once, and
+// else the largest without waves along the contraction (5120 x 5120: 96 rows 14.3
+// us with 32 x 64, 18.3 with 64 x 64; 128 rows 25.8 and 18.7, 256 rows 28.3 with 64 x
+// 128; 512 rows 42.7 with the last).
 template <bool F16, bool GATED>
 hipError_t stream_rows(const Fp4Args& a, hipStream_t st) {
   const MatmulArgs& p = a.mm;
-  const long long mean = p.offsets != nullptr ? (p.rows + p.E - 1) / p.E : p.rows;
-  if (mean <= 16) return stream_go<F16, 1, 2, 8, 2, GATED>(a, st);
-  if (mean <= 32) return stream_go<F16, 2, 4, 4, 2, GATED>(a, st);
-  return stream_go<F16, 4, 4, 4, 2, GATED>(a, st);
+  const int64_t rows = mean_rows(p), n = (int64_t)p.n * (GATED ? 2 : 1);
+  const bool x16 = (reinterpret_cast<uintptr_t>(p.a) & 15) == 0 && p.lda % 8 == 0;
+  if (!x16) {
+    if (rows <= 16) return stream_go<F16, 1, 2, 2, 2, 2, GATED, true>(a, st);
+    return stream_go<F16, 4, 2, 4, 2, 2, GATED, true>(a, st);
+  }
+  if (p.offsets != nullptr) {
+    if (rows <= 16) return stream_go<F16, 1, 2, 2, 2, 2, GATED>(a, st);
+    if (rows <= 40) return stream_go<F16, 2, 2, 4, 1, 2, GATED>(a, st);
+    return stream_go<F16, 4, 2, 4, 1, 3, GATED>(a, st);
+  }
+  if (rows <= 16) {
+    if (n >= 6144) return stream_go<F16, 1, 2, 1, 4, 2, GATED>(a, st);
+    if constexpr (GATED) return stream_go<F16, 1, 2, 1, 8, 2, GATED>(a, st);
+    else return stream_go<F16, 1, 1, 1, 8, 2, GATED>(a, st);
+  }
+  auto blocks = [&](int64_t bm, int64_t bn) { return (rows + bm - 1) / bm * ((n + bn - 1) / bn); };
+  if (blocks(32, 64) <= 256) return stream_go<F16, 2, 2, 2, 4, 2, GATED>(a, st);
+  if (blocks(64, 64) <= 256) return stream_go<F16, 4, 2, 2, 4, 2, GATED>(a, st);
+  if (blocks(64, 128) <= 256) return stream_go<F16, 4, 2, 4, 2, 2, GATED>(a, st);
+  return stream_go<F16, 4, 2, 4, 1, 3, GATED>(a, st);
 }
 
 // -------------------------------------------------------------- many rows
@@ -192,12 +337,11 @@ hipError_t launch_widen(bool f16, const uint8_t* codes, const uint8_t* exps, uin
   return hipGetLastError();
 }
 
-// Whether the weights are better widened first: a pass of 0.53 + 2 bytes and
-// the product's reading of 2 instead of 0.53.
-bool widens(const MatmulArgs& p) {
-  const long long mean = p.offsets != nullptr ? (p.rows + p.E - 1) / p.E : p.rows;
-  return mean > 64;
-}
+// Whether the weights are better widened first: a pass of 0.53 + 2 bytes a
+// weight against a product of 16-bit weights that is half as fast again
+// (5120 x 5120: 512 rows 42 us, widened 48, 1024 rows 71 and 70; 4096 -> 16384, 1024
+// rows 148 and 115; 32 experts of 4096 -> 1536, 512 rows each 258 and 297).
+bool widens(const MatmulArgs& p) { return mean_rows(p) > 640; }
 
 size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
 size_t matrix_bytes(const MatmulArgs& p) { return up256((size_t)p.E * p.n * p.k * 2); }
