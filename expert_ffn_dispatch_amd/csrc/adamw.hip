@@ -16,7 +16,15 @@
 // A block takes a chunk of one tensor; the list of tensors comes with the
 // launch's arguments (no copy to the device, nothing to keep for a graph).
 // Bound by memory: 30 bytes a value with fp32 masters, bf16 gradients and
-// copies and 32-bit states, 16 with states in 8.
+// copies and 32-bit states, 16 with states in 8.  302M values: 1417 us (6.4
+// TB/s) and 841 us (5.8 TB/s).  What the blocks under way read lies closer
+// together the smaller the blocks are: 1024 values to a block, us with states in
+// 32 and in 8 bits 1417 and 889, 2048 1474 and 889, 8192 1569 and 948, 32768 1663
+// and 998.  Stores, and with 32-bit states loads, carry the non-temporal hint
+// (1544 without it on loads); with 8-bit states the loads are better without
+// (889 -> 841).
+#include <type_traits>
+
 #include "common.h"
 #include "kernels.h"
 
@@ -31,9 +39,9 @@ template <> struct Raw<4> { typedef uint32_t type; };
 template <> struct Raw<8> { typedef uint32_t type __attribute__((ext_vector_type(2))); };
 template <> struct Raw<16> { typedef uint32_t type __attribute__((ext_vector_type(4))); };
 
-// V values of a type from memory (streamed: nothing is read twice), zeros
-// from the n-th on; and back.  At any alignment of the elements.
-template <int TYPE, int V>
+// V values of a type from memory, zeros from the n-th on; and back.  At any
+// alignment of the elements.  NT: loads with the non-temporal hint.
+template <int TYPE, int V, bool NT = true>
 struct Values {
   static constexpr int kSize = TYPE == kTypeF32 ? 4 : 2;
   static constexpr int kPiece = V * kSize < 16 ? V * kSize : 16, kPieces = V * kSize / kPiece;
@@ -44,7 +52,10 @@ struct Values {
     const char* a = static_cast<const char*>(p) + i * kSize;
     if (n >= V) {
 #pragma unroll
-      for (int k = 0; k < kPieces; ++k) raw[k] = __builtin_nontemporal_load(reinterpret_cast<const any_t*>(a + k * kPiece));
+      for (int k = 0; k < kPieces; ++k) {
+        const any_t* piece = reinterpret_cast<const any_t*>(a + k * kPiece);
+        raw[k] = NT ? __builtin_nontemporal_load(piece) : *piece;
+      }
     } else {
       uint32_t w[V * kSize / 4] = {};
 #pragma unroll
@@ -157,13 +168,13 @@ __device__ __forceinline__ uint32_t block_exponent(uint32_t top) {
   return top >= 0x7f800000u ? 255u : (uint32_t)max((int)((top + 0x1FFFFFu) >> 23) - 8, 1);
 }
 
-// E4M3 code of a magnitude of at most 448, rounded up where the part of a step
-// past the code below, in 1 / 65536, and `u` reach 65536.  Below 2^-6 the codes
-// have the spacing of the binade above it: 2^-6 is added and taken off.
-__device__ __forceinline__ uint32_t e4m3(float f, uint32_t u) {
-  const bool small = f < 0.015625f;
-  const uint32_t bits = __float_as_uint(small ? f + 0.015625f : f);
-  return min((bits + (u << 4)) >> 20, 960u + 126u) - (small ? 968u : 960u);
+// Byte K of `codes`: the E4M3 code of f, |f| <= 448, the neighbour further from
+// zero where the bits of f below the code's last, plus the upper bits of `seed`
+// at their place, carry into it (gfx950's conversion with such a rounding;
+// whole-number arithmetic took ten instructions more).
+template <int K>
+__device__ __forceinline__ uint32_t e4m3(uint32_t codes, float f, uint32_t seed) {
+  return (uint32_t)__builtin_amdgcn_cvt_sr_fp8_f32(f, seed, codes, K);
 }
 
 __device__ __forceinline__ void widen8(uint2 c, float (&f)[8]) {
@@ -182,7 +193,7 @@ __device__ __forceinline__ void widen8(uint2 c, float (&f)[8]) {
 __device__ __forceinline__ uint2 load_codes(const uint8_t* p, int n) {
   typedef uint32_t any_t __attribute__((ext_vector_type(2), aligned(1)));
   if (n >= 8) {
-    const auto v = __builtin_nontemporal_load(reinterpret_cast<const any_t*>(p));
+    const any_t v = *reinterpret_cast<const any_t*>(p);
     return uint2{v[0], v[1]};
   }
   uint2 c{0, 0};
@@ -205,8 +216,8 @@ __device__ __forceinline__ void store_codes(uint8_t* p, int n, uint2 c) {
 
 // -------------------------------------------------------------- the kernel
 
-constexpr int kThreads = 256;
-constexpr int kStep = 2048;                       // values of a block's turn; chunks are whole turns
+constexpr int kThreads = 128;
+constexpr int kStep = 1024;                       // values of a block's turn; chunks are whole turns
 
 template <int PT, int V>
 __device__ __forceinline__ void write_back(const AdamWTensor& t, int64_t i, int n, const float (&p)[V]) {
@@ -263,8 +274,8 @@ __device__ __forceinline__ void chunk8(const AdamWTensor& t, const Hyper& h, int
     const int64_t i = at + threadIdx.x * V;
     const int n = (int)max(min(end - i, (int64_t)V), (int64_t)0);
     const bool any = n > 0;                       // the block has values here: lane 0 of its sixteen does
-    Values<PT, V> p;
-    Values<GT, V> g;
+    Values<PT, V, false> p;
+    Values<GT, V, false> g;
     p.load(t.param, i, n);
     g.load(t.grad, i, n);
     const uint2 mw = load_codes(mc + i, n), vw = load_codes(vc + i, n);
@@ -275,17 +286,25 @@ __device__ __forceinline__ void chunk8(const AdamWTensor& t, const Hyper& h, int
     widen8(mw, m);
     widen8(vw, v);
     const float ms = __uint_as_float(me << 23), vs = __uint_as_float(ve << 23);
-    uint32_t mt = 0, vt = 0;
 #pragma unroll
     for (int q = 0; q < V; ++q) {
       m[q] *= ms;
       v[q] *= vs;
       v[q] *= v[q];
       step1(h, gf[q], pf[q], m[q], v[q], root[q]);
-      if (q < n) {                                // past the end all are zero but for a gradient scale that is no number
-        mt = max(mt, __float_as_uint(m[q]) & 0x7fffffffu);
-        vt = max(vt, __float_as_uint(v[q]) & 0x7fffffffu);
+    }
+    if (n < V) {                                  // zero past the end, also with a gradient scale that is no number
+#pragma unroll
+      for (int q = 0; q < V; ++q) {
+        m[q] = q < n ? m[q] : 0.f;
+        v[q] = q < n ? v[q] : 0.f;
       }
+    }
+    uint32_t mt = 0, vt = 0;
+#pragma unroll
+    for (int q = 0; q < V; ++q) {
+      mt = max(mt, __float_as_uint(m[q]) & 0x7fffffffu);
+      vt = max(vt, __float_as_uint(v[q]) & 0x7fffffffu);
     }
     mt = max16(mt);
     vt = max16(vt);
@@ -294,16 +313,23 @@ __device__ __forceinline__ void chunk8(const AdamWTensor& t, const Hyper& h, int
     const uint32_t mn = block_exponent(mt), vn = block_exponent(vt);
     const float mi = __uint_as_float((254u - mn) << 23), vi = __uint_as_float((254u - vn) << 23);
     uint2 mo{0, 0}, vo{0, 0};
-#pragma unroll
-    for (int q = 0; q < V; ++q) {
+    auto encode = [&](auto k, uint32_t& mw, uint32_t& vw, int q) __attribute__((always_inline)) {
+      constexpr int K = decltype(k)::value;
       const uint32_t z = draw((uint32_t)i + q, h.salt);
-      uint32_t c = e4m3(fabsf(m[q]) * mi, z & 0xffffu) | ((__float_as_uint(m[q]) >> 24) & 0x80u);
-      uint32_t d = e4m3(root[q] * vi, z >> 16);
-      if (d == 0 && v[q] > 0.f) d = 1;            // no divisor that was there is lost
-      if (mn == 255u) c = 0x7fu;
-      if (vn == 255u) d = 0x7fu;
-      (q < 4 ? mo.x : mo.y) |= c << (8 * (q & 3));
-      (q < 4 ? vo.x : vo.y) |= d << (8 * (q & 3));
+      mw = e4m3<K>(mw, m[q] * mi, z << 16);
+      // no divisor that was there is lost, and a root one bit too large stays a code
+      vw = e4m3<K>(vw, fminf(fmaxf(root[q] * vi, v[q] > 0.f ? 0x1p-9f : 0.f), 448.f), z & 0xffff0000u);
+    };
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      uint32_t& mw = w ? mo.y : mo.x;
+      uint32_t& vw = w ? vo.y : vo.x;
+      encode(std::integral_constant<int, 0>{}, mw, vw, 4 * w);
+      encode(std::integral_constant<int, 1>{}, mw, vw, 4 * w + 1);
+      encode(std::integral_constant<int, 2>{}, mw, vw, 4 * w + 2);
+      encode(std::integral_constant<int, 3>{}, mw, vw, 4 * w + 3);
+      if (mn == 255u) mw = 0x7f7f7f7fu;
+      if (vn == 255u) vw = 0x7f7f7f7fu;
     }
     if (!any) continue;
     write_back<PT>(t, i, n, pf);
@@ -348,8 +374,8 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamWArgs a) {
 hipError_t launch_adamw(AdamWArgs& a, hipStream_t st) {
   int64_t total = 0;
   for (int i = 0; i < a.count; ++i) total += a.tensor[i].numel;
-  // chunks of four turns, or of one where that would leave CUs idle
-  a.chunk = total >= (int64_t)kStep * 4 * 2048 ? kStep * 4 : kStep;
+  // chunks of one turn, or of as many as keep the grid at about 2^20 blocks
+  a.chunk = kStep * (int)(1 + (total >> 30));
   uint32_t chunks = 0;
   for (int i = 0; i < a.count; ++i) {
     a.tensor[i].first_chunk = chunks;

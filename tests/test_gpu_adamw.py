@@ -319,6 +319,24 @@ def test_a_tensor_split_or_whole_is_the_same():
         assert torch.equal(parts[k], t[k])
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_more_values_than_a_grid_of_one_turn_blocks(fp8):
+    """1.1e9 values: a block takes two turns.  The last values and some between are those of a short list of the same."""
+    n, k = (1 << 30) + 50_000_001, 4096
+    p, g = torch.zeros(n, dtype=BF, device=DEV), torch.zeros(n, dtype=BF, device=DEV)
+    m, v = (moe.Fp8Moment.zeros(p), moe.Fp8Moment.zeros(p)) if fp8 else (torch.zeros(n, device=DEV), torch.zeros(n, device=DEV))
+    rng = gen(3)
+    spots = [0, 1 << 20, (1 << 30) - 2048, (n - k) // 128 * 128]
+    values = [torch.randn(k, generator=rng, device=DEV).to(BF) for _ in spots]
+    for a, x in zip(spots, values):
+        g[a:a + k] = x
+    moe.moe_adamw(moe.AdamWTensors([p], [m], [v]), [g], step=1, lr=1e-2, weight_decay=0.0)
+    for a, x in zip(spots, values):
+        want, _, _, ep, _, _ = ref_step(torch.zeros_like(x), x, torch.zeros_like(x), torch.zeros_like(x), 1, 1e-2, 0.9, 0.999, 1e-8, 0.0)
+        check_param(p[a:a + k], want, ep, f"at {a}")
+    assert not p[spots[0] + k:spots[1]].any() and not p[spots[2] + k:spots[3]].any()
+
+
 def test_refusals():
     n = 256
     f = lambda dt=F32, k=n: torch.zeros(k, dtype=dt, device=DEV)  # noqa: E731
