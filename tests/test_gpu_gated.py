@@ -90,15 +90,20 @@ def test_backward(rows, n_in, width, act):
     assert only[0] is None and torch.equal(only[1], dwg) and torch.equal(only[2], dwu)
 
 
-@pytest.mark.parametrize("rows,n_in,width", [(4400, 1024, 2200), (2200, 512, 2000), (4001, 520, 2171), (900, 4096, 1536)])
-def test_rounds_with_a_cut_tail(rows, n_in, width):
-    """More tiles than the card has CUs, or fewer: the last round is cut along the contraction."""
+# rows, in, width, side of the tiles, tiles that are cut (all of them, or those behind whole rounds over the card)
+CUT_TAILS = [(300, 4096, 64, 128, 3), (4400, 4400, 2200, 256, 68), (4200, 2048, 2052, 256, 33), (2100, 4160, 2100, 128, 49)]
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+@pytest.mark.parametrize("rows,n_in,width", [c[:3] for c in CUT_TAILS] + [(4001, 520, 2171)])
+def test_whole_rounds_and_a_cut_tail(rows, n_in, width, act):
+    """The products are saved and joined partly in the tiles, partly where the slices are added."""
     g = gen(rows)
     x, dh = randn(g, rows, n_in), randn(g, rows, width)
     wg, wu = (randn(g, width, n_in, scale=n_in ** -0.5) for _ in range(2))
-    h, gate, up = moe.moe_gated_linear(x, wg, wu, want_pre=True)
-    check_forward(x, wg, wu, "silu", h, gate, up)
-    check_backward(dh, x, wg, wu, gate, up, "silu", *moe.moe_gated_linear_backward(dh, x, wg, wu, gate, up))
+    h, gate, up = moe.moe_gated_linear(x, wg, wu, act=act, want_pre=True)
+    check_forward(x, wg, wu, act, h, gate, up)
+    check_backward(dh, x, wg, wu, gate, up, act, *moe.moe_gated_linear_backward(dh, x, wg, wu, gate, up, act=act))
 
 
 def test_gradient_against_differences():
