@@ -889,7 +889,7 @@ moe::MatmulArgs gated_args(const moe_gated_dims& d, bool grouped, const void* x,
   a.k = d.in_features;
   a.act = d.act;
   a.f16 = d.dtype == MOE_DTYPE_F16;
-  a.whole = !grouped && d.rows <= 64 && d.in_features % 8 == 0 && d.ld_x % 8 == 0 && d.ld_w % 8 == 0;
+  a.whole = !grouped && d.rows <= moe::kMmGatedStreamRows && d.in_features % 8 == 0 && d.ld_x % 8 == 0 && d.ld_w % 8 == 0;
   return a;
 }
 moe::MatmulArgs gated_row_grad_args(const moe_gated_dims& d, const void* g, const void* w_gate, const void* w_up, void* dx) {

@@ -200,6 +200,7 @@ size_t matmul_workspace_bytes(MatmulForm f, const MatmulArgs& a);
 hipError_t launch_matmul(MatmulForm f, MatmulArgs a, void* ws, hipStream_t st);
 // Forward products of a few rows per group (matmul_stream.hip): whether a call
 // is one, and its launch.
+constexpr int kMmGatedStreamRows = 48;            // of dense gated products
 bool matmul_streams(const MatmulArgs& a);
 hipError_t launch_matmul_stream(const MatmulArgs& a, hipStream_t st);
 // The instances of one form (matmul_*.hip).

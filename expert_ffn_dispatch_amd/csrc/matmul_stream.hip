@@ -177,9 +177,12 @@ hipError_t stream_dense(const MatmulArgs& a, hipStream_t st) {
   if (a.n < 192 * 64) return stream_go<F16, RB, 2, 4, true>(a, st);
   return stream_go<F16, RB, 4, 4, true>(a, st);
 }
+// Gated: sixteen pairs of columns for up to sixteen rows (6144 -> 16384, one row
+// 74.6 us, 82.1 with 32), else 32 where they leave about 192 blocks (32 rows 84.8 with
+// sixteen, 78.9 so).
 template <bool F16, int RB>
 hipError_t stream_gated(const MatmulArgs& a, hipStream_t st) {
-  if (a.n < 192 * 32) return stream_go<F16, RB, 2, 4, true, true>(a, st);
+  if (RB == 1 || a.n < 192 * 32) return stream_go<F16, RB, 2, 4, true, true>(a, st);
   return stream_go<F16, RB, 4, 4, true, true>(a, st);
 }
 template <bool F16>
@@ -188,8 +191,7 @@ hipError_t stream_rows(const MatmulArgs& a, hipStream_t st) {
     if (a.offsets != nullptr) return stream_go<F16, 1, 2, 4, false, true>(a, st);
     if (a.rows <= 16) return stream_gated<F16, 1>(a, st);
     if (a.rows <= 32) return stream_gated<F16, 2>(a, st);
-    if (a.rows <= 48) return stream_gated<F16, 3>(a, st);
-    return stream_gated<F16, 4>(a, st);
+    return stream_gated<F16, 3>(a, st);
   }
   // groups of a row or two: 32 columns (64 rows over 128 experts of 2048 ->
   // 768 24.2 us, 31.9 with sixteen)
@@ -210,8 +212,13 @@ hipError_t stream_rows(const MatmulArgs& a, hipStream_t st) {
 // is that shape's: 64 experts of it cross a little earlier (32 rows 21.3 us
 // against 19.3), wider ones later (rows over 8 experts of 4096 -> 1536: 4 rows
 // 13.5 against 30.2, 8 rows 18.3 against the tiles' 31.3 that they take).
+// Gated: twice the weights to the rows, so up to twice as many rows as experts
+// (256 rows over 128 experts of 2048 -> 768 130 us against 137, 16 rows over 8 of
+// 4096 -> 1536 44 against 52), dense up to 48 (4096 -> 4096: 48 rows 20.9 us, 64 rows
+// 25.8 against 21.4).
 bool matmul_streams(const MatmulArgs& a) {
   if (!a.aligned) return false;
+  if (a.gated) return a.offsets != nullptr ? (long long)a.rows <= 2LL * a.E : a.rows <= kMmGatedStreamRows;
   return a.offsets != nullptr ? 2 * (long long)a.rows <= a.E : a.rows <= 64;
 }
 
