@@ -773,40 +773,42 @@ class AdamWTensors:
         self._table = (_lib.MoeAdamWTensor * max(1, self.count))()
         self._words = memoryview(self._table).cast("B").cast("Q")
         self._kept = []                         # every tensor's memory, whatever becomes of the caller's object
-        spans = []
+        device, spans = self.device, []
 
-        def place(i, field, t, n, dtypes, name):
-            if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != self.device:
-                raise ValueError(f"{name} {i}: expected a tensor on {self.device}")
+        def place(i, entry, field, t, n, dtypes):
+            if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != device:
+                raise ValueError(f"{field} {i}: expected a tensor on {device}")
             if t.dtype not in dtypes:
-                raise TypeError(f"{name} {i}: dtype {t.dtype} not in {tuple(dtypes)}")
+                raise TypeError(f"{field} {i}: dtype {t.dtype} not in {tuple(dtypes)}")
             if t.numel() != n or not t.is_contiguous():
-                raise ValueError(f"{name} {i}: expected {n} contiguous values, got shape {tuple(t.shape)}")
-            self._kept.append(t.detach())
-            setattr(self._table[i], field, t.data_ptr())
+                raise ValueError(f"{field} {i}: expected {n} contiguous values, got shape {tuple(t.shape)}")
+            at = t.data_ptr()
+            setattr(entry, field, at)
+            self._kept.append(t.untyped_storage())
             if n:
-                spans.append((t.data_ptr(), t.data_ptr() + n * t.element_size(), f"{name} {i}"))
+                spans.append((at, at + n * t.element_size(), field, i))
 
+        fp8, codes = self.fp8, (torch.float8_e4m3fn,)
         for i, (p, m, v, c) in enumerate(zip(params, exp_avg, exp_avg_sq, copies)):
-            n = self.numels[i]
-            place(i, "param", p, n, _DTYPES, "param")
+            n, e = self.numels[i], self._table[i]
+            place(i, e, "param", p, n, _DTYPES)
             for t, field in ((m, "exp_avg"), (v, "exp_avg_sq")):
-                if isinstance(t, Fp8Moment) != self.fp8:
+                if isinstance(t, Fp8Moment) != fp8:
                     raise TypeError(f"{field} {i}: 8-bit and 32-bit states in one list")
-                if self.fp8:
-                    place(i, field, t.codes, n, (torch.float8_e4m3fn,), field + " codes")
-                    place(i, field + "_exp", t.exps, -(-n // _lib.MOE_ADAMW_BLOCK), (torch.uint8,), field + " exponents")
+                if fp8:
+                    place(i, e, field, t.codes, n, codes)
+                    place(i, e, field + "_exp", t.exps, -(-n // _lib.MOE_ADAMW_BLOCK), (torch.uint8,))
                 else:
-                    place(i, field, t, n, (torch.float32,), field)
+                    place(i, e, field, t, n, (torch.float32,))
             if c is not None:
-                place(i, "copy", c, n, _HALVES, "copy")
-                self._table[i].copy_dtype = _DTYPES[c.dtype]
-            self._table[i].numel = n
-            self._table[i].param_dtype = _DTYPES[p.dtype]
+                place(i, e, "copy", c, n, _HALVES)
+                e.copy_dtype = _DTYPES[c.dtype]
+            e.numel = n
+            e.param_dtype = _DTYPES[p.dtype]
         spans.sort()
         for a, b in zip(spans, spans[1:]):
             if b[0] < a[1]:
-                raise ValueError(f"{a[2]} and {b[2]} overlap")
+                raise ValueError(f"{a[2]} {a[3]} and {b[2]} {b[3]} overlap")
         self._params = params
         self._at = [p.data_ptr() for p in params]
         self._devices = [p.get_device() for p in params]
