@@ -3,7 +3,8 @@
  * MI355X (gfx950): router -> softmax -> top-k -> dispatch / permutation ->
  * grouped SwiGLU expert GEMM (+ shared experts) -> combine / unpermutation.
  * The last section holds what stands around it in a block and in training:
- * layer norm, linear layers and products grouped by expert, with gradients.
+ * layer norm, linear layers, gated projections and products grouped by expert,
+ * with gradients, an AdamW step, and products with 4-bit weights.
  *
  * Sources.  The steps are those the page "MoE 少算 FLOPs，延迟反而涨了：慢在搬
  * token 的路上" (wink.run) lays out in its sections "dense 和 MoE 的差别" (the router
@@ -527,7 +528,8 @@ int moe_grouped_gated(const moe_gated_dims* dims, const void* x, const int32_t* 
 /*
  * Their gradients, from dh and the saved products:
  *   dgate = dh * up * act'(gate),  dup = dh * act(gate)
- * (rounded to dtype as operands of the products; relu's slope at 0 is 0),
+ * (rounded to dtype as operands of the products, so infinite past fp16's range
+ * with fp16 data; relu's slope at 0 is 0),
  *   dx = dgate w_gate + dup w_up,  dw_gate = dgate^T x,  dw_up = dup^T x.
  * dx [rows][in], dw_gate / dw_up [width][in] packed (grouped: [E][width][in],
  * zero for an expert without rows): outputs; dx or both of dw_gate and dw_up
