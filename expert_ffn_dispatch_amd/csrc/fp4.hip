@@ -11,7 +11,7 @@
 // bytes, a quarter of the cache's work that loads in the order of the matrix
 // instruction's operands cost (one lane to 16 bytes, each of another row: 64
 // cache accesses a load, which bounded it: 4096 rows over 128 experts' gated
-// projections of 2048 -> 768 158 us with both operands loaded that way, 76 so).
+// projections of 2048 -> 768 158 us with both operands loaded that way, 75 so).
 // A lane reads 16 bytes of codes of one weight row back, four lanes' 4 x 4
 // words are turned by two swaps of lane rows, and each word is a matrix
 // instruction's eight weights.  Exponents come four chunks at a time, spread
@@ -81,11 +81,11 @@ __global__ __launch_bounds__(64 * WN * WK, 2) void fp4_stream_kernel(Fp4Args a) 
   constexpr int XB = 16 * RB * kChunk, WB = NC * 512, STAGE = WK * XB + NW * WB;      // 16-bit words
   constexpr int PART = NW * RB * NC * 512;
   constexpr int G = NB == 3 ? 3 : 4;              // stages that share loaded exponents
+  static_assert(NB == 2 || NB == 3, "buffers");
   static_assert((!GATED || NC % 2 == 0) && AX * WN == 4 * RB, "whole pairs and loads");
   __shared__ __align__(16) uint16_t s0[STAGE > PART ? STAGE : PART];
   __shared__ __align__(16) uint16_t s1[STAGE];
   __shared__ __align__(16) uint16_t s2[NB > 2 ? STAGE : 8];
-  __shared__ __align__(16) uint16_t s3[NB > 3 ? STAGE : 8];
   const MatmulArgs& p = a.mm;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wk = wave / WN, wn = wave % WN;
@@ -191,7 +191,7 @@ __global__ __launch_bounds__(64 * WN * WK, 2) void fp4_stream_kernel(Fp4Args a) 
       }
     };
 #define FP4_WAIT(N) __builtin_amdgcn_s_waitcnt(((N) & 15) | (((N) >> 4) << 14) | 0x0F70)
-#define FP4_BUF(I) ((I) % NB == 0 ? s0 : (I) % NB == 1 ? s1 : (I) % NB == 2 ? s2 : s3)
+#define FP4_BUF(I) ((I) % NB == 0 ? s0 : (I) % NB == 1 ? s1 : s2)
     load_e(0);
 #pragma unroll
     for (int i = 0; i < (WN == 1 ? NB : NB - 1); ++i) load(FP4_BUF(i), i);

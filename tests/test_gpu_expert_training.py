@@ -94,6 +94,28 @@ def test_three_steps(N, M, E_, k, H, fp8):
             assert torch.equal(w, p.to(BF)), "the working copy is the master, rounded"
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_two_layers_side_by_side(fp8):
+    """Two layers trained on two streams at once: each as alone."""
+    def train(layer, x, dout):
+        for step in (1, 2, 3):
+            layer.forward(x)
+            moe.moe_adamw(layer.plan, layer.backward(dout)[1], step=step, lr=1e-2)
+        return layer.master
+
+    data = [(randn(gen(k), 96, 256), randn(gen(50 + k), 96, 256)) for k in range(2)]
+    want = [train(Layer(gen(9 + k), 96, 256, 8, 2, 128, fp8), *data[k]) for k in range(2)]
+    layers, streams = [Layer(gen(9 + k), 96, 256, 8, 2, 128, fp8) for k in range(2)], [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for k in range(2):
+        with torch.cuda.stream(streams[k]):
+            train(layers[k], *data[k])
+    torch.cuda.synchronize()
+    for layer, ref in zip(layers, want):
+        for a, b in zip(layer.master, ref):
+            assert torch.equal(a, b)
+
+
 def test_trained_experts_in_4_bits():
     """A step of training, the working weights quantised, and the layer served from the codes: the same as with the codes'
     values in 16 bits, but for the order of fp32 sums (a rounding step of h and of y)."""

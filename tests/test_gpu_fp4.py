@@ -201,6 +201,20 @@ def test_offsets_are_clamped_empty_and_not_a_number():
         assert torch.equal(torch.isnan(y[7]), col == 0) and torch.equal(torch.sign(y[7][col != 0]).double(), torch.sign(col[col != 0]))
 
 
+def test_rows_past_32_bits():
+    """Rows of x behind 4 GiB of a strided matrix, by expert, and the same rows packed."""
+    g = gen(10)
+    big = torch.zeros(2200, 1 << 20, dtype=BF, device=DEV)
+    x, off = big[:, :96], offsets_of([275] * 8)
+    x.copy_(randn(g, 2200, 96))
+    w, w2 = weights(g, 8, 40, 96), weights(g, 8, 40, 96)
+    packed = x.contiguous()
+    assert torch.equal(moe.moe_grouped_matmul_fp4(x, off, w), moe.moe_grouped_matmul_fp4(packed, off, w))
+    assert torch.equal(moe.moe_grouped_gated_fp4(x, off, w, w2), moe.moe_grouped_gated_fp4(packed, off, w, w2))
+    one = moe.Fp4Weights(w.codes[0], w.exps[0])
+    assert torch.equal(moe.moe_linear_fp4(x, one), moe.moe_linear_fp4(packed, one))
+
+
 def _calls(g):
     x, off = randn(g, 150, 256), offsets_of([40, 0, 60, 50])
     one, few, foff = x[:1].contiguous(), x[:8].contiguous(), offsets_of([3, 0, 1, 4])
