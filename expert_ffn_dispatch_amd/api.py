@@ -932,12 +932,13 @@ def _fp4(w, name, device, n_in, lead=None):
     if not isinstance(w, Fp4Weights):
         raise TypeError(f"{name}: expected Fp4Weights, got {type(w).__name__}")
     codes, exps = w
-    lead = tuple(codes.shape[:-1]) if lead is None else lead
+    lead = codes.shape[:-1] if lead is None else lead
     for t, what, per in ((codes, "codes", 2), (exps, "exponents", 32)):
         if t.device != device or t.dtype != torch.uint8:
             raise ValueError(f"{name}: {what} must be torch.uint8 on {device}, got {t.dtype} on {t.device}")
-        if n_in % 32 or tuple(t.shape) != (*lead, n_in // per) or not t.is_contiguous():
-            raise ValueError(f"{name}: {what} of shape {tuple(t.shape)}, expected a contiguous "
+        s = t.shape
+        if n_in % 32 or len(s) < 2 or s[:-1] != lead or s[-1] != n_in // per or not t.is_contiguous():
+            raise ValueError(f"{name}: {what} of shape {tuple(s)}, expected a contiguous "
                              f"{(*lead, f'{n_in} / {per}')} with a multiple of 32 inputs")
     return _lib.MoeFp4Matrix(codes.data_ptr(), exps.data_ptr())
 
@@ -998,7 +999,7 @@ def _gated_fp4(x, w_gate, w_up, offsets, act, h, stream):
     px, ldx = _mat(x, "x", dev, _HALVES)
     code = _act(act)
     g = _fp4(w_gate, "w_gate", dev, n_in)
-    shape = tuple(w_gate.codes.shape[:-1])
+    shape = w_gate.codes.shape[:-1]
     if len(shape) != (1 if offsets is None else 2):
         raise ValueError(f"w_gate: codes of shape {tuple(w_gate.codes.shape)}")
     u = _fp4(w_up, "w_up", dev, n_in, shape)

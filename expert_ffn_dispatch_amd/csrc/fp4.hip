@@ -17,8 +17,8 @@
 // instruction's eight weights.  Exponents come four chunks at a time, spread
 // over the same four lanes.  Waves that share rows of x (WN > 1) meet at a
 // barrier a chunk; with WN = 1 no wave waits for another.
-// Bound by the weights' 17/32 byte for few rows (6144 -> 16384, one row: 12.4
-// us, 4.3 TB/s with the launch), by the conversions and the matrix pipe for
+// Bound by the weights' 17/32 byte for few rows (6144 -> 16384, one row: 12
+// us, 4.4 TB/s with the launch), by the conversions and the matrix pipe for
 // many (16384 rows over 32 experts of 4096 -> 1536: 258 us, 0.8 PFLOP/s).
 #include "matmul.h"
 
@@ -70,19 +70,23 @@ __device__ __forceinline__ u32x4_t turn(u32x4_t v) {
 // NB, are on their way while one is multiplied.  GATED: columns are pairs,
 // sixteen of W_gate and their sixteen of W_up.  XREG: rows of x of any
 // alignment, which pass through registers (they wait for every load under way).
+// BM: rows of a tile, 16 RB or, for few, four: the matrix instruction's other
+// twelve repeat them and are dropped, and x is a quarter of the loads and LDS
+// reads (128 experts of 2048 -> 768, 64 rows, gated 22.9 -> 18.9 us).
 // (Registers stay below 256, without copies to the other half of the file.)
-template <bool F16, int RB, int NC, int WN, int WK, int NB, bool GATED, bool XREG>
+template <bool F16, int RB, int NC, int WN, int WK, int NB, bool GATED, bool XREG, int BM>
 __global__ __launch_bounds__(64 * WN * WK, 2) void fp4_stream_kernel(Fp4Args a) {
   constexpr int NW = WN * WK;
   constexpr int kCols = 16 * NC * WN;             // columns of a block, pairs counted twice
   constexpr int kOut = GATED ? kCols / 2 : kCols;
-  constexpr int AX = 4 * RB / WN;                 // loads of x of a wave and stage
+  constexpr bool FOUR = BM == 4;                  // every wave of a group makes the one load of x, of the same bytes
+  constexpr int AX = FOUR ? 1 : 4 * RB / WN;      // loads of x of a wave and stage
   constexpr int kLoads = NC + (XREG ? 0 : AX);    // of these and of codes that a later stage may leave under way
-  constexpr int XB = 16 * RB * kChunk, WB = NC * 512, STAGE = WK * XB + NW * WB;      // 16-bit words
+  constexpr int XB = BM * kChunk, WB = NC * 512, STAGE = WK * XB + NW * WB;      // 16-bit words
   constexpr int PART = NW * RB * NC * 512;
   constexpr int G = NB == 3 ? 3 : 4;              // stages that share loaded exponents
   static_assert(NB == 2 || NB == 3, "buffers");
-  static_assert((!GATED || NC % 2 == 0) && AX * WN == 4 * RB, "whole pairs and loads");
+  static_assert((!GATED || NC % 2 == 0) && (FOUR ? RB == 1 && !XREG : BM == 16 * RB && AX * WN == 4 * RB), "whole pairs and loads");
   __shared__ __align__(16) uint16_t s0[STAGE > PART ? STAGE : PART];
   __shared__ __align__(16) uint16_t s1[STAGE];
   __shared__ __align__(16) uint16_t s2[NB > 2 ? STAGE : 8];
@@ -92,7 +96,7 @@ __global__ __launch_bounds__(64 * WN * WK, 2) void fp4_stream_kernel(Fp4Args a) 
   const int fr = lane & 15, fg = lane >> 4;
   const int cpitch = p.k / 2, epitch = p.k / 32;
   MmTile t;
-  for (int step = 0; mm_find_tile<false, 16 * RB, kOut>(p, lane, step, t); ++step) {
+  for (int step = 0; mm_find_tile<false, BM, kOut>(p, lane, step, t); ++step) {
     mm_scalar(t);
     const int chunks = ceil_div(p.k, kChunk), n = ceil_div(chunks, WK);
     const int64_t row = (int64_t)t.e * p.n + t.col0;
@@ -101,6 +105,7 @@ __global__ __launch_bounds__(64 * WN * WK, 2) void fp4_stream_kernel(Fp4Args a) 
     const uint16_t* x0 = p.a + (int64_t)(t.g0 + t.row0) * p.lda;
     const __amdgpu_buffer_rsrc_t er = mm_rsrc(a.exps[0] + row * epitch);
     const __amdgpu_buffer_rsrc_t er2 = GATED ? mm_rsrc(a.exps[1] + row * epitch) : er;
+    const int x_first = FOUR ? 0 : 4 * wn * AX;     // this wave's rows of x
     uint32_t co[NC], eo[NC], xo[AX];
     const int wpiece = (lane & 3) ^ ((lane >> 4) & 3);
 #pragma unroll
@@ -111,7 +116,7 @@ __global__ __launch_bounds__(64 * WN * WK, 2) void fp4_stream_kernel(Fp4Args a) 
     }
 #pragma unroll
     for (int i = 0; i < AX; ++i) {
-      const int r = 4 * (wn * AX + i) + fg;
+      const int r = x_first + 4 * i + fg;
       xo[i] = r < t.nrows ? (uint32_t)r * (uint32_t)(2 * p.lda) + (uint32_t)((fr ^ (r & 15)) * 16) : kMmOut;
     }
     f32x4_t acc[NC][RB];
@@ -130,7 +135,7 @@ __global__ __launch_bounds__(64 * WN * WK, 2) void fp4_stream_kernel(Fp4Args a) 
       const int size = k0 < p.k ? (int)kMmBytes : 0;
       const __amdgpu_buffer_rsrc_t rw = rsrc(w0, size), rw2 = GATED ? rsrc(w1, size) : rw, rx = rsrc(x0, size);
       uint16_t* bw = buf + WK * XB + wave * WB;
-      uint16_t* bx = buf + wk * XB + wn * AX * 512;
+      uint16_t* bx = buf + wk * XB + x_first * kChunk;
       if (k0 + kChunk <= p.k || size == 0) {
 #pragma unroll
         for (int j = 0; j < NC; ++j) mm_dma16(GATED && (j & 1) ? rw2 : rw, co[j], (uint32_t)k0 / 2, bw + j * 512);
@@ -142,7 +147,7 @@ __global__ __launch_bounds__(64 * WN * WK, 2) void fp4_stream_kernel(Fp4Args a) 
           mm_dma16(GATED && (j & 1) ? rw2 : rw, k0 + wpiece * 32 < p.k ? co[j] : kMmOut, (uint32_t)k0 / 2, bw + j * 512);
 #pragma unroll
         for (int i = 0; i < AX; ++i) {
-          const int xk = (fr ^ ((4 * (wn * AX + i) + fg) & 15)) * 8;
+          const int xk = (fr ^ ((x_first + 4 * i + fg) & 15)) * 8;
           put_x(rx, k0 + xk < p.k ? xo[i] : kMmOut, (uint32_t)k0 * 2, bx + i * 512);
         }
       }
@@ -167,6 +172,7 @@ __global__ __launch_bounds__(64 * WN * WK, 2) void fp4_stream_kernel(Fp4Args a) 
         }
       }
     };
+    const int xr = FOUR ? fr & 3 : fr;
     u32x4_t x[RB][4], w[NC];
     auto read = [&](const uint16_t* buf) __attribute__((always_inline)) {
 #pragma unroll
@@ -176,7 +182,7 @@ __global__ __launch_bounds__(64 * WN * WK, 2) void fp4_stream_kernel(Fp4Args a) 
       for (int s = 0; s < 4; ++s)
 #pragma unroll
         for (int b = 0; b < RB; ++b)
-          x[b][s] = *reinterpret_cast<const u32x4_t*>(buf + wk * XB + (16 * b + fr) * kChunk + (((4 * s + fg) ^ fr) << 3));
+          x[b][s] = *reinterpret_cast<const u32x4_t*>(buf + wk * XB + (16 * b + xr) * kChunk + (((4 * s + fg) ^ xr) << 3));
     };
     auto multiply = [&](int q) __attribute__((always_inline)) {
 #pragma unroll
@@ -233,7 +239,7 @@ __global__ __launch_bounds__(64 * WN * WK, 2) void fp4_stream_kernel(Fp4Args a) 
         *reinterpret_cast<f32x4_t*>(part + (16 * b + fr) * kCols + 16 * (wn * NC + j) + 4 * (fg ^ (fr & 3))) = acc[j][b];
     __syncthreads();
     // eight columns of a row to a thread
-    for (int i = tid; i < RB * 16 * (kOut / 8); i += 64 * NW) {
+    for (int i = tid; i < BM * (kOut / 8); i += 64 * NW) {
       const int row = i / (kOut / 8), c = i % (kOut / 8), col = t.col0 + 8 * c, sw = 4 * (row & 3);
       if (row >= t.nrows || col >= p.n) continue;
       const int at = GATED ? 32 * (c >> 1) + 8 * (c & 1) : 8 * c;
@@ -267,22 +273,22 @@ __global__ __launch_bounds__(64 * WN * WK, 2) void fp4_stream_kernel(Fp4Args a) 
 #undef FP4_BUF
 }
 
-template <bool F16, int RB, int NC, int WN, int WK, int NB, bool GATED, bool XREG = false>
+template <bool F16, int RB, int NC, int WN, int WK, int NB, bool GATED, bool XREG = false, int BM = 16 * RB>
 hipError_t stream_go(const Fp4Args& a, hipStream_t st) {
   const MatmulArgs& p = a.mm;
   const long long groups = p.offsets != nullptr ? (p.E < p.rows ? p.E : p.rows) : 1;
-  const long long BM = 16 * RB, cols = ceil_div(p.n, (GATED ? 8 : 16) * NC * WN);
-  long long grid = ((p.rows + BM - 1) / BM + (p.offsets != nullptr ? groups : 0)) * cols;
+  const long long cols = ceil_div(p.n, (GATED ? 8 : 16) * NC * WN);
+  long long grid = (((long long)p.rows + BM - 1) / BM + (p.offsets != nullptr ? groups : 0)) * cols;
   grid = (grid + 7) / 8 * 8;
   if (grid > (1 << 20)) grid = 1 << 20;
-  hipLaunchKernelGGL((fp4_stream_kernel<F16, RB, NC, WN, WK, NB, GATED, XREG>), dim3((unsigned)grid), dim3(64 * WN * WK), 0, st, a);
+  hipLaunchKernelGGL((fp4_stream_kernel<F16, RB, NC, WN, WK, NB, GATED, XREG, BM>), dim3((unsigned)grid), dim3(64 * WN * WK), 0, st, a);
   return hipGetLastError();
 }
 int64_t mean_rows(const MatmulArgs& p) {
   return p.offsets != nullptr ? ((int64_t)p.rows + p.E - 1) / p.E : p.rows;
 }
 
-// Groups go by their mean rows (128 experts of 2048 -> 768, 64 rows 12.5 us with
+// Groups go by their mean rows (128 experts of 2048 -> 768, 64 rows 12.2 us with
 // 16-row blocks; 4096 rows, gated, 76 us with 32-row blocks, 82 with 64; 6144 rows
 // 52 us with 64-row blocks, 55 with 32; 24576 rows 129 and 139).
 // Dense: up to sixteen rows take narrow blocks, with eight waves along the
@@ -302,9 +308,15 @@ hipError_t stream_rows(const Fp4Args& a, hipStream_t st) {
     return stream_go<F16, 4, 2, 4, 2, 2, GATED, true>(a, st);
   }
   if (p.offsets != nullptr) {
+    if (rows <= 2) return stream_go<F16, 1, 2, 2, 2, 2, GATED, false, 4>(a, st);
     if (rows <= 16) return stream_go<F16, 1, 2, 2, 2, 2, GATED>(a, st);
     if (rows <= 40) return stream_go<F16, 2, 2, 4, 1, 2, GATED>(a, st);
     return stream_go<F16, 4, 2, 4, 1, 3, GATED>(a, st);
+  }
+  if (rows <= 4) {
+    if (n >= 6144) return stream_go<F16, 1, 2, 1, 4, 2, GATED, false, 4>(a, st);
+    if constexpr (GATED) return stream_go<F16, 1, 2, 1, 8, 2, GATED, false, 4>(a, st);
+    else return stream_go<F16, 1, 1, 1, 8, 2, GATED, false, 4>(a, st);
   }
   if (rows <= 16) {
     if (n >= 6144) return stream_go<F16, 1, 2, 1, 4, 2, GATED>(a, st);

@@ -123,7 +123,22 @@ def test_gated_linear(rows, n_in, width, act):
 GROUPS = [([5], 64, 64), ([1], 32, 1), ([0], 64, 24), ([0, 0, 3, 0], 96, 136), ([1] * 7, 128, 256), ([130, 0, 1, 33, 257], 192, 264),
           ([31, 32, 33, 0, 64, 65, 127, 128, 129], 256, 128), ([3, 9, 0, 2], 64, 131), ([700, 0, 2, 600], 512, 320),
           ([2] * 256, 64, 72), ([0] * 100 + [50] + [0] * 59, 128, 128), ([20] * 16, 1024, 768), ([17, 0, 40, 3, 11], 2048, 200),
-          ([60, 90, 0, 10], 288, 96)]
+          ([60, 90, 0, 10], 288, 96), ([9, 0, 1, 4, 5] + [0] * 9 + [3, 2], 2080, 200), ([1, 0, 3, 0], 4096, 776)]
+
+
+@pytest.mark.parametrize("n_in,n_out", [(2080, 6160), (96, 6144), (4096, 200), (32, 24)])
+@pytest.mark.parametrize("rows", [1, 2, 3, 4, 5])
+def test_few_rows(rows, n_in, n_out):
+    """Tiles of four rows and of sixteen; the row behind the last stays as it was."""
+    g = gen(rows * n_in + n_out)
+    x, w, w2 = randn(g, rows, n_in), weights(g, n_out, n_in), weights(g, n_out, n_in)
+    y, h = (torch.full((rows + 1, n_out), 7.0, dtype=BF, device=DEV) for _ in range(2))
+    moe.moe_linear_fp4(x, w, y=y[:rows])
+    moe.moe_gated_linear_fp4(x, w, w2, h=h[:rows])
+    ref = x.double() @ values(w).T
+    check(y[:rows], ref, u(BF) * ref.abs() + product_error(x, values(w)) + tiny(BF), "y")
+    check_forward(x, values(w), values(w2), "silu", h[:rows], None, None)
+    assert (y[rows] == 7).all() and (h[rows] == 7).all()
 
 
 @pytest.mark.parametrize("dtype", [BF, HF])
