@@ -916,12 +916,22 @@ struct GatedBackwardWs {
   uint16_t* g;               // [rows][2 half]: dgate | dup
   void* products;            // workspace of either product, one after the other
 };
-GatedBackwardWs carve_gated_backward(Carver& c, const moe_gated_dims& d, const int32_t* offsets) {
+// Also turns both products' arguments to the padded copies in the workspace
+// and lists these: the weights' first, then x's.
+GatedBackwardWs carve_gated_backward(Carver& c, const moe_gated_dims& d, moe::MatmulArgs& r, moe::MatmulArgs& g,
+                                     moe::PackJob* jobs, int& w_jobs, int& x_jobs) {
   GatedBackwardWs w;
   w.g = c.take<uint16_t>((size_t)d.rows * 2 * gated_half(d));
-  moe::MatmulArgs r = gated_row_grad_args(d, nullptr, nullptr, nullptr, nullptr);
-  moe::MatmulArgs g = gated_weight_grad_args(d, nullptr, nullptr, nullptr, nullptr);
-  r.offsets = g.offsets = offsets;
+  r.a = g.a = w.g;
+  auto take = [&](moe::MatmulForm f, moe::MatmulArgs& p, moe::PackJob* to, int& n) {
+    moe::MatmulArgs sized = p;
+    n = 0;
+    char* at = c.take<char>(moe::matmul_pack_jobs(f, sized, nullptr, to, n));
+    n = 0;
+    moe::matmul_pack_jobs(f, p, at, to, n);
+  };
+  take(moe::kMmRowGrad, r, jobs, w_jobs);
+  take(moe::kMmWeightGrad, g, jobs + w_jobs, x_jobs);
   const size_t a = moe::matmul_workspace_bytes(moe::kMmRowGrad, r), b = moe::matmul_workspace_bytes(moe::kMmWeightGrad, g);
   w.products = c.take<char>(a > b ? a : b);
   return w;
@@ -969,7 +979,12 @@ int gated_backward_ws(const char* fn, const moe_gated_dims* dims, bool grouped, 
   if (int r = check_gated(fn, d, grouped)) return r;
   if (bytes == nullptr) return fail(MOE_ERR_INVALID, "%s: bytes is NULL", fn);
   Carver c(nullptr);
-  carve_gated_backward(c, d, grouped ? &kSomeOffsets : nullptr);
+  moe::MatmulArgs r = gated_row_grad_args(d, nullptr, nullptr, nullptr, nullptr);
+  moe::MatmulArgs g = gated_weight_grad_args(d, nullptr, nullptr, nullptr, nullptr);
+  r.offsets = g.offsets = grouped ? &kSomeOffsets : nullptr;
+  moe::PackJob jobs[3];
+  int w_jobs, x_jobs;
+  carve_gated_backward(c, d, r, g, jobs, w_jobs, x_jobs);
   *bytes = c.off;
   return ok();
 }
@@ -1006,7 +1021,12 @@ int run_gated_backward(const char* fn, const moe_gated_dims* dims, bool grouped,
     return fail(MOE_ERR_INVALID, "%s: two outputs are one", fn);
   if (int r = check_ws(fn, ws, ws_bytes, need)) return r;
   Carver c(ws);
-  const GatedBackwardWs b = carve_gated_backward(c, d, expert_offsets);
+  moe::MatmulArgs row_grad = gated_row_grad_args(d, nullptr, w_gate, w_up, dx);
+  moe::MatmulArgs weight_grad = gated_weight_grad_args(d, nullptr, x, dw_gate, dw_up);
+  row_grad.offsets = weight_grad.offsets = expert_offsets;
+  moe::PackJob jobs[3];
+  int w_jobs, x_jobs;
+  const GatedBackwardWs b = carve_gated_backward(c, d, row_grad, weight_grad, jobs, w_jobs, x_jobs);
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (d.rows > 0) {
     moe::GatedGradArgs g{};
@@ -1023,18 +1043,14 @@ int run_gated_backward(const char* fn, const moe_gated_dims* dims, bool grouped,
     g.half = gated_half(d);
     g.act = d.act;
     g.f16 = d.dtype == MOE_DTYPE_F16;
+    for (int i = 0; i < w_jobs + x_jobs; ++i)
+      if (i < w_jobs ? dx != nullptr : dw_gate != nullptr) g.jobs[g.n_jobs++] = jobs[i];
     if (hipError_t e = moe::launch_gated_grad(g, st)) return device_error(fn, e);
   }
-  if (dx != nullptr) {
-    moe::MatmulArgs a = gated_row_grad_args(d, b.g, w_gate, w_up, dx);
-    a.offsets = expert_offsets;
-    if (hipError_t e = moe::launch_matmul(moe::kMmRowGrad, a, b.products, st)) return device_error(fn, e);
-  }
-  if (dw_gate != nullptr) {
-    moe::MatmulArgs a = gated_weight_grad_args(d, b.g, x, dw_gate, dw_up);
-    a.offsets = expert_offsets;
-    if (hipError_t e = moe::launch_matmul(moe::kMmWeightGrad, a, b.products, st)) return device_error(fn, e);
-  }
+  if (dx != nullptr)
+    if (hipError_t e = moe::launch_matmul(moe::kMmRowGrad, row_grad, b.products, st)) return device_error(fn, e);
+  if (dw_gate != nullptr)
+    if (hipError_t e = moe::launch_matmul(moe::kMmWeightGrad, weight_grad, b.products, st)) return device_error(fn, e);
   return ok();
 }
 

@@ -184,6 +184,7 @@ struct MatmulArgs {
   int64_t a_half;            // weight grad: elements from dgate's columns to dup's
   int b2_half;               // weight grad: E counts both gradients of every group of rows
   int a_padded;              // a's last piece of a row may be read whole and is zero past the width
+  int b_padded;              // so are b's, and b2's
   int f16;                   // operands are fp16 (else bf16)
   int whole;                 // no contraction slices (no workspace for them)
   // set by launch_matmul: the plan
@@ -198,6 +199,17 @@ enum MatmulForm { kMmForward = 0, kMmRowGrad = 1, kMmWeightGrad = 2 };
 // would not take 16-byte loads.  Of `a` it reads sizes, strides and flags only.
 size_t matmul_workspace_bytes(MatmulForm f, const MatmulArgs& a);
 hipError_t launch_matmul(MatmulForm f, MatmulArgs a, void* ws, hipStream_t st);
+// A copy with padded rows: out[r] = in[r], widened to `pitch` with zeros.
+struct PackJob {
+  const uint16_t* in;
+  uint16_t* out;             // [rows][pitch], 16-byte aligned
+  int64_t ld, rows;
+  int width, pitch;
+};
+// The copies of b and b2 that launch_matmul would make, for a launch of the
+// caller's: appended to `jobs`, their places from `to` on (null: sizes only),
+// and `a` turned to them.  Returns their bytes.
+size_t matmul_pack_jobs(MatmulForm f, MatmulArgs& a, void* to, PackJob* jobs, int& n);
 // Forward products of a few rows per group (matmul_stream.hip): whether a call
 // is one, and its launch.
 constexpr int kMmGatedStreamRows = 48;            // of dense gated products
@@ -251,6 +263,8 @@ struct GatedGradArgs {
   int E, rows, n;
   int half;                  // dup's first column: n to the next multiple of 64
   int act, f16;
+  int n_jobs;                // copies made in the same launch
+  PackJob jobs[3];
 };
 hipError_t launch_gated_grad(const GatedGradArgs& a, hipStream_t st);
 

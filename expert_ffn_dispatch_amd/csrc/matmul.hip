@@ -1,6 +1,8 @@
 // What the three forms share: the choice of contraction slices, the sum of
 // their partial results, and the gradients of the activation (with the bias
 // gradient) and of the gated projections' activation and product.
+#include <algorithm>
+
 #include "matmul.h"
 
 namespace moe {
@@ -277,15 +279,35 @@ __global__ __launch_bounds__(1024) void dbias_join_kernel(ActGradArgs p, const f
   }
 }
 
+// Rows first to end of a copy, over the blocks in x; a thread moves eight columns.
+__device__ __forceinline__ void pack_rows(const PackJob& j, int64_t first, int64_t end) {
+  const int chunks = j.pitch / 8;
+  for (int64_t i = first * chunks + (int64_t)blockIdx.x * 256 + threadIdx.x; i < end * chunks;
+       i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / chunks;
+    const int c = (int)(i - r * chunks) * 8;
+    *reinterpret_cast<u32x4_t*>(j.out + r * j.pitch + c) = load8(j.in + r * j.ld + c, j.width - c);
+  }
+}
+int64_t pack_blocks(const PackJob& j) { return (j.rows * (j.pitch / 8) + 255) / 256; }
+
 // dgate = dh up act'(gate) and dup = dh act(gate), rounded to the operands' 16
 // bits (as g above), side by side: g [rows][2 half], dup from column `half`
 // on (whole stages of the contraction), zeros past n.  A thread takes eight
 // columns of a row.  Bound by its five passes over rows x n.
+// The products' padded copies (x's rows are the groups', weights are copied
+// without groups only) are further rows of the grid: each is too short for a
+// launch of its own (777 x 1111 x 2222, fp16: the backward pass 71.3 us
+// with two launches for them, 62.6 so).
 template <bool F16>
 __global__ __launch_bounds__(256) void gated_grad_kernel(GatedGradArgs p) {
   const uint32_t chunks = (uint32_t)p.half / 8;
   int64_t first = 0, end = p.rows;
   if (p.offsets != nullptr) group_rows(p.offsets, p.E, p.rows, first, end);
+  if (blockIdx.y > 0) {
+    const PackJob j = p.jobs[blockIdx.y - 1];
+    return pack_rows(j, p.offsets != nullptr ? first : 0, p.offsets != nullptr ? end : j.rows);
+  }
   const int64_t last = (end - first) * chunks;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < last; i += (int64_t)gridDim.x * 256) {
     const int64_t k = last <= 0xffffffffLL ? (int64_t)((uint32_t)i / chunks) : i / chunks;
@@ -346,8 +368,9 @@ hipError_t launch_act_grad(const ActGradArgs& a, void* ws, hipStream_t st) {
 }
 
 hipError_t launch_gated_grad(const GatedGradArgs& a, hipStream_t st) {
-  const int64_t blocks = ((int64_t)a.rows * (a.half / 8) + 255) / 256;
-  const dim3 grid((unsigned)(blocks < 16384 ? blocks : 16384));
+  int64_t blocks = ((int64_t)a.rows * (a.half / 8) + 255) / 256;
+  for (int i = 0; i < a.n_jobs; ++i) blocks = std::max(blocks, pack_blocks(a.jobs[i]));
+  const dim3 grid((unsigned)(blocks < 16384 ? blocks : 16384), (unsigned)(1 + a.n_jobs));
   if (a.rows <= 0) return hipSuccess;
   if (a.f16) hipLaunchKernelGGL(gated_grad_kernel<true>, grid, dim3(256), 0, st, a);
   else hipLaunchKernelGGL(gated_grad_kernel<false>, grid, dim3(256), 0, st, a);
@@ -401,29 +424,16 @@ Plan matmul_plan(MatmulForm f, int E, int64_t rows, int64_t m, int64_t n, int64_
 
 namespace {
 
-// out[r] = in[r], widened to `pitch` with zeros; a thread moves eight columns.
 // With groups (offsets [E+1], as mm_bounds clamps them) only the rows from the
 // first group's first to the last group's last: the others belong to no
 // product, and are neither read nor worth the time.
-// A grid of two rows does the same for in2 and out2.
-__global__ __launch_bounds__(256) void pack_kernel(const uint16_t* in, const uint16_t* in2, int64_t ld, int64_t rows,
-                                                   int width, uint16_t* out, uint16_t* out2, int pitch,
-                                                   const int32_t* offsets, int E) {
-  const int chunks = pitch / 8;
-  if (blockIdx.y == 1) {
-    in = in2;
-    out = out2;
-  }
-  int64_t first = 0, end = rows;
+// A grid of two rows does the same for a second matrix.
+__global__ __launch_bounds__(256) void pack_kernel(PackJob j, PackJob j2, const int32_t* offsets, int E) {
+  int64_t first = 0, end = j.rows;
   if (offsets != nullptr) {
-    group_rows(offsets, E, rows, first, end);
+    group_rows(offsets, E, j.rows, first, end);
   }
-  for (int64_t i = first * chunks + (int64_t)blockIdx.x * 256 + threadIdx.x; i < end * chunks;
-       i += (int64_t)gridDim.x * 256) {
-    const int64_t r = i / chunks;
-    const int c = (int)(i - r * chunks) * 8;
-    *reinterpret_cast<u32x4_t*>(out + r * pitch + c) = load8(in + r * ld + c, width - c);
-  }
+  pack_rows(blockIdx.y == 1 ? j2 : j, first, end);
 }
 
 // Operands that do not take 16-byte loads are copied with padded rows where
@@ -448,7 +458,7 @@ Packing packing(MatmulForm f, const MatmulArgs& q) {
   if (q.whole || (f != kMmWeightGrad && q.offsets != nullptr)) return k;
   const int mats = q.gated && f != kMmWeightGrad ? 2 : 1;   // of the columns' operand
   const int groups = q.b2_half ? q.E / 2 : q.E;
-  const bool a = !(q.lda % 8 == 0 && (q.a_padded || k.wa % 8 == 0)), b = !(q.ldb % 8 == 0 && k.wb % 8 == 0);
+  const bool a = !(q.lda % 8 == 0 && (q.a_padded || k.wa % 8 == 0)), b = !(q.ldb % 8 == 0 && (q.b_padded || k.wb % 8 == 0));
   if (!a && !b) return k;
   auto pitch = [](int w) { return w >= 512 ? (w + 63) / 64 * 64 : (w + 7) / 8 * 8; };
   k.pa = pitch(k.wa);
@@ -466,13 +476,23 @@ Packing packing(MatmulForm f, const MatmulArgs& q) {
   k.mats = mats;
   return k;
 }
-hipError_t launch_pack(const uint16_t* in, const uint16_t* in2, int64_t ld, int64_t rows, int width, void* out,
-                       void* out2, int pitch, const int32_t* offsets, int E, hipStream_t st) {
-  const int64_t blocks = (rows * (pitch / 8) + 255) / 256;
-  hipLaunchKernelGGL(pack_kernel, dim3((unsigned)(blocks < 16384 ? blocks : 16384), in2 != nullptr ? 2 : 1), dim3(256), 0,
-                     st, in, in2, ld, rows, width, static_cast<uint16_t*>(out), static_cast<uint16_t*>(out2), pitch,
-                     offsets, E);
+hipError_t launch_pack(const PackJob* jobs, int n, const int32_t* offsets, int E, hipStream_t st) {
+  const int64_t blocks = pack_blocks(jobs[0]);
+  hipLaunchKernelGGL(pack_kernel, dim3((unsigned)(blocks < 16384 ? blocks : 16384), (unsigned)n), dim3(256), 0, st,
+                     jobs[0], jobs[n - 1], offsets, E);
   return hipGetLastError();
+}
+// b's copies, in their places from `to` on.
+int b_jobs(const MatmulArgs& a, const Packing& k, char* to, PackJob* jobs) {
+  const uint16_t* in[2] = {a.b, a.b2};
+  for (int i = 0; i < k.mats; ++i)
+    jobs[i] = PackJob{in[i], to != nullptr ? reinterpret_cast<uint16_t*>(to + i * k.bytes_b) : nullptr, a.ldb, k.rb, k.wb, k.pb};
+  return k.mats;
+}
+void use_b_copies(MatmulArgs& a, const PackJob* jobs, int n) {
+  a.b = jobs[0].out;
+  if (n == 2) a.b2 = jobs[1].out;
+  a.ldb = jobs[0].pitch;
 }
 bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -495,28 +515,36 @@ size_t matmul_workspace_bytes(MatmulForm f, const MatmulArgs& a) {
   return k.bytes_a + k.mats * k.bytes_b + up256(x > y ? x : y);
 }
 
+size_t matmul_pack_jobs(MatmulForm f, MatmulArgs& a, void* to, PackJob* jobs, int& n) {
+  const Packing k = packing(f, a);
+  if (!k.b || k.a) return 0;                      // (with k.a, launch_matmul copies both)
+  const int mats = b_jobs(a, k, static_cast<char*>(to), jobs + n);
+  use_b_copies(a, jobs + n, mats);
+  a.b_padded = 1;
+  n += mats;
+  return mats * k.bytes_b;
+}
+
 hipError_t launch_matmul(MatmulForm f, MatmulArgs a, void* ws, hipStream_t st) {
   if (a.m == 0 || (f != kMmWeightGrad && a.rows == 0)) return hipSuccess;
   const Packing k = packing(f, a);
   const bool a16 = al16(a.a) && a.lda % 8 == 0 && (a.a_padded || k.wa % 8 == 0);
-  const bool b16 = al16(a.b) && (a.b2 == nullptr || al16(a.b2)) && a.ldb % 8 == 0 && k.wb % 8 == 0;
+  const bool b16 = al16(a.b) && (a.b2 == nullptr || al16(a.b2)) && a.ldb % 8 == 0 && (a.b_padded || k.wb % 8 == 0);
   a.aligned = (a16 || k.a) && (b16 || k.b);
   char* w = static_cast<char*>(ws);
   const int groups = a.b2_half ? a.E / 2 : a.E;
   if (a.aligned && a.rows > 0) {
     if (k.a) {
-      if (hipError_t e = launch_pack(a.a, nullptr, a.lda, k.ra, k.wa, w, nullptr, k.pa, a.offsets, groups, st)) return e;
-      a.a = reinterpret_cast<const uint16_t*>(w);
+      const PackJob j{a.a, reinterpret_cast<uint16_t*>(w), a.lda, k.ra, k.wa, k.pa};
+      if (hipError_t e = launch_pack(&j, 1, a.offsets, groups, st)) return e;
+      a.a = j.out;
       a.lda = k.pa;
     }
     if (k.b) {
-      char* to = w + k.bytes_a;
-      if (hipError_t e = launch_pack(a.b, k.mats == 2 ? a.b2 : nullptr, a.ldb, k.rb, k.wb, to, to + k.bytes_b, k.pb,
-                                     a.offsets, groups, st))
-        return e;
-      a.b = reinterpret_cast<const uint16_t*>(to);
-      if (k.mats == 2) a.b2 = reinterpret_cast<const uint16_t*>(to + k.bytes_b);
-      a.ldb = k.pb;
+      PackJob jobs[2];
+      const int n = b_jobs(a, k, w + k.bytes_a, jobs);
+      if (hipError_t e = launch_pack(jobs, n, a.offsets, groups, st)) return e;
+      use_b_copies(a, jobs, n);
     }
   }
   a.parts = reinterpret_cast<float*>(w + k.bytes_a + k.mats * k.bytes_b);
