@@ -137,7 +137,10 @@ __device__ __forceinline__ void step1(const Hyper& h, float grad, float& p, floa
   const float g = grad * h.scale;
   m = m * h.b1 + g * h.a1;
   v = v * h.b2 + g * g * h.a2;
-  root = __builtin_amdgcn_sqrtf(v);               // within 1 ulp, as the reciprocal: both far below the step's own rounding
+  // within 1 ulp, as the reciprocal: both far below the step's own rounding
+  // (the instruction takes numbers below 2^-126 for zeros, which shows where eps is 0)
+  const bool low = v < 0x1p-96f;
+  root = __builtin_amdgcn_sqrtf(v * (low ? 0x1p64f : 1.f)) * (low ? 0x1p-32f : 1.f);
   p = p * h.keep - m * __builtin_amdgcn_rcpf(root * h.root + h.eps) * h.size;
 }
 

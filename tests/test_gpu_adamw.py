@@ -98,6 +98,20 @@ def test_mixed_types_in_one_list_and_missing_gradients():
     moe.moe_adamw(moe.AdamWTensors([], [], []), [], step=1, lr=1.0)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_no_eps_and_tiny_gradients(fp8):
+    """Without eps the step is lr for the first gradient of any size whose square has bits: here second moments down to
+    2^-128, 21 bits below which fp32 rounds (ref_step counts relative roundings: 2^-22 more of v, half that of its root)."""
+    n = 2000
+    e = torch.randint(-60, 20, (n,), generator=gen(3), device=DEV)
+    grad = torch.ldexp(1 + torch.rand(n, generator=gen(4), device=DEV), e) * torch.where(e % 2 == 0, 1.0, -1.0)
+    p = torch.ones(n, device=DEV)
+    m, v = ([moe.Fp8Moment.zeros(p)] if fp8 else [torch.zeros_like(p)] for _ in range(2))
+    want, _, _, ep, _, _ = ref_step(p, grad, torch.zeros_like(p), torch.zeros_like(p), 1, 1e-2, 0.9, 1 - 2.0 ** -8, 0.0, 0.0)
+    moe.moe_adamw(moe.AdamWTensors([p], m, v), [grad], step=1, lr=1e-2, beta2=1 - 2.0 ** -8, eps=0.0, weight_decay=0.0)
+    check(p, want, ep + 1e-2 * 2.0 ** -22, "param")
+
+
 # ------------------------------------------------------------- 8-bit states
 
 def draws(n, step):
