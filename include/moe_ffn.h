@@ -363,9 +363,11 @@ int moe_set_stage_events(void* const* events, int n);
 
 /* ===================== around the expert layer ============================
  *
- * Layer norm, linear layers with a fused epilogue and matrix products grouped
- * by expert, each with its gradients: what a block needs beside moe_layer, and
- * what training its experts needs.  The conventions above hold, except:
+ * Layer norm, linear layers with a fused epilogue, matrix products grouped by
+ * expert and gated projections, each with its gradients, the optimiser's step
+ * and products with 4-bit weights: what a block needs beside moe_layer, and
+ * what training and serving its experts needs.  The conventions above hold,
+ * except:
  *  - types are given per call (moe_dtype); pointers need only their element's
  *    alignment (workspaces MOE_WORKSPACE_ALIGN bytes as above).  Rows may be
  *    strided: ld_* is the distance of two rows in elements (0 = packed), at
