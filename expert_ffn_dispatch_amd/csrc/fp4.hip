@@ -288,16 +288,24 @@ int64_t mean_rows(const MatmulArgs& p) {
   return p.offsets != nullptr ? ((int64_t)p.rows + p.E - 1) / p.E : p.rows;
 }
 
-// Groups go by their mean rows (128 experts of 2048 -> 768, 64 rows 12.2 us with
-// 16-row blocks; 4096 rows, gated, 76 us with 32-row blocks, 82 with 64; 6144 rows
-// 52 us with 64-row blocks, 55 with 32; 24576 rows 129 and 139).
+// Groups go by their mean rows, us on 128 experts of 2048 -> 768 unless stated.
+// Up to two: tiles of four rows.  Up to eight: 16-row tiles of 64 columns (8 rows
+// each to 8 experts of 4096 -> 4096 16.9, 20.8 with 32-row tiles).  Up to 28: 32 rows x
+// 256 columns, whose eight waves share x, where that leaves a block for most CUs
+// (16 each 34.6, 44.0 with 16 x 64, 37.0 with 32 x 128; gated, 23 each 63.3 and 68.9 with 32 x
+// 128), else as up to eight, and from 17 to 40 32 x 128 in two parts of the
+// contraction (31 each to 8 experts of 4096 -> 4096 27.7, 31.5 with 48 x 128).
+// More: 48 x 128 (64 each 56.8, 64.8 with 64 x 128; gated 100 and 106), and gated from 97 on
+// 96 x 128 (128 each 154, 163 with 48 x 128).
 // Dense: up to sixteen rows take narrow blocks, with eight waves along the
 // contraction where that leaves fewer blocks than CUs (8 rows, 4096 x 4096 6.3 us
 // with 16 columns, 7.0 with 32; one row, 6144 -> 16384 17 and 12.3).  More rows
-// take the first of ever larger blocks of which the card holds all at once, and
-// else the largest without waves along the contraction (5120 x 5120: 96 rows 14.3
-// us with 32 x 64, 18.3 with 64 x 64; 128 rows 25.8 and 18.7, 256 rows 28.3 with 64 x
-// 128; 512 rows 42.7 with the last).
+// take the first of ever larger blocks, a block's time growing with them, of which
+// every CU gets one at most (5120 x 5120: 96 rows 14.1 us with 32 x 64, 15.9 with 48 x 64;
+// 128 rows 25.6 and 15.9; 256 rows 24.6 with 48 x 128, 28.2 with 64 x 128; 512 rows 35.6 with 96 x
+// 128, 42.1 with 64 x 128 as follows), and else 64 x 128 or 96 x 128 without waves along
+// the contraction, two blocks to a CU, by the rounds over the card at 1 : 1.35 (5120 x
+// 5120, 900 rows 71.6 us by 64, 60.4 by 96).
 template <bool F16, bool GATED>
 hipError_t stream_rows(const Fp4Args& a, hipStream_t st) {
   const MatmulArgs& p = a.mm;
@@ -309,9 +317,13 @@ hipError_t stream_rows(const Fp4Args& a, hipStream_t st) {
   }
   if (p.offsets != nullptr) {
     if (rows <= 2) return stream_go<F16, 1, 2, 2, 2, 2, GATED, false, 4>(a, st);
+    const bool wide = p.E * ((n + 255) / 256) >= 192;
+    if (wide && rows > 8 && rows <= 28) return stream_go<F16, 2, 2, 8, 1, 3, GATED>(a, st);
     if (rows <= 16) return stream_go<F16, 1, 2, 2, 2, 2, GATED>(a, st);
-    if (rows <= 40) return stream_go<F16, 2, 2, 4, 1, 2, GATED>(a, st);
-    return stream_go<F16, 4, 2, 4, 1, 3, GATED>(a, st);
+    if (!wide && rows <= 40) return stream_go<F16, 2, 2, 4, 2, 2, GATED>(a, st);
+    if constexpr (GATED)
+      if (rows > 96) return stream_go<F16, 6, 2, 4, 1, 2, GATED>(a, st);
+    return stream_go<F16, 3, 2, 4, 1, 2, GATED>(a, st);
   }
   if (rows <= 4) {
     if (n >= 6144) return stream_go<F16, 1, 2, 1, 4, 2, GATED, false, 4>(a, st);
@@ -324,9 +336,16 @@ hipError_t stream_rows(const Fp4Args& a, hipStream_t st) {
     else return stream_go<F16, 1, 1, 1, 8, 2, GATED>(a, st);
   }
   auto blocks = [&](int64_t bm, int64_t bn) { return (rows + bm - 1) / bm * ((n + bn - 1) / bn); };
-  if (blocks(32, 64) <= 256) return stream_go<F16, 2, 2, 2, 4, 2, GATED>(a, st);
-  if (blocks(64, 64) <= 256) return stream_go<F16, 4, 2, 2, 4, 2, GATED>(a, st);
-  if (blocks(64, 128) <= 256) return stream_go<F16, 4, 2, 4, 2, 2, GATED>(a, st);
+  auto fits = [&](int64_t bm, int64_t bn) { return blocks(bm, bn) <= 256; };
+  if (fits(32, 64)) return stream_go<F16, 2, 2, 2, 4, 2, GATED>(a, st);
+  if (fits(48, 64)) return stream_go<F16, 3, 2, 2, 4, 2, GATED>(a, st);
+  if (fits(64, 64)) return stream_go<F16, 4, 2, 2, 4, 2, GATED>(a, st);
+  if (fits(32, 128)) return stream_go<F16, 2, 2, 4, 2, 2, GATED>(a, st);
+  if (fits(48, 128)) return stream_go<F16, 3, 2, 4, 2, 2, GATED>(a, st);
+  if (fits(64, 128)) return stream_go<F16, 4, 2, 4, 2, 2, GATED>(a, st);
+  if (fits(96, 128)) return stream_go<F16, 6, 2, 4, 2, 2, GATED>(a, st);
+  if (27 * ((blocks(96, 128) + 511) / 512) < 20 * ((blocks(64, 128) + 511) / 512))
+    return stream_go<F16, 6, 2, 4, 1, 2, GATED>(a, st);
   return stream_go<F16, 4, 2, 4, 1, 3, GATED>(a, st);
 }
 
@@ -349,11 +368,19 @@ hipError_t launch_widen(bool f16, const uint8_t* codes, const uint8_t* exps, uin
   return hipGetLastError();
 }
 
-// Whether the weights are better widened first: a pass of 0.53 + 2 bytes a
-// weight against a product of 16-bit weights that is half as fast again
-// (5120 x 5120: 512 rows 42 us, widened 48, 1024 rows 71 and 70; 4096 -> 16384, 1024
-// rows 148 and 115; 32 experts of 4096 -> 1536, 512 rows each 258 and 297).
-bool widens(const MatmulArgs& p) { return mean_rows(p) > 640; }
+// Whether the weights are better widened first: 2.53 bytes a weight, products
+// at 1.4 PFLOP/s in place of 1.0, and about 12 us of launches and tiles that fill
+// the card less well, which many rows or many weights make up for (us without and
+// with: 5120 x 5120, 1200 rows 74 and 79, 2048 rows 115 and 99; 2048 x 2048, 2048 rows 23 and
+// 28, 4096 rows 42 and 36; 32 experts of 4096 -> 1536, gated, 850 rows each 670 and 692, 1300
+// rows 999 and 935).  Rows of x at an odd pitch pass through registers at half the
+// rate; the products of 16-bit weights copy them (5120 x 5120: 600 rows 103 us, 1400
+// rows widened 85), but not those of groups.
+bool widens(const MatmulArgs& p) {
+  const int64_t weights = (int64_t)p.E * p.n * p.k * (p.gated ? 2 : 1);
+  if (p.lda % 8 == 0) return mean_rows(p) > 900 + 12000000000LL / weights;
+  return mean_rows(p) > (p.offsets != nullptr ? 640 : 300) + 6000000000LL / weights;
+}
 
 size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
 size_t matrix_bytes(const MatmulArgs& p) { return up256((size_t)p.E * p.n * p.k * 2); }

@@ -85,7 +85,8 @@ def test_quantise(dtype):
 # rows, in, out: one token, few rows, odd outputs, partial chunks of the contraction, more rows than a tile
 SHAPES = [(1, 32, 1), (1, 64, 64), (1, 2048, 520), (3, 96, 5), (2, 6144, 48), (16, 160, 40), (17, 512, 256), (31, 1056, 130),
           (33, 256, 6200), (48, 128, 77), (64, 992, 136), (65, 256, 264), (130, 288, 392), (300, 4096, 64), (257, 768, 512),
-          (700, 1024, 1003), (90, 2048, 768), (130, 160, 4096), (257, 96, 4096), (600, 64, 8200)]
+          (700, 1024, 1003), (90, 2048, 768), (130, 160, 4096), (257, 96, 4096), (600, 64, 8200),
+          (7000, 1024, 2050), (4000, 2048, 2048)]
 
 
 @pytest.mark.parametrize("act", ACTS)
@@ -123,7 +124,7 @@ def test_gated_linear(rows, n_in, width, act):
 GROUPS = [([5], 64, 64), ([1], 32, 1), ([0], 64, 24), ([0, 0, 3, 0], 96, 136), ([1] * 7, 128, 256), ([130, 0, 1, 33, 257], 192, 264),
           ([31, 32, 33, 0, 64, 65, 127, 128, 129], 256, 128), ([3, 9, 0, 2], 64, 131), ([700, 0, 2, 600], 512, 320),
           ([2] * 256, 64, 72), ([0] * 100 + [50] + [0] * 59, 128, 128), ([20] * 16, 1024, 768), ([17, 0, 40, 3, 11], 2048, 200),
-          ([60, 90, 0, 10], 288, 96), ([9, 0, 1, 4, 5] + [0] * 9 + [3, 2], 2080, 200), ([1, 0, 3, 0], 4096, 776)]
+          ([60, 90, 0, 10], 288, 96), ([9, 0, 1, 4, 5] + [0] * 9 + [3, 2], 2080, 200), ([1, 0, 3, 0], 4096, 776), ([6000, 0, 4100, 1], 1024, 2056)]
 
 
 @pytest.mark.parametrize("n_in,n_out", [(2080, 6160), (96, 6144), (4096, 200), (32, 24)])

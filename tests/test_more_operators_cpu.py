@@ -164,7 +164,7 @@ def test_fp4_widths_and_pointers(lib):  # noqa: F811
         assert call(d, C, R(fp4(codes=A + 8)), D, *ws) == INV and "16-byte" in _err(lib), name
         assert call(d, C, R(m), None, *ws) == INV and "NULL" in _err(lib), name
         assert call(d, C, R(m), C, *ws) == INV, name
-        few, many = dims(rows=64, in_features=4096), dims(rows=4096, in_features=4096)
+        few, many = dims(rows=64, in_features=4096), dims(rows=1 << 17, in_features=4096)
         assert size(query, few) == 0, "the codes are read as they are"
         mats = 2 if "gated" in name else 1
         assert size(query, many) >= mats * 2 * 64 * 4096, "the weights are widened"
