@@ -301,7 +301,8 @@ int64_t mean_rows(const MatmulArgs& p) {
 // contraction where that leaves fewer blocks than CUs (8 rows, 4096 x 4096 6.3 us
 // with 16 columns, 7.0 with 32; one row, 6144 -> 16384 17 and 12.3).  More rows
 // take the first of ever larger blocks, a block's time growing with them, of which
-// every CU gets one at most (5120 x 5120: 96 rows 14.1 us with 32 x 64, 15.9 with 48 x 64;
+// every CU gets one at most (6784 -> 112, 256 rows 8.2 us with 16 x 16, 14.9 with 32 x 64;
+// 8192 -> 2048, 128 rows 12.7 with 32 x 32, 18.2 with 32 x 64; 5120 x 5120: 96 rows 14.1 us with 32 x 64, 15.9 with 48 x 64;
 // 128 rows 25.6 and 15.9; 256 rows 24.6 with 48 x 128, 28.2 with 64 x 128; 512 rows 35.6 with 96 x
 // 128, 42.1 with 64 x 128 as follows), and else 64 x 128 or 96 x 128 without waves along
 // the contraction, two blocks to a CU, by the rounds over the card at 1 : 1.35 (5120 x
@@ -337,6 +338,10 @@ hipError_t stream_rows(const Fp4Args& a, hipStream_t st) {
   }
   auto blocks = [&](int64_t bm, int64_t bn) { return (rows + bm - 1) / bm * ((n + bn - 1) / bn); };
   auto fits = [&](int64_t bm, int64_t bn) { return blocks(bm, bn) <= 256; };
+  if constexpr (!GATED)
+    if (fits(16, 16)) return stream_go<F16, 1, 1, 1, 8, 2, GATED>(a, st);
+  if (fits(16, 32)) return stream_go<F16, 1, 2, 1, 4, 2, GATED>(a, st);
+  if (fits(32, 32)) return stream_go<F16, 2, 2, 1, 4, 2, GATED>(a, st);
   if (fits(32, 64)) return stream_go<F16, 2, 2, 2, 4, 2, GATED>(a, st);
   if (fits(48, 64)) return stream_go<F16, 3, 2, 2, 4, 2, GATED>(a, st);
   if (fits(64, 64)) return stream_go<F16, 4, 2, 2, 4, 2, GATED>(a, st);

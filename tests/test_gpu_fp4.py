@@ -86,7 +86,7 @@ def test_quantise(dtype):
 SHAPES = [(1, 32, 1), (1, 64, 64), (1, 2048, 520), (3, 96, 5), (2, 6144, 48), (16, 160, 40), (17, 512, 256), (31, 1056, 130),
           (33, 256, 6200), (48, 128, 77), (64, 992, 136), (65, 256, 264), (130, 288, 392), (300, 4096, 64), (257, 768, 512),
           (700, 1024, 1003), (90, 2048, 768), (130, 160, 4096), (257, 96, 4096), (600, 64, 8200),
-          (7000, 1024, 2050), (4000, 2048, 2048)]
+          (7000, 1024, 2050), (4000, 2048, 2048), (257, 2080, 100), (129, 4096, 500), (120, 2048, 1000)]
 
 
 @pytest.mark.parametrize("act", ACTS)
