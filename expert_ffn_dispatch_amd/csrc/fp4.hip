@@ -19,7 +19,7 @@
 // barrier a chunk; with WN = 1 no wave waits for another.
 // Bound by the weights' 17/32 byte for few rows (6144 -> 16384, one row: 12
 // us, 4.4 TB/s with the launch), by the conversions and the matrix pipe for
-// many (16384 rows over 32 experts of 4096 -> 1536: 258 us, 0.8 PFLOP/s).
+// many (16000 rows over 32 experts of 4096 -> 1536: 244 us, 0.8 PFLOP/s).
 #include "matmul.h"
 
 namespace moe {
