@@ -125,11 +125,12 @@ __device__ __forceinline__ float act_grad(float z, int act) {
 
 // act(z) and act'(z) of eight values together: one exponential and one
 // reciprocal each, and one branch for all, so that they overlap (777 x 2222 with
-// gelu (tanh) 11 us with a branch for each value).
+// gelu (tanh) 11 us with a branch for each value).  z is cut as in act_grad; above
+// zero the value is z's own.
 __device__ __forceinline__ void act_both(const float (&z)[8], int act, float (&value)[8], float (&slope)[8]) {
 #define ACT_EACH                                                               \
   _Pragma("unroll") for (int q = 0; q < 8; ++q) {                              \
-    const float w = fabsf(z[q]) > 128.f ? copysignf(128.f, z[q]) : z[q];       /* as above */
+    const float w = fabsf(z[q]) > 128.f ? copysignf(128.f, z[q]) : z[q], y = z[q] < 0.f ? w : z[q];
   switch (act) {
     case kActRelu:
 #pragma unroll
@@ -141,7 +142,7 @@ __device__ __forceinline__ void act_both(const float (&z)[8], int act, float (&v
     case kActGelu:
       ACT_EACH
         const float e = __expf(-0.5f * w * w), n = mm_normal(w, e);
-        value[q] = z[q] * n;
+        value[q] = y * n;
         slope[q] = n + w * 0.39894228040143268f * e;
       }
       break;
@@ -149,7 +150,7 @@ __device__ __forceinline__ void act_both(const float (&z)[8], int act, float (&v
       ACT_EACH
         float s, c;
         logistic(1.5957691216057307f * (w + 0.044715f * w * w * w), s, c);
-        value[q] = z[q] * s;
+        value[q] = y * s;
         slope[q] = s + w * s * c * 1.5957691216057307f * (1.f + 0.134145f * w * w);
       }
       break;
@@ -157,7 +158,7 @@ __device__ __forceinline__ void act_both(const float (&z)[8], int act, float (&v
       ACT_EACH
         float s, c;
         logistic(w, s, c);
-        value[q] = z[q] * s;
+        value[q] = y * s;
         slope[q] = s + w * s * c;
       }
       break;
@@ -169,6 +170,13 @@ __device__ __forceinline__ void act_both(const float (&z)[8], int act, float (&v
       }
   }
 #undef ACT_EACH
+}
+
+// A saved product times f.  An infinite one stands for a finite sum past its
+// type's range (fp16: 65504): times 0 it is 0, where the formula in numbers that
+// hold the sum has 0.
+__device__ __forceinline__ float saved_times(float v, float f) {
+  return f == 0.f && fabsf(v) == __builtin_inff() ? f : v * f;
 }
 
 // The rows of the groups (offsets as mm_bounds clamps them): where they
@@ -322,8 +330,8 @@ __global__ __launch_bounds__(256) void gated_grad_kernel(GatedGradArgs p) {
     act_both(z, p.act, value, slope);
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
-      u[q] *= d[q] * slope[q];
-      z[q] = d[q] * value[q];
+      u[q] = saved_times(u[q], d[q] * slope[q]);
+      z[q] = saved_times(value[q], d[q]);
     }
     uint16_t* o = p.g + r * 2 * p.half + c;
     *reinterpret_cast<u32x4_t*>(o) = u32x4_t{mm_pack2<F16>(u[0], u[1]), mm_pack2<F16>(u[2], u[3]),

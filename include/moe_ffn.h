@@ -531,7 +531,8 @@ int moe_grouped_gated(const moe_gated_dims* dims, const void* x, const int32_t* 
  * Their gradients, from dh and the saved products:
  *   dgate = dh * up * act'(gate),  dup = dh * act(gate)
  * (rounded to dtype as operands of the products, so infinite past fp16's range
- * with fp16 data; relu's slope at 0 is 0),
+ * with fp16 data; relu's slope at 0 is 0; an infinite gate or up, a product past
+ * its type's range, gives 0 where what it is multiplied by is 0),
  *   dx = dgate w_gate + dup w_up,  dw_gate = dgate^T x,  dw_up = dup^T x.
  * dx [rows][in], dw_gate / dw_up [width][in] packed (grouped: [E][width][in],
  * zero for an expert without rows): outputs; dx or both of dw_gate and dw_up

@@ -2,6 +2,8 @@
 formulas in 64 bits.  Tolerances count roundings as in test_gpu_operators.py;
 the operands of the gradients' products are rounded to the data's type first,
 which adds u sum|a b| for each."""
+import math
+
 import pytest
 import torch
 
@@ -140,6 +142,46 @@ def test_activation_at_large_values(act, dtype):
     # dup = dh act(gate)
     dx = moe.moe_gated_linear_backward(one, one, 0 * eye, eye, z, one, act=act)[0]
     assert torch.equal(dx, z.clamp(min=0))
+
+
+# gate, up, dh
+PAST = [(-math.inf, 1, 1), (-math.inf, 2, 0), (-math.inf, -math.inf, 1), (-300, math.inf, 1), (-300, -math.inf, 2), (math.inf, 3, 1),
+        (math.inf, 2, 0), (-2, math.inf, 0), (math.inf, math.inf, 1), (0.5, math.inf, 1), (0.5, math.nan, 0), (-300, 1, math.nan),
+        (-300, math.nan, 1), (math.nan, 1, 1), (1, -2, 0), (-300, 3, 1)]
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("act", ACTS)
+def test_saved_products_past_the_type(act, dtype):
+    """A saved product that is infinite stands for a finite sum past the type's range (fp16: 65504): its gradient is the limit,
+    0 where the other factor is 0, infinite elsewhere, and no number only where an operand is none.  One row of ones as x:
+    the weights' gradients are dgate and dup."""
+    z, up, d = (torch.tensor([c[i] for c in PAST], device=DEV).to(dtype)[None] for i in range(3))
+    x, w = torch.ones(1, 8, dtype=dtype, device=DEV), torch.zeros(len(PAST), 8, dtype=dtype, device=DEV)
+    _, dg, du = moe.moe_gated_linear_backward(d, x, w, w, z, up, act=act, want_dx=False)
+    for i, (zi, ui, di) in enumerate(PAST):
+        far = zi if act == "none" else max(zi, 0.0) if zi == zi else zi          # act(gate), past |gate| = 128
+        slope = 1.0 if act == "none" else float(zi > 0) if zi == zi or act == "relu" else zi
+        if abs(zi) < 128:
+            far, slope = act_ref(z[0, i].double(), act).item(), act_grad_ref(z[0, i].double(), act).item()
+        for got, saved, factor in ((dg, ui, di * slope), (du, far, di)):
+            want = 0.0 if factor == 0 and abs(saved) == math.inf else saved * factor
+            have = got[i, 0].item()
+            assert (have != have) == (want != want) and (want != want or have == want or (
+                math.isfinite(want) and abs(have - want) <= 2 * u(dtype) * abs(want) + 2 * FUN)), (PAST[i], have, want)
+
+
+@pytest.mark.parametrize("act", ACTS[1:])
+def test_gates_below_the_types_range(act):
+    """A gate sum of -80000 in fp16: h is 0, the saved gate -inf, and the step has no gradient through it."""
+    x = torch.tensor([[40000.0, 1.0], [1.0, 1.0]], device=DEV).to(HF)
+    wg, wu = torch.tensor([[-2.0, 0.0], [0.0, 1.0]], device=DEV).to(HF), torch.tensor([[0.0, 1.0], [0.0, 2.0]], device=DEV).to(HF)
+    h, gate, up = moe.moe_gated_linear(x, wg, wu, act=act, want_pre=True)
+    assert h[0, 0] == 0 and gate[0, 0] == -math.inf
+    dh = torch.tensor([[1.0, 0.0], [0.0, 1.0]], device=DEV).to(HF)
+    dx, dwg, dwu = moe.moe_gated_linear_backward(dh, x, wg, wu, gate, up, act=act)
+    assert not dx[0].any() and not dwg[0].any() and not dwu[0].any()
+    assert torch.isfinite(dx).all() and torch.isfinite(dwg).all() and torch.isfinite(dwu).all()
 
 
 @pytest.mark.parametrize("n_in,width,pad,shift", [(128, 192, 8, 0), (128, 192, 3, 0), (136, 72, 16, 8), (96, 64, 8, 1),
