@@ -751,6 +751,7 @@ class Fp8Moment(NamedTuple):
 
 
 _TABLE_WORDS = ctypes.sizeof(_lib.MoeAdamWTensor) // 8
+_data_ptr = torch.Tensor.data_ptr
 
 
 class AdamWTensors:
@@ -758,8 +759,8 @@ class AdamWTensors:
     or fp32), their first and second moments (fp32 tensors of the same sizes, or
     Fp8Moment, all of one kind) and, where given, copies (bf16 or fp16, None for
     a parameter without one) that receive the new parameters.  Contiguous, on
-    one device, without overlaps; the object keeps the memory of all.  One call
-    at a time uses it."""
+    one device, without overlaps; the object keeps the memory of all, and is
+    refused once any of them lies elsewhere.  One call at a time uses it."""
 
     def __init__(self, params, exp_avg, exp_avg_sq, copies=None):
         params, exp_avg, exp_avg_sq = list(params), list(exp_avg), list(exp_avg_sq)
@@ -773,6 +774,7 @@ class AdamWTensors:
         self._table = (_lib.MoeAdamWTensor * max(1, self.count))()
         self._words = memoryview(self._table).cast("B").cast("Q")
         self._kept = []                         # every tensor's memory, whatever becomes of the caller's object
+        self._tensors, self._at = [], []        # every tensor, and where it was
         device, spans = self.device, []
 
         def place(i, entry, field, t, n, dtypes):
@@ -785,6 +787,8 @@ class AdamWTensors:
             at = t.data_ptr()
             setattr(entry, field, at)
             self._kept.append(t.untyped_storage())
+            self._tensors.append(t)
+            self._at.append(at)
             if n:
                 spans.append((at, at + n * t.element_size(), field, i))
 
@@ -809,16 +813,14 @@ class AdamWTensors:
         for a, b in zip(spans, spans[1:]):
             if b[0] < a[1]:
                 raise ValueError(f"{a[2]} {a[3]} and {b[2]} {b[3]} overlap")
-        self._params = params
-        self._at = [p.data_ptr() for p in params]
         self._devices = [p.get_device() for p in params]
         self._grad_types = None
 
     def _entries(self, grads):
         """The table with this step's gradients.  (List by list: 37 tensors one by
         one took 22 us, of a step of 9.)"""
-        if [p.data_ptr() for p in self._params] != self._at:      # param.data = ...
-            raise ValueError("a parameter's memory has moved since the list was made")
+        if list(map(_data_ptr, self._tensors)) != self._at:       # t.data = ..., or a storage of another size
+            raise ValueError("the memory of a parameter, state or copy has moved since the list was made")
         if len(grads) != self.count:
             raise ValueError(f"grads: {len(grads)} for {self.count} parameters")
         if any(g is None for g in grads):

@@ -378,3 +378,31 @@ def test_refusals():
     p.data = f()
     with pytest.raises(ValueError, match="moved"):
         moe.moe_adamw(plan, [f()], 1, 0.1)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("what", ["p", "m", "v", "c"])
+@pytest.mark.parametrize("how", ["data", "freed"])
+def test_memory_that_is_no_longer_the_lists(how, what, fp8):
+    """A parameter, state or copy that was given other memory, or whose memory was freed: refused before anything is written."""
+    for part in range(2 if fp8 and what in "mv" else 1):     # codes, exponents
+        ts, plan = _two(gen(3), fp8)
+        x = ts[1][what + "8"][part] if fp8 and what in "mv" else ts[1][what]
+        before, size = [y.clone() for y in _state(ts, fp8)], x.untyped_storage().nbytes()
+        old, saved = x.data, x.clone()
+        if how == "data":
+            x.data = saved
+        else:
+            x.untyped_storage().resize_(0)
+        with pytest.raises(ValueError, match="moved"):
+            moe.moe_adamw(plan, [t["g"] for t in ts], step=1, lr=0.1)
+        if how == "data":
+            x.data = old
+        else:
+            x.untyped_storage().resize_(size)
+            x.copy_(saved)
+        for a, b in zip(_state(ts, fp8), before):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+        if how == "data":                           # its own memory again
+            moe.moe_adamw(plan, [t["g"] for t in ts], step=1, lr=0.1)
+            assert not torch.equal(ts[1]["p"], before[2])
