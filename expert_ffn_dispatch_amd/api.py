@@ -754,13 +754,22 @@ _TABLE_WORDS = ctypes.sizeof(_lib.MoeAdamWTensor) // 8
 _data_ptr = torch.Tensor.data_ptr
 
 
+def _same_order(a, b):
+    """Whether contiguous values of the two shapes lie in the same order: one shape (but for ones), or one of them flat."""
+    if a == b:
+        return True
+    p, q = ([n for n in s if n != 1] for s in (a, b))
+    return a.numel() == b.numel() and (p == q or len(p) <= 1 or len(q) <= 1)
+
+
 class AdamWTensors:
     """The tensors that moe_adamw updates, looked over once: params (bf16, fp16
-    or fp32), their first and second moments (fp32 tensors of the same sizes, or
-    Fp8Moment, all of one kind) and, where given, copies (bf16 or fp16, None for
-    a parameter without one) that receive the new parameters.  Contiguous, on
-    one device, without overlaps; the object keeps the memory of all, and is
-    refused once any of them lies elsewhere.  One call at a time uses it."""
+    or fp32), their first and second moments (fp32 tensors, or Fp8Moment, all of
+    one kind) and, where given, copies (bf16 or fp16, None for a parameter
+    without one) that receive the new parameters.  All of the parameter's shape,
+    or one of the two flat; contiguous, on one device, without overlaps.  The
+    object keeps the memory of all, and is refused once any of them lies
+    elsewhere.  One call at a time uses it."""
 
     def __init__(self, params, exp_avg, exp_avg_sq, copies=None):
         params, exp_avg, exp_avg_sq = list(params), list(exp_avg), list(exp_avg_sq)
@@ -769,7 +778,7 @@ class AdamWTensors:
             raise ValueError("params, exp_avg, exp_avg_sq and copies: different lengths")
         self.fp8 = bool(params) and isinstance(exp_avg[0], Fp8Moment)
         self.device = params[0].device if params else None
-        self.numels = [p.numel() for p in params]
+        self._shapes = [p.shape for p in params]
         self.count = len(params)
         self._table = (_lib.MoeAdamWTensor * max(1, self.count))()
         self._words = memoryview(self._table).cast("B").cast("Q")
@@ -784,6 +793,8 @@ class AdamWTensors:
                 raise TypeError(f"{field} {i}: dtype {t.dtype} not in {tuple(dtypes)}")
             if t.numel() != n or not t.is_contiguous():
                 raise ValueError(f"{field} {i}: expected {n} contiguous values, got shape {tuple(t.shape)}")
+            if not field.endswith("_exp") and not _same_order(t.shape, self._shapes[i]):
+                raise ValueError(f"{field} {i}: shape {tuple(t.shape)} beside a parameter of {tuple(self._shapes[i])}")
             at = t.data_ptr()
             setattr(entry, field, at)
             self._kept.append(t.untyped_storage())
@@ -794,7 +805,7 @@ class AdamWTensors:
 
         fp8, codes = self.fp8, (torch.float8_e4m3fn,)
         for i, (p, m, v, c) in enumerate(zip(params, exp_avg, exp_avg_sq, copies)):
-            n, e = self.numels[i], self._table[i]
+            n, e = p.numel(), self._table[i]
             place(i, e, "param", p, n, _DTYPES)
             for t, field in ((m, "exp_avg"), (v, "exp_avg_sq")):
                 if isinstance(t, Fp8Moment) != fp8:
@@ -814,7 +825,7 @@ class AdamWTensors:
             if b[0] < a[1]:
                 raise ValueError(f"{a[2]} {a[3]} and {b[2]} {b[3]} overlap")
         self._devices = [p.get_device() for p in params]
-        self._grad_types = None
+        self._grad_types = self._grad_shapes = None
 
     def _entries(self, grads):
         """The table with this step's gradients.  (List by list: 37 tensors one by
@@ -825,9 +836,11 @@ class AdamWTensors:
             raise ValueError(f"grads: {len(grads)} for {self.count} parameters")
         if any(g is None for g in grads):
             return self._some(grads)
-        if ([g.numel() for g in grads] != self.numels or [g.get_device() for g in grads] != self._devices
+        shapes = [g.shape for g in grads]
+        if (shapes != self._grad_shapes or [g.get_device() for g in grads] != self._devices
                 or not all([g.is_contiguous() for g in grads])):
             self._refuse(grads)
+            self._grad_shapes = shapes
         types = [g.dtype for g in grads]
         if types != self._grad_types:
             self._types(types)
@@ -843,9 +856,9 @@ class AdamWTensors:
         self._grad_types = types
 
     def _refuse(self, grads):
-        for i, (g, n, d) in enumerate(zip(grads, self.numels, self._devices)):
-            if g is not None and (g.numel() != n or g.get_device() != d or not g.is_contiguous()):
-                raise ValueError(f"grad {i}: expected {n} contiguous values on {self.device}, got shape "
+        for i, (g, s, d) in enumerate(zip(grads, self._shapes, self._devices)):
+            if g is not None and (not _same_order(g.shape, s) or g.get_device() != d or not g.is_contiguous()):
+                raise ValueError(f"grad {i}: expected contiguous values of shape {tuple(s)} on {self.device}, got shape "
                                  f"{tuple(g.shape)} on {g.device}")
 
     def _some(self, grads):
@@ -875,9 +888,9 @@ def _scalar(t, name, dtype, device):
 def moe_adamw(tensors: AdamWTensors, grads, step, lr, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
               weight_decay: float = 0.01, grad_scale=None, stream=None):
     """One AdamW step in place over all tensors; grads: one for each (bf16, fp16
-    or fp32; None leaves its parameter as it is).  step (from 1) and lr: numbers,
-    or one-element device tensors (int32, fp32), which a captured call reads at
-    every replay.  grad_scale: a one-element fp32 device tensor that the
+    or fp32, of its shape or flat; None leaves its parameter as it is).  step
+    (from 1) and lr: numbers, or one-element device tensors (int32, fp32), which
+    a captured call reads at every replay.  grad_scale: a one-element fp32 device tensor that the
     gradients are multiplied by, or None."""
     dev = tensors.device
     if dev is None:

@@ -406,3 +406,25 @@ def test_memory_that_is_no_longer_the_lists(how, what, fp8):
         if how == "data":                           # its own memory again
             moe.moe_adamw(plan, [t["g"] for t in ts], step=1, lr=0.1)
             assert not torch.equal(ts[1]["p"], before[2])
+
+
+def test_shapes():
+    """States, copies and gradients have their parameter's shape, or are flat (or the parameter is): never another order."""
+    f = lambda *s, dt=F32: torch.randn(s, generator=gen(sum(s)), device=DEV).to(dt)  # noqa: E731
+    new = moe.AdamWTensors
+    for kw in (dict(m=f(24, 16)), dict(v=f(24, 16)), dict(c=f(24, 16, dt=BF)), dict(m=f(2, 8, 24))):
+        a = {**dict(p=f(16, 24), m=f(16, 24), v=f(16, 24), c=f(16, 24, dt=BF)), **kw}
+        with pytest.raises(ValueError, match="shape"):
+            new([a["p"]], [a["m"]], [a["v"]], copies=[a["c"]])
+    p, m, v, p2 = f(16, 24), torch.zeros(16, 24, device=DEV), torch.zeros(16 * 24, device=DEV), f(16 * 24)
+    plan = new([p, p2], [m, torch.zeros_like(p2)], [v, torch.zeros_like(p2)])
+    for bad in ([f(24, 16), f(16 * 24)], [f(4, 4, 24), f(16 * 24)], [f(24, 16), None]):
+        with pytest.raises(ValueError, match="shape"):
+            moe.moe_adamw(plan, bad, 1, 0.1)
+    assert not m.any() and not v.any()
+    for grads in ([f(16, 24), f(16 * 24)], [f(16 * 24), f(16, 24)], [f(16, 1, 24), f(1, 16 * 24)], [f(16, 24), None]):
+        want = ref_step(p, grads[0].view(16, 24), m, v.view(16, 24), 1, **HYPER)
+        moe.moe_adamw(plan, grads, 1, **HYPER)
+        check_param(p, want[0], want[3], "param")
+    with pytest.raises(ValueError, match="shape"):  # also after others were taken
+        moe.moe_adamw(plan, [f(24, 16), f(16 * 24)], 1, 0.1)
