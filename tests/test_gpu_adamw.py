@@ -428,3 +428,22 @@ def test_shapes():
         check_param(p, want[0], want[3], "param")
     with pytest.raises(ValueError, match="shape"):  # also after others were taken
         moe.moe_adamw(plan, [f(24, 16), f(16 * 24)], 1, 0.1)
+
+
+@pytest.mark.parametrize("eps", [1e-8, 1e-3])
+def test_8_bit_extremes_step_by_step(eps):
+    """Gradients from the smallest to the largest: each step against the formula, from the states that the codes hold.  Numbers
+    below 2^-126 round by 2^-150 at most: in m's terms and sum and m's product (four), over eps at least, and p's own; v's
+    three are 2^-74 of its root, over eps."""
+    g = torch.logspace(-44, 18, 128 * 4, device=DEV)
+    p = torch.zeros_like(g)
+    m, v = moe.Fp8Moment.zeros(p), moe.Fp8Moment.zeros(p)
+    plan = moe.AdamWTensors([p], [m], [v])
+    for t in (1, 2, 3):
+        r = v.values().double()
+        want, m1, _, ep, _, _ = ref_step(p, g, m.values(), r * r, t, 1e-3, 0.9, 0.999, eps, 0.0)
+        moe.moe_adamw(plan, [g], step=t, lr=1e-3, eps=eps, weight_decay=0.0)
+        size = 1e-3 / (1 - 0.9 ** t) / eps
+        low = size * 4 * 2.0 ** -150 + size * m1.abs() * 2.0 * 2.0 ** -74 / math.sqrt(1 - 0.999 ** t) / eps + 4 * 2.0 ** -150
+        check_param(p, want, ep + low, f"step {t}")
+        assert (p <= 0).all()
