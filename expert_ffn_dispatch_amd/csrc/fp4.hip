@@ -73,7 +73,10 @@ __device__ __forceinline__ u32x4_t turn(u32x4_t v) {
 // BM: rows of a tile, 16 RB or, for few, four: the matrix instruction's other
 // twelve repeat them and are dropped, and x is a quarter of the loads and LDS
 // reads (128 experts of 2048 -> 768, 64 rows, gated 22.9 -> 18.9 us).
-// (Registers stay below 256, without copies to the other half of the file.)
+// (Registers stay below 256.  Above, an instance of 4 x 8 blocks in a wave had the
+// address of the groups' offsets parked in the other half of the file inside a
+// block for some lanes, and the others read their next tile through what was there
+// before.  tests/test_compiled_kernels_cpu.py holds every instance to that.)
 template <bool F16, int RB, int NC, int WN, int WK, int NB, bool GATED, bool XREG, int BM>
 __global__ __launch_bounds__(64 * WN * WK, 2) void fp4_stream_kernel(Fp4Args a) {
   constexpr int NW = WN * WK;
@@ -154,7 +157,8 @@ __global__ __launch_bounds__(64 * WN * WK, 2) void fp4_stream_kernel(Fp4Args a) 
     };
     uint32_t er4[NC];
     u32x4_t ex[NC];
-    // exponents of four chunks from c on, the fg-th in the lanes of fg
+    // exponents of four chunks from c on, the fg-th in the lanes of fg (four bytes
+    // at any address: buffer loads need no alignment)
     auto load_e = [&](int c) __attribute__((always_inline)) {
       const int at = (wk + WK * (c + fg)) * 4;
       if ((epitch & 3) == 0) {

@@ -178,8 +178,8 @@ hipError_t stream_dense(const MatmulArgs& a, hipStream_t st) {
   return stream_go<F16, RB, 4, 4, true>(a, st);
 }
 // Gated: sixteen pairs of columns for up to sixteen rows (6144 -> 16384, one row
-// 74.6 us, 82.1 with 32), else 32 where they leave about 192 blocks (32 rows 84.8 with
-// sixteen, 78.9 so).
+// 66.3 us, 76.6 with 32; eight rows 68.2 and 79.0), else 32 where they leave about
+// 192 blocks (32 rows 88.5 with sixteen, 87.8 so).
 template <bool F16, int RB>
 hipError_t stream_gated(const MatmulArgs& a, hipStream_t st) {
   if (RB == 1 || a.n < 192 * 32) return stream_go<F16, RB, 2, 4, true, true>(a, st);

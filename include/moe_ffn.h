@@ -559,7 +559,8 @@ int moe_grouped_gated_backward(const moe_gated_dims* dims, const void* dh, const
  * 0 (else MOE_ERR_UNSUPPORTED): codes [..][out][in / 2] bytes, weight 2 i in the
  * low half of byte i, and exponents [..][out][in / 32], both packed.
  * Exponents 1..254; with fp16 data 104..140, at which every code is an fp16
- * number (others are rounded to fp16).  Device pointers, codes 16-byte aligned.
+ * number (others are rounded to fp16).  Device pointers, codes 16-byte aligned,
+ * exponents at any address.
  */
 typedef struct moe_fp4_matrix {
   const uint8_t* codes;
@@ -648,9 +649,15 @@ typedef struct moe_adamw_tensor {
  * if its part of the step, as the 16 bits below the code's last, plus u reaches
  * 65536, where u is the low (m) or high (r) half of a hash of the value's
  * index in its tensor and the step: right on average, since nearest rounding
- * would hold an average still that moves by less than half a step.  r > 0
- * keeps a code of at least 1.  A block with a value that is not finite becomes
+ * would hold an average still that moves by less than half a step.  (m and r
+ * are; v = r^2 of the next step is larger by the rounding's variance: 2.5, 4.0 and
+ * 4.0 % on average at beta2 = 0.95, 0.99 and 0.999 with normal gradients, a single
+ * r 11 to 15 % rms from that of 32-bit states.)  r > 0 keeps a code of at least 1.  A block with a value that is not finite becomes
  * NaN (exponent 255).  The update itself takes the unrounded m and v.
+ *
+ * No step is left out: a gradient that is not finite (an overflow under a loss
+ * scale) goes into states and parameters, so a caller who expects one looks for
+ * it before the call.
  *
  * tensors: host array, read before the call returns.  With lr_device and
  * step_device a captured call replays with their values of that time.
